@@ -1,4 +1,5 @@
-"""MI355X (gfx950) Kimi Delta Attention: chunked prefill, append-prefill and decode.
+"""MI355X (gfx950) Kimi Delta Attention: chunked prefill, append-prefill and decode, and what serving
+needs next to them (paged key-value cache, branching, beam search; ``serving.py``).
 
 Thin Python binding over the C ABI in ``include/kda.h`` (library ``_kda.so``).  This
 module only checks and marshals torch tensors (device memory) and the current HIP stream;
@@ -18,7 +19,8 @@ from . import _lib
 from ._lib import KdaError  # noqa: F401
 
 __all__ = ["prefill_chunked", "append_prefill", "decode_step", "chunked_backward", "workspace_size", "is_supported",
-           "version", "KdaError", "kernel_timing"]
+           "version", "KdaError", "kernel_timing", "cache_append", "paged_decode", "cache_fork", "cache_free",
+           "cache_reserve", "cache_compact", "pages_copy", "beam_select", "beam_reorder"]
 
 _DT = {torch.float32: _lib.KDA_F32, torch.bfloat16: _lib.KDA_BF16}
 
@@ -328,3 +330,7 @@ def decode_step(q, k, v, g, beta, state, *, out=None, state_out=None, prologue_g
                                     _options(gate, gate_scale=prologue_gate_scale),
                                     _stream(dev)))
     return out
+
+
+from .serving import (beam_reorder, beam_select, cache_append, cache_compact, cache_fork, cache_free,  # noqa: E402
+                      cache_reserve, paged_decode, pages_copy)

@@ -24,9 +24,16 @@ KDA_NOALLOC_SCRATCH_BYTES = 128 << 20  # the fixed device scratch of kda_append_
 EXPORTS = ("kda_prefill_chunked", "kda_append_prefill", "kda_decode_step", "kda_prefill_chunked_ex",
            "kda_append_prefill_ex", "kda_decode_step_ex", "kda_append_prefill_noalloc", "kda_chunked_backward", "kda_workspace_size",
            "kda_is_supported", "kda_validate_cu_seqlens", "kda_validate_snapshot_cu", "kda_validate_gates",
-           "kda_status_string", "kda_last_error", "kda_version", "kda_timing_begin", "kda_timing_end")
+           "kda_status_string", "kda_last_error", "kda_version", "kda_timing_begin", "kda_timing_end",
+           "kda_cache_append", "kda_paged_decode", "kda_paged_decode_workspace", "kda_cache_fork", "kda_cache_free",
+           "kda_cache_reserve", "kda_cache_compact", "kda_cache_workspace_size", "kda_pages_copy", "kda_beam_select",
+           "kda_beam_select_workspace", "kda_beam_reorder", "kda_validate_page_table")
 KERNEL_NAMES = {1: "kda_prep", 2: "kda_state", 3: "kda_chunk_f32", 4: "kda_decode", 5: "kda_bwd_factors",
-                6: "kda_bwd_fwd_chain", 7: "kda_bwd_rev_chain", 8: "kda_bwd_grad_state", 9: "kda_bwd_grad_chunk"}
+                6: "kda_bwd_fwd_chain", 7: "kda_bwd_rev_chain", 8: "kda_bwd_grad_state", 9: "kda_bwd_grad_chunk",
+                10: "kda_cache_append", 11: "kda_paged_decode", 12: "kda_paged_join", 13: "kda_cache_fork",
+                14: "kda_cache_free", 15: "kda_cache_scan", 16: "kda_cache_reserve", 17: "kda_cache_plan",
+                18: "kda_cache_remap", 19: "kda_pages_copy", 20: "kda_beam_scan", 21: "kda_beam_join",
+                22: "kda_beam_reorder"}
 
 _LIB = None
 
@@ -90,6 +97,29 @@ def load():
     L.kda_validate_snapshot_cu.argtypes = [vp, vp, i32, i32, i32]
     L.kda_validate_gates.restype = ctypes.c_int
     L.kda_validate_gates.argtypes = [vp, i64, vp, i64, i32]
+    f32 = ctypes.c_float
+    for name, args in {
+        "kda_cache_append": [vp, vp, i64, i64, vp, vp, i32, i64, vp, vp, i64, i64, i32, i32, vp, i64, i32, i32, i32,
+                             i32, vp],
+        "kda_paged_decode": [vp, i64, vp, vp, i64, i64, i32, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, f32, i32,
+                             i32, i64, vp, vp, vp, sz, vp],
+        "kda_cache_fork": [vp, i64, vp, i32, i32, vp, i32, vp, i32, vp, i64, vp, vp],
+        "kda_cache_free": [vp, i64, vp, i32, i32, vp, i32, vp, i32, vp],
+        "kda_cache_reserve": [vp, i64, vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, sz, vp],
+        "kda_cache_compact": [vp, i64, i32, i32, vp, i32, vp, i64, vp, vp, vp, sz, vp],
+        "kda_pages_copy": [vp, vp, vp, i32, i32, vp, i64, vp],
+        "kda_beam_select": [vp, i64, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp],
+        "kda_beam_reorder": [vp, vp, i32, vp, i32, i32, vp],
+        "kda_validate_page_table": [vp, i64, vp, i32, i32, i32, i32, i64],
+    }.items():
+        getattr(L, name).restype = ctypes.c_int
+        getattr(L, name).argtypes = args
+    L.kda_paged_decode_workspace.restype = sz
+    L.kda_paged_decode_workspace.argtypes = [i32, i32, i32, i32, i32, i64, i32, i32]
+    L.kda_cache_workspace_size.restype = sz
+    L.kda_cache_workspace_size.argtypes = [i32, i32]
+    L.kda_beam_select_workspace.restype = sz
+    L.kda_beam_select_workspace.argtypes = [i32, i32, i32, i32]
     _LIB = L
     return L
 

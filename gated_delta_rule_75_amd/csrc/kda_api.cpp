@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "kda_api_util.h"
 #include "kda_internal.h"
 
 // ---------------------------------------------------------------------------------------
@@ -60,10 +61,12 @@ void timed_end(hipStream_t s) {
 }  // namespace kda
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
 
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace kda {
+namespace api {
+
 int fail(int status, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -84,20 +87,6 @@ bool env_flag(const char* name) {
     return v && v[0] && std::strcmp(v, "0") != 0;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Span {
-    const void* p;
-    size_t bytes;
-};
-
-bool overlap(Span a, Span b) {
-    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
 int check_hip(hipError_t e, hipStream_t s, const char* what) {
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
     if (env_flag("KDA_DEBUG_SYNC")) {
@@ -107,26 +96,18 @@ int check_hip(hipError_t e, hipStream_t s, const char* what) {
     return ok();
 }
 
-// Host-side stand-in for a launch failure, for tests of the error path only.
-bool injected_launch_failure() { return env_flag("KDA_TEST_FAIL_LAUNCH"); }
+}  // namespace api
+}  // namespace kda
+
+namespace {
+
+using namespace kda::api;
 
 // ---------------------------------------------------------------------------------------
 // Debug checks of device-resident data (KDA_DEBUG_CHECK=1): the offsets and gates are
 // copied to the host, after the caller's stream has drained, and validated before any
 // launch.  Off by default: the calls then never synchronise.
 // ---------------------------------------------------------------------------------------
-bool debug_check() { return env_flag("KDA_DEBUG_CHECK"); }
-
-template <typename T>
-int fetch(const void* dev, size_t count, hipStream_t s, std::vector<T>& out, const char* name) {
-    out.resize(count);
-    if (!count) return KDA_OK;
-    hipError_t e = hipStreamSynchronize(s);
-    if (e == hipSuccess) e = hipMemcpy(out.data(), dev, count * sizeof(T), hipMemcpyDeviceToHost);
-    if (e != hipSuccess) return fail(KDA_ERR_HIP, "%s (debug check): %s", name, hipGetErrorString(e));
-    return KDA_OK;
-}
-
 float bf16_bits_to_float(uint16_t b) {
     const uint32_t u = static_cast<uint32_t>(b) << 16;
     float f;
@@ -161,8 +142,6 @@ int debug_check_gates(const float* g, size_t ng, const void* beta, size_t nb, in
     }
     return kda_validate_gates(hg.data(), (int64_t)ng, hb.data(), (int64_t)nb, prologue ? 1 : 0);
 }
-
-bool valid_dtype(int32_t d) { return d == KDA_F32 || d == KDA_BF16; }
 
 // Which chunked implementation serves (dtype, dk, dv, chunk): 2 = matrix cores, 1 = fp32, 0 = none.
 int prefill_path(int32_t dtype, int32_t dk, int32_t dv, int32_t chunk) {

@@ -1,0 +1,461 @@
+// Beam search next to the recurrence: the choice of the continuations and the reordering of the
+// fixed-size states (include/kda.h, kda_beam_select and kda_beam_reorder).
+//
+// Choice.  With x the logits of a beam, c[k, v] = score_k + x_v - log sum_u exp(x_u).  Within a beam
+// the order of c is that of x, so every beam needs only its n_out best logits, and one pass over the
+// logits gives them together with the running maximum and sum of the log-sum: the bytes of the
+// logits bound it.  A row is split over workgroups; a second launch joins the parts of a group's rows
+// and orders the remaining candidates by c in fp64.
+//
+// The best logits are found with a threshold: the maxima of n_out disjoint groups of threads are
+// n_out different logits, so the least of them is no larger than the n_out-th best, and whatever
+// lies below it is out.  What is left (about n_out log n_out logits for unordered ones) is collected
+// and ranked by a key of value and token, so ties go to the lower token whatever the order of
+// collection.  Where more are left than the list holds (a row of equal logits, say), the choice is
+// made by repeated maxima over the keys instead.
+#include <math.h>
+
+#include "kda_device.h"
+#include "kda_internal.h"
+
+namespace kda {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxOut = 64;     // n_out and K at most
+constexpr int kThreads = 256;
+constexpr int kPer = 16;        // logits of a thread per round
+constexpr int kRound = kThreads * kPer;
+constexpr int kList = 1024;     // collected keys of a part of a row
+
+// Keys order like (value descending, token ascending) when compared as larger first.  No key of a
+// token is 0.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ uint64_t key_of(float x, int token) {
+    return ((uint64_t)ordered(x) << 32) | (0xFFFFFFFFu - (uint32_t)token);
+}
+// NaN counts as -inf; -0 is +0
+__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : x + 0.f; }
+
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int off) {
+    const uint32_t lo = __shfl_xor((uint32_t)x, off, 64), hi = __shfl_xor((uint32_t)(x >> 32), off, 64);
+    return ((uint64_t)hi << 32) | lo;
+}
+
+// Parts of a row in the workspace: keys [rows, parts, n_out], then (maximum, sum) [rows, parts].
+struct SelectPlan {
+    int parts;
+    int per_part;  // tokens of a part, a multiple of kRound
+};
+
+__host__ __device__ inline int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
+
+inline SelectPlan select_plan(int64_t rows, int V) {
+    // about four workgroups per CU, and at least one round each; rounds begin at 16-byte boundaries,
+    // up to 7 tokens before the row
+    const int64_t rounds = div_up((int64_t)V + 7, kRound);
+    int64_t parts = div_up(1024, rows < 1 ? 1 : rows);
+    parts = parts > rounds ? rounds : parts;
+    const int64_t per = div_up(rounds, parts);
+    return SelectPlan{(int)div_up(rounds, per), (int)(per * kRound)};
+}
+
+// The logits of a thread's kPer tokens of the round at `base` (row + base is 16-byte aligned).  A
+// whole round is read in 16-byte vectors; one that the row's ends cut, value by value with the
+// tokens strided over the threads, so that short ones fill every thread.
+template <typename T>
+struct Round {
+    static constexpr int W = 16 / sizeof(T);  // logits per vector
+    static __device__ __forceinline__ int token(int base, int i, bool whole) {
+        return whole ? base + (i / W) * kThreads * W + (int)threadIdx.x * W + i % W
+                     : base + i * kThreads + (int)threadIdx.x;
+    }
+    static __device__ __forceinline__ void load(const T* row, int base, int first, int last, bool whole,
+                                                float (&x)[kPer]) {
+        if (whole) {
+#pragma unroll
+            for (int v = 0; v < kPer / W; ++v) {
+                const u32x4 b = *reinterpret_cast<const u32x4*>(row + token(base, v * W, true));
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    if (sizeof(T) == 4) x[v * W + j] = clean(__uint_as_float(b[j]));
+                    else x[v * W + j] = clean(bf16_to_f32((uint16_t)(b[j >> 1] >> (16 * (j & 1)))));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int t = token(base, i, false);
+                x[i] = t >= first && t < last ? clean(ld_in(row, t)) : -INFINITY;
+            }
+        }
+    }
+};
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, SelectPlan plan, int group_shift,
+                                                             uint64_t* keys, float2* sums) {
+    __shared__ uint64_t s_list[kList];
+    __shared__ uint64_t s_key[kThreads / 64];
+    __shared__ float s_m[kThreads / 64], s_l[kThreads / 64];
+    __shared__ int s_count;
+    const int64_t row = blockIdx.x / plan.parts;
+    const int part = blockIdx.x % plan.parts, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint64_t* out = keys + (row * plan.parts + part) * a.n_out;
+    if (a.finished && a.finished[row]) {
+        // the end token at log-probability 0, then the others in order at -inf
+        if (tid < a.n_out) {
+            uint64_t k = 0;
+            if (part == 0) {
+                const int t = tid - 1 < a.eos ? tid - 1 : tid;
+                k = tid == 0 ? key_of(0.f, a.eos) : t < a.V ? key_of(-INFINITY, t) : 0;
+            }
+            out[tid] = k;
+        }
+        if (tid == 0) sums[row * plan.parts + part] = part == 0 ? make_float2(0.f, 1.f) : make_float2(-INFINITY, 0.f);
+        return;
+    }
+    const T* x0 = static_cast<const T*>(a.logits) + row * a.row_stride;
+    // tokens of the part, from `begin` (aligned, before the row for part 0 of a row that is not)
+    const int begin = part * plan.per_part - (int)((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
+    const int first = begin < 0 ? 0 : begin, last = begin + plan.per_part < a.V ? begin + plan.per_part : a.V;
+    if (tid == 0) s_count = 0;
+    float m = -INFINITY, l = 0.f, bar = -INFINITY;  // running maximum and sum of this thread, threshold
+    for (int base = begin; base < last; base += kRound) {
+        const bool whole = base >= 0 && base + kRound <= last;
+        float x[kPer];
+        Round<T>::load(x0, base, first, last, whole, x);
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
+        const float now = fmaxf(m, top), ref = now == -INFINITY ? 0.f : now;
+        float sum = l * fast_exp(m - ref);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum += fast_exp(x[i] - ref);
+        m = now;
+        l = sum;
+        // the least of the maxima of groups of 2^group_shift threads
+        float g = top;
+        for (int off = 1; off < (1 << group_shift) && off < 64; off <<= 1) g = fmaxf(g, __shfl_xor(g, off, 64));
+        float least = g;
+        if (group_shift >= 6) {
+            if (lane == 0) s_m[wave] = g;
+            __syncthreads();
+            const int waves = 1 << (group_shift - 6);
+            least = INFINITY;
+            for (int w0 = 0; w0 < kThreads / 64; w0 += waves) {
+                float gm = s_m[w0];
+                for (int w = 1; w < waves; ++w) gm = fmaxf(gm, s_m[w0 + w]);
+                least = fminf(least, gm);
+            }
+        } else {
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) least = fminf(least, __shfl_xor(least, off, 64));
+            if (lane == 0) s_m[wave] = least;
+            __syncthreads();
+            for (int w = 0; w < kThreads / 64; ++w) least = fminf(least, s_m[w]);
+        }
+        bar = fmaxf(bar, least);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (x[i] >= bar && x[i] > -INFINITY) {
+                const int at = atomicAdd(&s_count, 1);
+                if (at < kList) s_list[at] = key_of(x[i], Round<T>::token(base, i, whole));
+            }
+        __syncthreads();  // s_m is written again in the next round
+    }
+    // log-sum of the part
+    float M = m;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
+    if (lane == 0) s_m[wave] = M;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 64; ++w) M = fmaxf(M, s_m[w]);
+    float sum = l * fast_exp(m - (M == -INFINITY ? 0.f : M));
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    if (lane == 0) s_l[wave] = sum;
+    __syncthreads();
+    if (tid == 0) {
+        sum = 0.f;
+        for (int w = 0; w < kThreads / 64; ++w) sum += s_l[w];
+        sums[row * plan.parts + part] = make_float2(M, sum);
+    }
+    const int count = s_count;
+    if (count <= kList) {
+        if (count < a.n_out && wave == 0) {
+            // fewer logits than places are above -inf, and all of those are in the list: the first of
+            // the part's other tokens follow at -inf
+            int filled = count;
+            for (int t0 = first; t0 < last && filled < a.n_out; t0 += 64) {
+                bool other = t0 + lane < last;
+                for (int j = 0; j < count; ++j) other = other && 0xFFFFFFFFu - (uint32_t)s_list[j] != (uint32_t)(t0 + lane);
+                const uint64_t mask = __ballot(other);
+                const int at = filled + __popcll(mask & ((1ull << lane) - 1));
+                if (other && at < a.n_out) out[at] = key_of(-INFINITY, t0 + lane);
+                filled += __popcll(mask);
+            }
+            if (lane >= filled && lane < a.n_out) out[lane] = 0;
+        }
+        for (int i = tid; i < count; i += kThreads) {
+            const uint64_t k = s_list[i];
+            int rank = 0;
+            for (int j = 0; j < count; ++j) rank += s_list[j] > k;
+            if (rank < a.n_out) out[rank] = k;
+        }
+        return;
+    }
+    // too many at or above the threshold: one maximum of the keys below the last one after another
+    uint64_t limit = ~0ull;
+    for (int o = 0; o < a.n_out; ++o) {
+        uint64_t best = 0;
+        for (int base = begin; base < last; base += kRound) {
+            const bool whole = base >= 0 && base + kRound <= last;
+            float x[kPer];
+            Round<T>::load(x0, base, first, last, whole, x);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int t = Round<T>::token(base, i, whole);
+                const uint64_t k = t >= first && t < last ? key_of(x[i], t) : 0;
+                if (k < limit && k > best) best = k;
+            }
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+            const uint64_t y = shfl_xor64(best, off);
+            best = y > best ? y : best;
+        }
+        __syncthreads();
+        if (lane == 0) s_key[wave] = best;
+        __syncthreads();
+        for (int w = 0; w < kThreads / 64; ++w) best = s_key[w] > best ? s_key[w] : best;
+        if (tid == 0) out[o] = best;
+        limit = best;
+    }
+}
+
+// A candidate of the join: c, the beam and the key inside the beam.
+struct Cand {
+    double c;
+    uint64_t key;
+    int beam;
+};
+// whether a comes before b
+__device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
+    if (a.c != b.c) return a.c > b.c;
+    if (a.beam != b.beam) return a.beam < b.beam;
+    return a.key > b.key;
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinList = 1024;
+
+__global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs a, SelectPlan plan, int group_shift,
+                                                                 const uint64_t* keys, const float2* sums) {
+    __shared__ double s_lse[kMaxOut];
+    __shared__ Cand s_list[kJoinList];
+    __shared__ Cand s_best[kJoinThreads / 64];
+    __shared__ double s_m[kJoinThreads / 64];
+    __shared__ int s_count;
+    const int64_t b = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (tid == 0) s_count = 0;
+    // the beams' log-sums: a wave per beam, its lanes over the parts
+    for (int k = wave; k < a.K; k += kJoinThreads / 64) {
+        const float2* y = sums + (b * a.K + k) * plan.parts;
+        double M = -INFINITY, sum = 0.;
+        for (int p = lane; p < plan.parts; p += 64) M = fmax(M, (double)y[p].x);
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) M = fmax(M, __shfl_xor(M, off, 64));
+        for (int p = lane; p < plan.parts; p += 64)
+            if (y[p].y != 0.f) sum += exp((double)y[p].x - M) * (double)y[p].y;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        if (lane == 0) s_lse[k] = sum == 0. ? -INFINITY : M + log(sum);
+    }
+    __syncthreads();
+    const int per_beam = plan.parts * a.n_out, n = a.K * per_beam;
+    const uint64_t* ks = keys + b * n;
+    auto cand = [&](int i) {
+        Cand x;
+        x.beam = i / per_beam;
+        x.key = ks[i];
+        double c = (double)a.scores[b * a.K + x.beam] + (double)unordered((uint32_t)(x.key >> 32)) - s_lse[x.beam];
+        x.c = c != c ? -INFINITY : c;
+        return x;
+    };
+    // threshold: the least of the maxima of n_out groups of threads
+    double top = -INFINITY;
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const Cand x = cand(i);
+        if (x.key) top = fmax(top, x.c);
+    }
+    for (int off = 1; off < (1 << group_shift) && off < 64; off <<= 1) top = fmax(top, __shfl_xor(top, off, 64));
+    double bar = top;
+    if (group_shift >= 6) {
+        if (lane == 0) s_m[wave] = top;
+        __syncthreads();
+        const int waves = 1 << (group_shift - 6);
+        bar = INFINITY;
+        for (int w0 = 0; w0 < kJoinThreads / 64; w0 += waves) {
+            double gm = s_m[w0];
+            for (int w = 1; w < waves; ++w) gm = fmax(gm, s_m[w0 + w]);
+            bar = fmin(bar, gm);
+        }
+    } else {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) bar = fmin(bar, __shfl_xor(bar, off, 64));
+        if (lane == 0) s_m[wave] = bar;
+        __syncthreads();
+        for (int w = 0; w < kJoinThreads / 64; ++w) bar = fmin(bar, s_m[w]);
+    }
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const Cand x = cand(i);
+        if (x.key && x.c >= bar && x.c > -INFINITY) {
+            const int at = atomicAdd(&s_count, 1);
+            if (at < kJoinList) s_list[at] = x;
+        }
+    }
+    __syncthreads();
+    auto emit = [&](int o, const Cand& x) {
+        const int64_t at = b * a.n_out + o;
+        const int token = (int)(0xFFFFFFFFu - (uint32_t)x.key);
+        a.scores_out[at] = (float)x.c;
+        a.parents[at] = x.beam;
+        a.tokens[at] = token;
+        if (a.finished) a.finished_out[at] = (a.finished[b * a.K + x.beam] != 0 || token == a.eos) ? 1 : 0;
+    };
+    const int count = s_count;
+    if (count >= a.n_out && count <= kJoinList) {
+        for (int i = tid; i < count; i += kJoinThreads) {
+            const Cand x = s_list[i];
+            int rank = 0;
+            for (int j = 0; j < count; ++j) rank += before(s_list[j], x);
+            if (rank < a.n_out) emit(rank, x);
+        }
+        return;
+    }
+    Cand limit{INFINITY, ~0ull, -1};  // before every candidate
+    for (int o = 0; o < a.n_out; ++o) {
+        Cand best{-INFINITY, 0, 0x7FFFFFFF};  // behind every candidate
+        for (int i = tid; i < n; i += kJoinThreads) {
+            const Cand x = cand(i);
+            if (x.key && before(limit, x) && before(x, best)) best = x;
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+            Cand y;
+            y.c = __shfl_xor(best.c, off, 64);
+            y.key = shfl_xor64(best.key, off);
+            y.beam = __shfl_xor(best.beam, off, 64);
+            if (before(y, best)) best = y;
+        }
+        __syncthreads();
+        if (lane == 0) s_best[wave] = best;
+        __syncthreads();
+        for (int w = 0; w < kJoinThreads / 64; ++w)
+            if (before(s_best[w], best)) best = s_best[w];
+        if (tid == 0) emit(o, best);
+        limit = best;
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// reorder
+// ------------------------------------------------------------------------------------------
+// In place without scratch: a thread owns one 16-byte column of all K rows of a group, reads the
+// rows it needs into registers and then writes the rows that change, so nobody reads what another
+// one has written.  Rows that stay cost nothing, and a row with several children is read from
+// memory once.
+constexpr int kReorderThreads = 256;
+
+template <int KM>
+__global__ __launch_bounds__(kReorderThreads) void beam_reorder_kernel(PoolList pl, const int32_t* parents, int K,
+                                                                       int64_t groups) {
+    // column group, then state, then group of beams
+    int64_t g = blockIdx.x;
+    const int64_t cg = g % groups;
+    g /= groups;
+    const int st = (int)(g % pl.count);
+    const int64_t b = g / pl.count;
+    const int64_t bytes = pl.bytes[st], at = (cg * kReorderThreads + threadIdx.x) * 16;
+    if (at >= bytes) return;
+    char* base = pl.base[st] + b * K * bytes + at;
+    const int32_t* par = parents + b * K;
+    u32x4 x[KM];
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+        const int p = k < K ? par[k] : k;
+        if (p != k && p >= 0 && p < K) x[k] = *reinterpret_cast<const u32x4*>(base + p * bytes);
+    }
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+        const int p = k < K ? par[k] : k;
+        if (p != k && p >= 0 && p < K) *reinterpret_cast<u32x4*>(base + k * bytes) = x[k];
+    }
+}
+
+// log2 of the threads per group when 256 threads make at least n_out groups
+int group_shift_of(int n_out) {
+    int shift = 8;
+    while ((1 << (8 - shift)) < n_out) --shift;
+    return shift;
+}
+
+}  // namespace
+
+size_t beam_select_workspace(int64_t B, int K, int V, int n_out) {
+    const SelectPlan p = select_plan(B * K, V);
+    return (size_t)div_up(B * K * p.parts * ((int64_t)n_out + 1) * 8, 256) * 256;
+}
+
+hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s) {
+    const int64_t rows = (int64_t)a.B * a.K;
+    if (rows == 0) return hipSuccess;
+    const SelectPlan plan = select_plan(rows, a.V);
+    uint64_t* keys = static_cast<uint64_t*>(a.ws);
+    float2* sums = reinterpret_cast<float2*>(keys + rows * plan.parts * a.n_out);
+    const int shift = group_shift_of(a.n_out);
+    const bool timed = timing_on();
+    if (timed) timed_begin(kKernelBeamScan, s);
+    const dim3 grid((unsigned)(rows * plan.parts));
+    if (a.bf16)
+        hipLaunchKernelGGL(beam_scan_kernel<uint16_t>, grid, dim3(kThreads), 0, s, a, plan, shift, keys, sums);
+    else
+        hipLaunchKernelGGL(beam_scan_kernel<float>, grid, dim3(kThreads), 0, s, a, plan, shift, keys, sums);
+    hipError_t e = hipGetLastError();
+    if (timed) timed_end(s);
+    if (e != hipSuccess) return e;
+    if (timed) timed_begin(kKernelBeamJoin, s);
+    hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)a.B), dim3(kJoinThreads), 0, s, a, plan, shift, keys, sums);
+    e = hipGetLastError();
+    if (timed) timed_end(s);
+    return e;
+}
+
+hipError_t launch_beam_reorder(const PoolList& p, const int32_t* parents, int B, int K, hipStream_t s) {
+    int64_t most = 0;
+    for (int i = 0; i < p.count; ++i) most = p.bytes[i] > most ? p.bytes[i] : most;
+    if (B == 0 || K <= 1 || most == 0) return hipSuccess;
+    const int64_t groups = div_up(most, kReorderThreads * 16);
+    const dim3 grid((unsigned)(groups * p.count * B)), block(kReorderThreads);
+    const bool timed = timing_on();
+    if (timed) timed_begin(kKernelBeamReorder, s);
+    if (K <= 4) hipLaunchKernelGGL(beam_reorder_kernel<4>, grid, block, 0, s, p, parents, K, groups);
+    else if (K <= 8) hipLaunchKernelGGL(beam_reorder_kernel<8>, grid, block, 0, s, p, parents, K, groups);
+    else if (K <= 16) hipLaunchKernelGGL(beam_reorder_kernel<16>, grid, block, 0, s, p, parents, K, groups);
+    else if (K <= 32) hipLaunchKernelGGL(beam_reorder_kernel<32>, grid, block, 0, s, p, parents, K, groups);
+    else hipLaunchKernelGGL(beam_reorder_kernel<64>, grid, block, 0, s, p, parents, K, groups);
+    const hipError_t e = hipGetLastError();
+    if (timed) timed_end(s);
+    return e;
+}
+
+}  // namespace kda

@@ -1,0 +1,583 @@
+// Pages of a key-value cache: writing new tokens, sharing, reserving, freeing, compacting and
+// copying pages (include/kda.h, "Serving next to the recurrence").
+//
+// The only state besides the tables is one reference count per page.  Free pages are found from
+// the counts: a scan turns them into one bit per page with a running count per 64-bit word and per
+// block, after which the r-th free page is two binary searches and a select inside one word, and
+// the number of used pages before a page one look-up.  Nothing keeps a list whose order could
+// depend on the order in which workgroups ran, so the pages handed out are always the lowest free
+// ones and every integer result is the same from run to run.  The atomics are integer additions and
+// exchanges whose results do not depend on their order.
+#include "kda_device.h"
+#include "kda_internal.h"
+
+namespace kda {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBlockPages = 4096;              // pages per block of the scan
+constexpr int kBlockWords = kBlockPages / 64;  // 64-bit words per block
+
+// ------------------------------------------------------------------------------------------
+// append: keys and values of new tokens into their pages
+// ------------------------------------------------------------------------------------------
+// Pure traffic: each value is read once and written once.  A workgroup takes `tb` tokens; its first
+// threads find the page slot of each (a table look-up, and a binary search over cu_seqlens for
+// packed segments), then all of them move 16-byte vectors of keys and values, a token's head at a
+// time (128 .. 1024 contiguous bytes of a page).
+constexpr int kAppendThreads = 256;
+constexpr int kAppendMaxTokens = 16;
+
+template <bool PACKED>
+__global__ __launch_bounds__(kAppendThreads) void append_kernel(CacheAppendArgs a, int tb, int vpt, int vph_shift,
+                                                                uint32_t vpt_magic) {
+    __shared__ int64_t s_k[kAppendMaxTokens], s_v[kAppendMaxTokens];  // slot offsets in bytes, -1: dropped
+    const int64_t t0 = (int64_t)blockIdx.x * tb;
+    const int nt = (int)(a.T_total - t0 < tb ? a.T_total - t0 : tb);
+    const int row_bytes = a.d * a.esz;
+    if ((int)threadIdx.x < nt) {
+        const int64_t t = t0 + threadIdx.x;
+        int64_t n = t, i = 0;
+        bool in = true;
+        if (PACKED) {  // the last segment that begins at or before t (empty ones begin where the next does)
+            int64_t lo = 0, hi = a.N - 1;
+            while (lo < hi) {
+                const int64_t mid = (lo + hi + 1) >> 1;
+                if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+            }
+            n = lo;
+            i = t - a.cu[n];
+            in = i >= 0 && t < a.cu[n + 1];
+        }
+        int64_t ko = -1, vo = -1;
+        const int64_t pos = (int64_t)a.start[n] + i;
+        if (in && pos >= 0) {
+            const int64_t col = pos / a.page_size;
+            if (col < a.pt.width) {
+                const int32_t p = a.pt.table[n * a.pt.stride + col];
+                if (p >= 0 && p < a.pt.n_pages) {
+                    const int64_t slot = (pos - col * a.page_size) * row_bytes;
+                    ko = p * a.kp_stride * a.esz + slot;
+                    vo = p * a.vp_stride * a.esz + slot;
+                }
+            }
+        }
+        s_k[threadIdx.x] = ko;
+        s_v[threadIdx.x] = vo;
+    }
+    __syncthreads();
+    const char* ks = static_cast<const char*>(a.k) + t0 * a.k_stride * a.esz;
+    const char* vs = static_cast<const char*>(a.v) + t0 * a.v_stride * a.esz;
+    const int64_t kst = a.k_stride * a.esz, vst = a.v_stride * a.esz;
+    const int64_t head_bytes = (int64_t)a.page_size * row_bytes;
+    const int total = nt * vpt;
+    const int vmask = (1 << vph_shift) - 1;
+#pragma unroll 4
+    for (int x = threadIdx.x; x < total; x += kAppendThreads) {
+        const int t = (int)__umulhi((uint32_t)x, vpt_magic);  // x / vpt (exact: x * vpt < 2^32)
+        const int r = x - t * vpt;
+        const int64_t ko = s_k[t], vo = s_v[t];
+        if (ko < 0) continue;
+        const int64_t at = (int64_t)(r >> vph_shift) * head_bytes + (r & vmask) * 16;
+        const u32x4 kv = *reinterpret_cast<const u32x4*>(ks + t * kst + (int64_t)r * 16);
+        const u32x4 vv = *reinterpret_cast<const u32x4*>(vs + t * vst + (int64_t)r * 16);
+        *reinterpret_cast<u32x4*>(static_cast<char*>(a.kp) + ko + at) = kv;
+        *reinterpret_cast<u32x4*>(static_cast<char*>(a.vp) + vo + at) = vv;
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// fork and free: table rows and counts
+// ------------------------------------------------------------------------------------------
+constexpr int kTableThreads = 256;
+
+__device__ __forceinline__ bool is_page(int32_t e, int n_pages) { return e >= 0 && e < n_pages; }
+
+// One thread per entry of the wider of the two sets.  An entry that stays what it was touches no
+// count; otherwise the new page gains a reference and the old one loses it.
+__global__ __launch_bounds__(kTableThreads) void fork_kernel(CacheForkArgs a, uint32_t cols) {
+    const int64_t row = blockIdx.x / cols;
+    const int j = (blockIdx.x % cols) * kTableThreads + threadIdx.x;
+    const bool was = row < a.N, is = row < a.N_out;
+    const int32_t parent = is ? a.parents[row] : -1;
+    const bool live = parent >= 0 && parent < a.N;
+    if (j < a.pt.width) {
+        const int32_t old = was ? a.pt.table[row * a.pt.stride + j] : -1;
+        const int32_t now = live ? a.pt.table[parent * a.pt.stride + j] : -1;
+        if (is) a.table_out[row * a.out_stride + j] = now;
+        if (old != now) {
+            if (is_page(now, a.pt.n_pages)) atomicAdd(a.refs + now, 1);
+            if (is_page(old, a.pt.n_pages)) atomicSub(a.refs + old, 1);
+        }
+    }
+    if (j == 0 && is) a.lengths_out[row] = live ? a.lengths[parent] : 0;
+}
+
+// The exchange makes the first of several workgroups that were given the same row the only one that
+// sees its pages.
+__global__ __launch_bounds__(kTableThreads) void free_kernel(CacheFreeArgs a, uint32_t cols) {
+    const int32_t row = a.rows[blockIdx.x / cols];
+    if (row < 0 || row >= a.N) return;
+    const int j = (blockIdx.x % cols) * kTableThreads + threadIdx.x;
+    if (j < a.width) {
+        const int32_t old = atomicExch(a.table + row * a.stride + j, -1);
+        if (is_page(old, a.n_pages)) atomicSub(a.refs + old, 1);
+    }
+    if (j == 0) a.lengths[row] = 0;
+}
+
+// ------------------------------------------------------------------------------------------
+// scan of the counts
+// ------------------------------------------------------------------------------------------
+// Workspace of reserve and compact.  `bits`: one bit per page (free pages for reserve, used ones
+// for compact); `before`: set bits of the word's block before the word; `block`: set bits of the
+// block; `aux`: per sequence the number of pages needed (reserve), or the counts of the moved
+// pages (compact).
+struct CacheWs {
+    uint64_t* bits;
+    uint32_t* before;
+    int32_t* block;
+    int32_t* aux;
+    int words, blocks;
+};
+
+__host__ __device__ inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+__host__ __device__ inline CacheWs cache_ws(void* ws, int64_t n_pages) {
+    CacheWs w;
+    const int64_t blocks = up(n_pages, kBlockPages) / kBlockPages, words = blocks * kBlockWords;
+    char* p = static_cast<char*>(ws);
+    w.bits = reinterpret_cast<uint64_t*>(p);
+    w.before = reinterpret_cast<uint32_t*>(p + words * 8);
+    w.block = reinterpret_cast<int32_t*>(p + words * 12);
+    w.aux = reinterpret_cast<int32_t*>(p + words * 12 + up(blocks * 4, 16));
+    w.words = (int)words;
+    w.blocks = (int)blocks;
+    return w;
+}
+
+constexpr int kScanThreads = 256;
+
+// One block of 4096 pages per workgroup: wave w takes words w, w + 4, ...; pages behind the pool
+// count as not set.
+template <bool FREE>
+__device__ __forceinline__ void scan_block(const int32_t* refs, int n_pages, const CacheWs& w, int b) {
+    __shared__ uint32_t s_pop[kBlockWords];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int32_t r[kBlockWords / 4];
+#pragma unroll
+    for (int i = 0; i < kBlockWords / 4; ++i) {
+        const int p = b * kBlockPages + (i * 4 + wave) * 64 + lane;
+        r[i] = p < n_pages ? refs[p] : (FREE ? 1 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kBlockWords / 4; ++i) {
+        const uint64_t m = __ballot(FREE ? r[i] <= 0 : r[i] > 0);
+        if (lane == 0) {
+            w.bits[b * kBlockWords + i * 4 + wave] = m;
+            s_pop[i * 4 + wave] = __popcll(m);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < kBlockWords) {  // one wave: running counts of the block's 64 words
+        const uint32_t own = s_pop[lane];
+        uint32_t x = own;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t y = __shfl_up(x, off, 64);
+            if (lane >= off) x += y;
+        }
+        w.before[b * kBlockWords + lane] = x - own;
+        if (lane == 63) w.block[b] = (int32_t)x;
+    }
+}
+
+// Exclusive running sums of the blocks' counts into LDS; the total is s_prefix[blocks].
+constexpr int kMaxBlocks = (1 << 24) / kBlockPages;
+
+__device__ __forceinline__ void block_prefix(const CacheWs& w, int32_t* s_prefix) {
+    // wave 0: 64 blocks at a time
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x;
+        int32_t carry = 0;
+        for (int b0 = 0; b0 < w.blocks; b0 += 64) {
+            const int32_t own = b0 + lane < w.blocks ? w.block[b0 + lane] : 0;
+            int32_t x = own;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const int32_t y = __shfl_up(x, off, 64);
+                if (lane >= off) x += y;
+            }
+            if (b0 + lane < w.blocks) s_prefix[b0 + lane] = carry + x - own;
+            carry += __shfl(x, 63, 64);
+        }
+        if (lane == 0) s_prefix[w.blocks] = carry;
+    }
+    __syncthreads();
+}
+
+// the page of the r-th set bit, 0 <= r < total
+__device__ __forceinline__ int32_t select_page(const CacheWs& w, const int32_t* s_prefix, int32_t r) {
+    int lo = 0, hi = w.blocks - 1;
+    while (lo < hi) {  // the last block that begins at or before rank r
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_prefix[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    const int b = lo;
+    uint32_t k = (uint32_t)(r - s_prefix[b]);
+    lo = 0;
+    hi = kBlockWords - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (w.before[b * kBlockWords + mid] <= k) lo = mid; else hi = mid - 1;
+    }
+    const uint64_t m = w.bits[b * kBlockWords + lo];
+    k -= w.before[b * kBlockWords + lo];
+    int at = 0;
+#pragma unroll
+    for (int half = 32; half > 0; half >>= 1) {
+        const uint32_t c = __popcll((m >> at) & ((1ull << half) - 1));
+        if (k >= c) {
+            k -= c;
+            at += half;
+        }
+    }
+    return b * kBlockPages + lo * 64 + at;
+}
+
+// set bits before page p, 0 <= p <= n_pages rounded up to a block
+__device__ __forceinline__ int32_t bits_before(const CacheWs& w, const int32_t* s_prefix, int32_t p) {
+    const int b = p / kBlockPages;
+    if (b >= w.blocks) return s_prefix[w.blocks];
+    const int word = p >> 6;
+    return s_prefix[b] + (int32_t)w.before[word] + __popcll(w.bits[word] & ((1ull << (p & 63)) - 1));
+}
+
+__device__ __forceinline__ bool bit_of(const CacheWs& w, int32_t p) { return (w.bits[p >> 6] >> (p & 63)) & 1; }
+
+// ------------------------------------------------------------------------------------------
+// reserve
+// ------------------------------------------------------------------------------------------
+// First launch: the blocks' scans, and one wave per sequence that counts the pages it needs and
+// marks them in its row: -1 where there is no page, -2 - e where page e is shared.  The marks carry
+// the verdict on the counts as they were when the call began over to the second launch, which
+// changes them.
+constexpr int kRowsPerGroup = kScanThreads / 64;
+
+// columns that hold the new tokens' positions; none where nothing is to be reserved, bad where the
+// row is too narrow
+struct Span64 {
+    int64_t first, last;
+    bool none, bad;
+};
+__device__ __forceinline__ Span64 new_columns(int32_t len, int32_t add, int page_size, int width) {
+    Span64 s{0, -1, true, false};
+    if (add <= 0) return s;
+    if (len < 0) {
+        s.bad = true;
+        return s;
+    }
+    s.first = len / page_size;
+    s.last = ((int64_t)len + add - 1) / page_size;
+    s.bad = s.last >= width || (int64_t)len + add > INT32_MAX;
+    s.none = s.bad;
+    return s;
+}
+
+__global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserveArgs a) {
+    const CacheWs w = cache_ws(a.ws, a.n_pages);
+    if ((int)blockIdx.x < w.blocks) {
+        scan_block<true>(a.refs, a.n_pages, w, blockIdx.x);
+        return;
+    }
+    const int lane = threadIdx.x & 63;
+    const int64_t n = (int64_t)(blockIdx.x - w.blocks) * kRowsPerGroup + (threadIdx.x >> 6);
+    if (n >= a.N) return;
+    const Span64 s = new_columns(a.lengths[n], a.new_tokens[n], a.page_size, a.width);
+    int32_t need = 0;
+    if (!s.none)
+        for (int64_t j0 = s.first; j0 <= s.last; j0 += 64) {
+            const int64_t j = j0 + lane;
+            bool want = false;
+            if (j <= s.last) {
+                int32_t* e = a.table + n * a.stride + j;
+                const int32_t p = *e;
+                const bool page = is_page(p, a.n_pages);
+                want = !page || a.refs[p] > 1;
+                if (want) *e = page ? -2 - p : -1;
+            }
+            need += __popcll(__ballot(want));
+        }
+    if (lane == 0) w.aux[n] = s.bad ? -1 : need;
+}
+
+// Second launch: one wave per sequence.  Its first page is the free one whose rank is the sum of the
+// needs before it; a sequence that is not served gets its marks taken back.
+__global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs a) {
+    __shared__ int32_t s_prefix[kMaxBlocks + 1];
+    __shared__ int64_t s_sum[kRowsPerGroup];
+    const CacheWs w = cache_ws(a.ws, a.n_pages);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n0 = (int64_t)blockIdx.x * kRowsPerGroup, n = n0 + wave;
+    // pages needed by the sequences before this group
+    int64_t sum = 0;
+    for (int64_t i = threadIdx.x; i < n0; i += kScanThreads) sum += w.aux[i] > 0 ? w.aux[i] : 0;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    if (lane == 0) s_sum[wave] = sum;
+    block_prefix(w, s_prefix);  // ends with a barrier
+    if (n >= a.N) return;
+    int64_t base = 0;
+    for (int i = 0; i < kRowsPerGroup; ++i) base += s_sum[i];
+    for (int i = 0; i < wave; ++i) base += w.aux[n0 + i] > 0 ? w.aux[n0 + i] : 0;
+    const int32_t need = w.aux[n], len = a.lengths[n], add = a.new_tokens[n];
+    const Span64 s = new_columns(len, add, a.page_size, a.width);
+    const bool served = add > 0 && need >= 0 && base + need <= s_prefix[w.blocks];
+    int32_t from = -1, to = -1;
+    if (!s.none)
+        for (int64_t j0 = s.first; j0 <= s.last; j0 += 64) {
+            const int64_t j = j0 + lane;
+            int32_t* e = a.table + n * a.stride + j;
+            const int32_t mark = j <= s.last ? *e : 0;
+            const uint64_t m = __ballot(mark < 0);
+            if (mark < 0) {
+                const int32_t old = -2 - mark;  // -1: no page before
+                if (served) {
+                    const int32_t p = select_page(w, s_prefix, (int32_t)(base + __popcll(m & ((1ull << lane) - 1))));
+                    *e = p;
+                    a.refs[p] = 1;
+                    if (old >= 0) {
+                        atomicSub(a.refs + old, 1);
+                        if (j == s.first && len % a.page_size) {
+                            from = old;
+                            to = p;
+                        }
+                    }
+                } else if (old >= 0) {
+                    *e = old;
+                }
+            }
+            base += __popcll(m);
+        }
+    // the copied page, if any, is the first column's: lane 0 of the first round
+    if (lane == 0) {
+        a.copies[2 * n] = from;
+        a.copies[2 * n + 1] = to;
+        a.granted[n] = served ? add : 0;
+        if (served) a.lengths[n] = len + add;
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// compact
+// ------------------------------------------------------------------------------------------
+// With L used pages, the holes are the free pages before L and the movers the used ones at or
+// behind it; there are as many of one as of the other, and sources and targets are disjoint, so the
+// copies can run in any order.
+__global__ __launch_bounds__(kScanThreads) void compact_scan_kernel(CacheCompactArgs a) {
+    scan_block<false>(a.refs, a.pt.n_pages, cache_ws(a.ws, a.pt.n_pages), blockIdx.x);
+}
+
+__global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(CacheCompactArgs a) {
+    __shared__ int32_t s_prefix[kMaxBlocks + 1];
+    const CacheWs w = cache_ws(a.ws, a.pt.n_pages);
+    block_prefix(w, s_prefix);
+    const int32_t L = s_prefix[w.blocks], front = bits_before(w, s_prefix, L), count = L - front;
+    const int p = blockIdx.x * kScanThreads + threadIdx.x;
+    if (p < a.pt.n_pages) {
+        const bool used = bit_of(w, p);
+        if (used != (p < L)) {
+            const int32_t before = bits_before(w, s_prefix, p);
+            if (!used) {
+                a.moves[2 * (int64_t)(p - before) + 1] = p;
+            } else {
+                a.moves[2 * (int64_t)(before - front)] = p;
+                w.aux[before - front] = a.refs[p];
+            }
+        }
+    }
+    if (p < a.pt.n_pages / 2 && p >= count) {
+        a.moves[2 * (int64_t)p] = -1;
+        a.moves[2 * (int64_t)p + 1] = -1;
+    }
+}
+
+__global__ __launch_bounds__(kScanThreads) void compact_remap_kernel(CacheCompactArgs a, int count_groups,
+                                                                     int col_groups) {
+    __shared__ int32_t s_prefix[kMaxBlocks + 1];
+    const CacheWs w = cache_ws(a.ws, a.pt.n_pages);
+    block_prefix(w, s_prefix);
+    const int32_t L = s_prefix[w.blocks];
+    if ((int)blockIdx.x < count_groups) {
+        const int p = blockIdx.x * kScanThreads + threadIdx.x;
+        if (p < a.pt.n_pages) {
+            int32_t r = 0;
+            if (p < L) r = bit_of(w, p) ? a.refs[p] : w.aux[p - bits_before(w, s_prefix, p)];
+            a.refs_out[p] = r;
+        }
+        return;
+    }
+    const int g = blockIdx.x - count_groups;
+    const int64_t row = g / col_groups;
+    const int j = (g % col_groups) * kScanThreads + threadIdx.x;
+    if (j >= a.pt.width) return;
+    int32_t e = a.pt.table[row * a.pt.stride + j];
+    if (e >= L && e < a.pt.n_pages && bit_of(w, e))
+        e = a.moves[2 * (int64_t)(bits_before(w, s_prefix, e) - bits_before(w, s_prefix, L)) + 1];
+    a.table_out[row * a.out_stride + j] = e;
+}
+
+// ------------------------------------------------------------------------------------------
+// copies of pages
+// ------------------------------------------------------------------------------------------
+// Traffic only.  Work items are (pair, pool, 32 KiB piece); a workgroup takes every G-th item, so
+// that the valid pairs spread over the chip wherever they stand in the list.  A wave reads the pairs
+// of 64 of its workgroup's items at once and steps over the ones without a page.
+constexpr int kCopyThreads = 256;
+constexpr int64_t kCopyPiece = 32768;
+constexpr int kCopyGroups = 2048;
+
+__global__ __launch_bounds__(kCopyThreads) void pages_copy_kernel(PoolList pl, int n_pages, const int32_t* pairs,
+                                                                  int64_t n_pairs, int pieces, int64_t items) {
+    const int lane = threadIdx.x & 63;
+    const int64_t G = gridDim.x;
+    const int per_pair = pl.count * pieces;
+    for (int64_t it0 = blockIdx.x; it0 < items; it0 += 64 * G) {
+        const int64_t it = it0 + lane * G;
+        int32_t src = -1, dst = -1;
+        if (it < items) {
+            const int64_t pair = it / per_pair;
+            src = pairs[2 * pair];
+            dst = pairs[2 * pair + 1];
+        }
+        uint64_t m = __ballot(is_page(src, n_pages) && is_page(dst, n_pages) && src != dst);
+        while (m) {
+            const int l = __builtin_ctzll(m);
+            m &= m - 1;
+            const int64_t item = it0 + l * G;
+            const int rest = (int)(item % per_pair);
+            const int pool = rest / pieces;
+            const int64_t off = (int64_t)(rest % pieces) * kCopyPiece;
+            const int64_t left = pl.bytes[pool] - off;
+            if (left <= 0) continue;
+            const int vecs = (int)((left < kCopyPiece ? left : kCopyPiece) >> 4);
+            const u32x4* s = reinterpret_cast<const u32x4*>(pl.base[pool] + __shfl(src, l, 64) * pl.stride[pool] + off);
+            u32x4* d = reinterpret_cast<u32x4*>(pl.base[pool] + __shfl(dst, l, 64) * pl.stride[pool] + off);
+            for (int v0 = 0; v0 < vecs; v0 += 4 * kCopyThreads) {
+                u32x4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int v = v0 + i * kCopyThreads + threadIdx.x;
+                    if (v < vecs) x[i] = s[v];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int v = v0 + i * kCopyThreads + threadIdx.x;
+                    if (v < vecs) d[v] = x[i];
+                }
+            }
+        }
+    }
+}
+
+template <typename F>
+hipError_t timed_launch(int id, hipStream_t s, F launch) {
+    const bool timed = timing_on();
+    if (timed) timed_begin(id, s);
+    launch();
+    const hipError_t e = hipGetLastError();
+    if (timed) timed_end(s);
+    return e;
+}
+
+int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
+
+}  // namespace
+
+hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t s) {
+    if (a.T_total == 0) return hipSuccess;
+    const int vph = a.d * a.esz / 16, vpt = a.H * vph;
+    int tb = (4 * kAppendThreads) / vpt;  // about four vectors of keys per thread
+    tb = tb < 1 ? 1 : tb > kAppendMaxTokens ? kAppendMaxTokens : tb;
+    const uint32_t magic = (uint32_t)(((1ull << 32) + vpt - 1) / vpt);
+    const unsigned grid = (unsigned)div_up(a.T_total, tb);
+    return timed_launch(kKernelCacheAppend, s, [&] {
+        if (a.cu)
+            hipLaunchKernelGGL(append_kernel<true>, dim3(grid), dim3(kAppendThreads), 0, s, a, tb, vpt,
+                               __builtin_ctz(vph), magic);
+        else
+            hipLaunchKernelGGL(append_kernel<false>, dim3(grid), dim3(kAppendThreads), 0, s, a, tb, vpt,
+                               __builtin_ctz(vph), magic);
+    });
+}
+
+hipError_t launch_cache_fork(const CacheForkArgs& a, hipStream_t s) {
+    const int64_t rows = a.N > a.N_out ? a.N : a.N_out;
+    if (rows == 0) return hipSuccess;
+    const int64_t cols = a.pt.width ? div_up(a.pt.width, kTableThreads) : 1;
+    return timed_launch(kKernelCacheFork, s, [&] {
+        hipLaunchKernelGGL(fork_kernel, dim3((unsigned)(cols * rows)), dim3(kTableThreads), 0, s, a,
+                           (uint32_t)cols);
+    });
+}
+
+hipError_t launch_cache_free(const CacheFreeArgs& a, hipStream_t s) {
+    if (a.n_rows == 0) return hipSuccess;
+    const int64_t cols = a.width ? div_up(a.width, kTableThreads) : 1;
+    return timed_launch(kKernelCacheFree, s, [&] {
+        hipLaunchKernelGGL(free_kernel, dim3((unsigned)(cols * a.n_rows)), dim3(kTableThreads), 0, s, a,
+                           (uint32_t)cols);
+    });
+}
+
+size_t cache_workspace(int64_t N, int64_t n_pages) {
+    const int64_t blocks = div_up(n_pages, kBlockPages), aux = N > n_pages / 2 ? N : n_pages / 2;
+    return (size_t)up(blocks * kBlockWords * 12 + up(blocks * 4, 16) + aux * 4, 256);
+}
+
+hipError_t launch_cache_reserve(const CacheReserveArgs& a, hipStream_t s) {
+    if (a.N == 0) return hipSuccess;
+    const int64_t blocks = div_up(a.n_pages, kBlockPages), groups = div_up(a.N, kRowsPerGroup);
+    hipError_t e = timed_launch(kKernelCacheScan, s, [&] {
+        hipLaunchKernelGGL(reserve_scan_kernel, dim3((unsigned)(blocks + groups)), dim3(kScanThreads), 0, s, a);
+    });
+    if (e != hipSuccess) return e;
+    return timed_launch(kKernelCacheReserve, s, [&] {
+        hipLaunchKernelGGL(reserve_kernel, dim3((unsigned)groups), dim3(kScanThreads), 0, s, a);
+    });
+}
+
+hipError_t launch_cache_compact(const CacheCompactArgs& a, hipStream_t s) {
+    const int64_t blocks = div_up(a.pt.n_pages, kBlockPages), groups = div_up(a.pt.n_pages, kScanThreads);
+    const int64_t cols = div_up(a.pt.width, kScanThreads);
+    if (groups + a.N * cols == 0) return hipSuccess;
+    hipError_t e = hipSuccess;
+    if (blocks)
+        e = timed_launch(kKernelCacheScan, s, [&] {
+            hipLaunchKernelGGL(compact_scan_kernel, dim3((unsigned)blocks), dim3(kScanThreads), 0, s, a);
+        });
+    if (e == hipSuccess && groups)
+        e = timed_launch(kKernelCachePlan, s, [&] {
+            hipLaunchKernelGGL(compact_plan_kernel, dim3((unsigned)groups), dim3(kScanThreads), 0, s, a);
+        });
+    if (e != hipSuccess) return e;
+    return timed_launch(kKernelCacheRemap, s, [&] {
+        hipLaunchKernelGGL(compact_remap_kernel, dim3((unsigned)(groups + a.N * cols)), dim3(kScanThreads), 0, s, a,
+                           (int)groups, cols ? (int)cols : 1);
+    });
+}
+
+hipError_t launch_pages_copy(const PoolList& p, int n_pages, const int32_t* pairs, int64_t n_pairs, hipStream_t s) {
+    int64_t most = 0;
+    for (int i = 0; i < p.count; ++i) most = p.bytes[i] > most ? p.bytes[i] : most;
+    if (n_pairs == 0 || most == 0) return hipSuccess;
+    const int64_t pieces = div_up(most, kCopyPiece), items = n_pairs * p.count * pieces;
+    const unsigned grid = (unsigned)(items < kCopyGroups ? items : kCopyGroups);
+    return timed_launch(kKernelPagesCopy, s, [&] {
+        hipLaunchKernelGGL(pages_copy_kernel, dim3(grid), dim3(kCopyThreads), 0, s, p, n_pages, pairs, n_pairs,
+                           (int)pieces, items);
+    });
+}
+
+}  // namespace kda

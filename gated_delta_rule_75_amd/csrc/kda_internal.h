@@ -18,7 +18,20 @@ enum KernelId {
     kKernelBwdFwdChain = 6,
     kKernelBwdRevChain = 7,
     kKernelBwdGradState = 8,
-    kKernelBwdGradChunk = 9
+    kKernelBwdGradChunk = 9,
+    kKernelCacheAppend = 10,
+    kKernelPagedDecode = 11,
+    kKernelPagedJoin = 12,
+    kKernelCacheFork = 13,
+    kKernelCacheFree = 14,
+    kKernelCacheScan = 15,
+    kKernelCacheReserve = 16,
+    kKernelCachePlan = 17,
+    kKernelCacheRemap = 18,
+    kKernelPagesCopy = 19,
+    kKernelBeamScan = 20,
+    kKernelBeamJoin = 21,
+    kKernelBeamReorder = 22
 };
 bool timing_on();
 void timed_begin(int kernel_id, hipStream_t s);
@@ -115,5 +128,130 @@ hipError_t noalloc_scratch(hipStream_t s, void** out);
 // decode step
 bool decode_supported(int dk, int dv);
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------------------
+// paged key-value cache and beam search
+// ---------------------------------------------------------------------------------------
+// Pages [n_pages, H_kv, page_size, d] and the table that names them (include/kda.h).
+struct PageTable {
+    const int32_t* table;
+    int64_t stride;  // elements between rows
+    int width;       // entries of a row
+    int n_pages;
+};
+
+struct CacheAppendArgs {
+    const void* k;
+    const void* v;
+    int64_t k_stride, v_stride;  // elements between tokens
+    const int32_t* cu;           // [N + 1] or nullptr (one token per sequence)
+    const int32_t* start;        // [N]
+    int64_t N, T_total;
+    void* kp;
+    void* vp;
+    int64_t kp_stride, vp_stride;  // elements between pages
+    PageTable pt;
+    int page_size, H, d, esz;
+};
+hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t s);
+
+struct PagedDecodeArgs {
+    const void* q;
+    int64_t q_stride;
+    const void* kp;
+    const void* vp;
+    int64_t kp_stride, vp_stride;
+    PageTable pt;
+    const int32_t* lengths;
+    int64_t N;
+    int page_size, Hq, Hkv, d, bf16;
+    float scale;
+    int window, sinks;
+    int64_t max_length;  // > 0, at most width * page_size
+    float* o;
+    float* lse;  // or nullptr
+    void* ws;
+};
+bool paged_decode_supported(int d);
+size_t paged_decode_workspace(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_length, int window, int sinks);
+hipError_t launch_paged_decode(const PagedDecodeArgs& a, hipStream_t s);
+
+struct CacheForkArgs {
+    PageTable pt;
+    const int32_t* lengths;
+    int64_t N;
+    int32_t* refs;
+    const int32_t* parents;
+    int64_t N_out;
+    int32_t* table_out;
+    int64_t out_stride;
+    int32_t* lengths_out;
+};
+hipError_t launch_cache_fork(const CacheForkArgs& a, hipStream_t s);
+
+struct CacheFreeArgs {
+    int32_t* table;
+    int64_t stride;
+    int width, n_pages;
+    int32_t* lengths;
+    int64_t N;
+    int32_t* refs;
+    const int32_t* rows;
+    int64_t n_rows;
+};
+hipError_t launch_cache_free(const CacheFreeArgs& a, hipStream_t s);
+
+struct CacheReserveArgs {
+    int32_t* table;
+    int64_t stride;
+    int width, n_pages, page_size;
+    int32_t* lengths;
+    int64_t N;
+    int32_t* refs;
+    const int32_t* new_tokens;
+    int32_t* copies;
+    int32_t* granted;
+    void* ws;
+};
+hipError_t launch_cache_reserve(const CacheReserveArgs& a, hipStream_t s);
+
+struct CacheCompactArgs {
+    PageTable pt;
+    int64_t N;
+    const int32_t* refs;
+    int32_t* table_out;
+    int64_t out_stride;
+    int32_t* refs_out;
+    int32_t* moves;
+    void* ws;
+};
+hipError_t launch_cache_compact(const CacheCompactArgs& a, hipStream_t s);
+size_t cache_workspace(int64_t N, int64_t n_pages);
+
+// Buffers of one launch that copies pages or reorders rows.
+constexpr int kMaxPools = 32;
+struct PoolList {
+    char* base[kMaxPools];
+    int64_t stride[kMaxPools];  // bytes between pages
+    int64_t bytes[kMaxPools];   // bytes of a page
+    int count;
+};
+hipError_t launch_pages_copy(const PoolList& p, int n_pages, const int32_t* pairs, int64_t n_pairs, hipStream_t s);
+hipError_t launch_beam_reorder(const PoolList& p, const int32_t* parents, int B, int K, hipStream_t s);
+
+struct BeamSelectArgs {
+    const void* logits;
+    int64_t row_stride;
+    const float* scores;
+    const uint8_t* finished;
+    int B, K, V, n_out, eos, bf16;
+    float* scores_out;
+    int32_t* parents;
+    int32_t* tokens;
+    uint8_t* finished_out;
+    void* ws;
+};
+size_t beam_select_workspace(int64_t B, int K, int V, int n_out);
+hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s);
 
 }  // namespace kda

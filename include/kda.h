@@ -312,6 +312,227 @@ int kda_validate_snapshot_cu(const int32_t* cu, const int32_t* snapshot_cu, int3
                              int32_t chunk);
 int kda_validate_gates(const float* g, int64_t n_g, const float* beta, int64_t n_beta, int32_t raw);
 
+/*
+ * Serving next to the recurrence: paged key-value cache, branching, beam search
+ * ==========================================================================
+ *
+ * A hybrid stack runs softmax-attention layers between its recurrent ones.
+ * Their keys and values grow with the context, so a serving program keeps them
+ * in pages of a fixed number of tokens, names the pages of a sequence in a
+ * table, and shares pages between sequences that have a common beginning.  The
+ * recurrent states have a fixed size and are copied instead.
+ *
+ * Layouts (all device memory owned by the caller; the Conventions above hold):
+ *   k_pages, v_pages  [n_pages, H_kv, page_size, d] dtype: page p starts
+ *                     p * page_stride elements behind the pointer and is
+ *                     contiguous.  16-byte aligned, and so is the stride in
+ *                     bytes; a stride larger than the page is allowed (several
+ *                     layers, or keys and values, in one pool).
+ *   page_size         tokens per page, a multiple of 16 (16 .. 4096)
+ *   page_table        int32 [N, table_pages], row n starts n * table_stride
+ *                     elements behind the pointer: entry j names the page that
+ *                     holds tokens j * page_size .. of sequence n.  An entry
+ *                     outside [0, n_pages) means that there is no page (write
+ *                     -1): attention leaves its tokens out, writes to it are
+ *                     dropped.
+ *   lengths           int32 [N], tokens of each sequence
+ *   refcount          int32 [n_pages]: how many table entries (of all tables of
+ *                     the pool) name the page; 0 means that it is free.  There
+ *                     is no other list of free pages.
+ * Every index that a kernel reads from device memory (table entries, parents,
+ * rows, copy pairs) is checked against its range there, so that a wrong one is
+ * left out and never makes a kernel read or write outside the caller's buffers.
+ * All calls are deterministic: integer results do not depend on the order in
+ * which workgroups run, and free pages are taken lowest first.
+ */
+
+/*
+ * kda_cache_append — writes the keys and values of new tokens into the pages.
+ *   k, v        token t at t * k_stride (v_stride) elements: [H_kv, d] dtype,
+ *               contiguous; 16-byte aligned, strides too
+ *   cu_seqlens  DEVICE int32 [N + 1] as in kda_append_prefill (tokens
+ *               cu[n] .. cu[n+1]-1 belong to sequence n), or NULL: one token per
+ *               sequence (T_total = N)
+ *   start       int32 [N], the position of each sequence's first new token
+ * Token i of sequence n goes to position start[n] + i.  A position without a
+ * page (before 0, behind the table, or at an entry that names none) is dropped.
+ * The pages written must belong to one sequence each (kda_cache_reserve sees to
+ * that); two sequences that write the same slot leave either value.
+ * d in {64, 128, 256}.
+ */
+int kda_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens,
+                     const int32_t* start, int32_t N, int64_t T_total, void* k_pages, void* v_pages,
+                     int64_t k_page_stride, int64_t v_page_stride, int32_t n_pages, int32_t page_size,
+                     const int32_t* page_table, int64_t table_stride, int32_t table_pages, int32_t H_kv, int32_t d,
+                     int32_t dtype, void* hip_stream);
+
+/*
+ * kda_paged_decode — softmax attention of one new token per sequence over its
+ * pages (the token's own key and value are in the pages already):
+ *   s_t = scale * q . k_t,   out = sum_t softmax(s)_t v_t,   lse = log sum_t exp(s_t)
+ * over the visible tokens t < lengths[n] of sequence n.
+ *   q       sequence n at n * q_stride elements: [H_q, d] dtype, contiguous;
+ *           16-byte aligned, stride too.  H_q is a multiple of H_kv, and query
+ *           heads g * H_q / H_kv .. share key-value head g.
+ *   window  0, or only the last `window` tokens are visible ...
+ *   sinks   ... and the first `sinks` tokens (0 without a window)
+ *   max_length  an upper bound of lengths that sizes the launch; 0: the table's
+ *           table_pages * page_size.  A longer sequence is cut there.
+ *   out     [N, H_q, d] float; lse [N, H_q] float or NULL
+ * A sequence without a visible token (or whose every visible score is -inf)
+ * gives out = 0 and lse = -inf.  Tokens that are not visible are never used,
+ * whatever bits their slots hold.  Products are exact in bf16 with fp32 sums;
+ * with KDA_BF16 the softmax weights enter their product as bf16 hi plus bf16 lo
+ * (within about 2^-17 of the fp32 weight).
+ * workspace: kda_paged_decode_workspace bytes for the same arguments, 256-byte
+ * aligned, overlapping no argument; holds the partial results where a sequence
+ * is split over several workgroups.  Needs no initialisation.
+ * d in {64, 128, 256}; lengths are a caller contract (checked with
+ * KDA_DEBUG_CHECK=1: 0 <= lengths[n] <= the bound); values below 0 count as 0.
+ */
+int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int64_t k_page_stride,
+                     int64_t v_page_stride, int32_t n_pages, int32_t page_size, const int32_t* page_table,
+                     int64_t table_stride, int32_t table_pages, const int32_t* lengths, int32_t N, int32_t H_q,
+                     int32_t H_kv, int32_t d, int32_t dtype, float scale, int32_t window, int32_t sinks,
+                     int64_t max_length, float* out, float* lse, void* workspace, size_t workspace_bytes,
+                     void* hip_stream);
+
+/* Workspace bytes of kda_paged_decode (max_length > 0: the bound given, or
+ * table_pages * page_size); (size_t)-1 for an unsupported or invalid combination. */
+size_t kda_paged_decode_workspace(int32_t N, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype, int64_t max_length,
+                                  int32_t window, int32_t sinks);
+
+/*
+ * kda_cache_fork — a new set of sequences from an old one, sharing its pages:
+ * new sequence i is old sequence parents[i] (its table row and length), or empty
+ * where parents[i] is outside [0, N).  The old set is released: refcount goes up
+ * by what the new table names and down by what the old one named.  So the same
+ * call branches (an index several times), reorders beams, keeps (i at place i)
+ * and drops sequences.
+ *   page_table, lengths          N rows, table_pages wide
+ *   table_out, lengths_out       N_out rows, as wide; must not overlap the old
+ * Tokens to come are written only after kda_cache_reserve has given the
+ * branches pages of their own.
+ */
+int kda_cache_fork(const int32_t* page_table, int64_t table_stride, const int32_t* lengths, int32_t N,
+                   int32_t table_pages, int32_t* refcount, int32_t n_pages, const int32_t* parents, int32_t N_out,
+                   int32_t* table_out, int64_t table_out_stride, int32_t* lengths_out, void* hip_stream);
+
+/*
+ * kda_cache_free — drops sequences in place: for every r of rows [n_rows] (int32)
+ * the pages of row r lose one reference, its entries become -1 and its length 0.
+ * A row outside [0, N) is left out; one that is named twice is freed once.
+ */
+int kda_cache_free(int32_t* page_table, int64_t table_stride, int32_t* lengths, int32_t N, int32_t table_pages,
+                   int32_t* refcount, int32_t n_pages, const int32_t* rows, int32_t n_rows, void* hip_stream);
+
+/*
+ * kda_cache_reserve — makes room for new_tokens[n] more tokens of every sequence
+ * (int32 [N]; 0 or less: the sequence is left alone).  Every page that holds one
+ * of the positions lengths[n] .. lengths[n] + new_tokens[n] - 1 is made the
+ * sequence's own: an entry without a page, or with one that had more than one
+ * reference when the call began, gets a free page (refcount 1) and gives its old
+ * one back.  Where the old page held tokens of the sequence (a shared page that
+ * is partly filled), the pair (old, new) is returned for kda_pages_copy.
+ *   copies   int32 [N, 2]: the page to copy from and to, or -1, -1
+ *   granted  int32 [N]: new_tokens[n], or 0 where nothing was reserved
+ * lengths[n] grows by granted[n].  Free pages are taken lowest first, sequences
+ * in order; a sequence is served if the pages needed by it and by those before it
+ * are there, whether those were served or not, and if its table row is wide
+ * enough; otherwise it is left as it was.
+ * workspace: kda_cache_workspace_size(N, n_pages) bytes, 256-byte aligned.
+ */
+int kda_cache_reserve(int32_t* page_table, int64_t table_stride, int32_t* lengths, int32_t N, int32_t table_pages,
+                      int32_t* refcount, int32_t n_pages, int32_t page_size, const int32_t* new_tokens,
+                      int32_t* copies, int32_t* granted, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * kda_cache_compact — plans the move of the pages in use to the front of the pool
+ * with the fewest copies: with L pages in use, the i-th used page at or behind L
+ * (ascending) takes the place of the i-th free one before L.
+ *   table_out     page_table with the new places (may be page_table itself)
+ *   refcount_out  refcount with the new places (may be refcount itself); pages
+ *                 L .. are 0
+ *   moves         int32 [n_pages / 2, 2]: (from, to) pairs for kda_pages_copy, in
+ *                 ascending order, then -1, -1
+ * The pages themselves are moved by kda_pages_copy with `moves`, for every pool
+ * the table belongs to.  Entries of other tables of the same pool have to be
+ * mapped in the same call (pass them as further rows).
+ * workspace: kda_cache_workspace_size(N, n_pages) bytes, 256-byte aligned.
+ */
+int kda_cache_compact(const int32_t* page_table, int64_t table_stride, int32_t N, int32_t table_pages,
+                      const int32_t* refcount, int32_t n_pages, int32_t* table_out, int64_t table_out_stride,
+                      int32_t* refcount_out, int32_t* moves, void* workspace, size_t workspace_bytes,
+                      void* hip_stream);
+
+/* Workspace bytes of kda_cache_reserve and kda_cache_compact; (size_t)-1 for
+ * negative sizes or n_pages >= 2^24. */
+size_t kda_cache_workspace_size(int32_t N, int32_t n_pages);
+
+/*
+ * kda_pages_copy — copies pages inside each of n_pools pools: for every pair
+ * (from, to) of pairs [n_pairs, 2] (DEVICE int32) the `page_bytes` bytes of page
+ * `from` go to page `to`.  Pairs with an index outside [0, n_pages) are left out.
+ * No page may be the target of two pairs, or the source of one and the target of
+ * another (the pairs of kda_cache_reserve and kda_cache_compact are such).
+ *   pools, page_strides, page_bytes  HOST arrays of n_pools entries: the pool's
+ *            device address, bytes between pages, bytes of a page (all multiples
+ *            of 16).  Read before the call returns.
+ * Any rows of equal size are pages here, for instance recurrent states
+ * [n_pages, H, d_k, d_v].
+ */
+int kda_pages_copy(void* const* pools, const int64_t* page_strides, const int64_t* page_bytes, int32_t n_pools,
+                   int32_t n_pages, const int32_t* pairs, int64_t n_pairs, void* hip_stream);
+
+/*
+ * kda_beam_select — one step of beam search for B groups of K beams: the n_out
+ * best continuations of each group over its beams and the vocabulary,
+ *   c[k, v] = scores[k] + x[k, v] - log sum_u exp(x[k, u])
+ *   logits     beam r = b * K + k at r * row_stride elements: [V] dtype.  NaN
+ *              counts as -inf.
+ *   scores     [B, K] float, the beams' sums of log-probabilities so far (-inf: a
+ *              beam that does not take part yet)
+ *   finished   uint8 [B, K] or NULL.  A beam with finished != 0 goes on with token
+ *              `eos` alone, at its own score; its logits are not read.
+ *   scores_out, parents, tokens  [B, n_out] float, int32, int32: the chosen c in
+ *              descending order, the beam k it continues (0 .. K-1) and its token
+ *   finished_out  uint8 [B, n_out], with finished only: the parent was finished, or
+ *              the token is `eos`
+ * Order: within a beam by logit, ties to the lower token; over the beams by c
+ * (computed in fp64 from the logit and the beam's log-sum, a running fp32 sum:
+ * beams whose c differ by less than its rounding, about 1e-7, may change places),
+ * ties to the lower beam.  A c that is NaN counts as -inf; continuations of -inf fill the places
+ * that no other one takes.
+ * 1 <= K, n_out <= 64, n_out <= K * V, V < 2^24; eos in [0, V) with finished.
+ * workspace: kda_beam_select_workspace bytes, 256-byte aligned.
+ */
+int kda_beam_select(const void* logits, int64_t row_stride, const float* scores, const uint8_t* finished, int32_t B,
+                    int32_t K, int32_t V, int32_t n_out, int32_t eos, int32_t dtype, float* scores_out,
+                    int32_t* parents, int32_t* tokens, uint8_t* finished_out, void* workspace, size_t workspace_bytes,
+                    void* hip_stream);
+
+/* Workspace bytes of kda_beam_select; (size_t)-1 for an invalid combination. */
+size_t kda_beam_select_workspace(int32_t B, int32_t K, int32_t V, int32_t n_out);
+
+/*
+ * kda_beam_reorder — reorders fixed-size states to the beams they continue, in
+ * place: row b * K + k of every state becomes what row b * K + parents[b, k] was.
+ * Rows whose parent is their own index are neither read nor written for
+ * themselves; a parent outside [0, K) leaves its row as it is.
+ *   states, row_bytes  HOST arrays of n_states entries: the device address of
+ *            [B * K] contiguous rows and the bytes of a row (multiples of 16).
+ *            Read before the call returns.
+ *   parents  DEVICE int32 [B, K]; 1 <= K <= 64
+ */
+int kda_beam_reorder(void* const* states, const int64_t* row_bytes, int32_t n_states, const int32_t* parents,
+                     int32_t B, int32_t K, void* hip_stream);
+
+/* Host-side validator (as those above) of a page table and lengths, HOST arrays:
+ * 0 <= lengths[n] <= min(max_length, table_pages * page_size) and entries that
+ * are -1 or in [0, n_pages). */
+int kda_validate_page_table(const int32_t* page_table, int64_t table_stride, const int32_t* lengths, int32_t N,
+                            int32_t table_pages, int32_t page_size, int32_t n_pages, int64_t max_length);
+
 /* Workspace bytes an op needs (B_or_N sequences, T tokens per sequence for
  * KDA_OP_PREFILL or T_total for KDA_OP_APPEND and KDA_OP_BACKWARD).  0 for
  * KDA_OP_DECODE.
@@ -351,7 +572,20 @@ typedef enum {
     KDA_KERNEL_BWD_FWD_CHAIN = 6,  /* backward: states entering each chunk */
     KDA_KERNEL_BWD_REV_CHAIN = 7,  /* backward: state gradients, chunks in reverse */
     KDA_KERNEL_BWD_GRAD_STATE = 8, /* backward: products over the value axis */
-    KDA_KERNEL_BWD_GRAD_CHUNK = 9  /* backward: in-chunk gradients */
+    KDA_KERNEL_BWD_GRAD_CHUNK = 9, /* backward: in-chunk gradients */
+    KDA_KERNEL_CACHE_APPEND = 10,  /* keys and values written into pages */
+    KDA_KERNEL_PAGED_DECODE = 11,  /* attention over pages */
+    KDA_KERNEL_PAGED_JOIN = 12,    /* attention over pages: join of the split parts */
+    KDA_KERNEL_CACHE_FORK = 13,    /* tables of branched sequences */
+    KDA_KERNEL_CACHE_FREE = 14,    /* sequences dropped */
+    KDA_KERNEL_CACHE_SCAN = 15,    /* reserve, compact: counts of free or used pages */
+    KDA_KERNEL_CACHE_RESERVE = 16, /* reserve: pages handed out */
+    KDA_KERNEL_CACHE_PLAN = 17,    /* compact: moves */
+    KDA_KERNEL_CACHE_REMAP = 18,   /* compact: tables and counts */
+    KDA_KERNEL_PAGES_COPY = 19,    /* pages copied */
+    KDA_KERNEL_BEAM_SCAN = 20,     /* beam search: best logits and log-sum of a part of a row */
+    KDA_KERNEL_BEAM_JOIN = 21,     /* beam search: choice over the beams */
+    KDA_KERNEL_BEAM_REORDER = 22   /* states reordered */
 } kda_kernel;
 
 int kda_timing_begin(void);
