@@ -3,7 +3,7 @@
 Tolerances (u = 2^-24, the fp32 unit roundoff).  Attention, per query with n visible tokens, every
 bound worst-case: a score s is a sum of d exact (bf16) or once-rounded (fp32) products, so it is off
 by ds <= (d + 3) u scale sum|q k|; a weight p = exp(s - m) is off by the factor 1 +- (2 ds + w), w =
-2^-17 for a weight carried as bf16 hi + lo plus 8 u for the exponential and its argument's
+u for a weight carried as three bf16 plus 8 u for the exponential and its argument's
 rounding, |s - m| <= 2 S1 included in ds; sums of n terms and of rescaled partial sums add (n + 64) u.
 So |out - exact| <= vmax (4 ds + 2 w + 2 (n + 64) u) and |lse - exact| <= 2 ds + w + (n + 64) u +
 4 u |lse|.  Everything that is copied or counted is compared bit for bit.
@@ -84,7 +84,7 @@ def attention64(cache, n, q, scale, window=0, sinks=0, absent=()):
     lse = torch.logsumexp(s, 0)
     out = (torch.exp(s - lse)[..., None] * v).sum(0)
     ds = (d + 3) * U * size
-    w = (2.0 ** -17 if cache.kp.dtype == BF16 else 0.0) + 8 * U
+    w = 9 * U
     acc = (len(seen) + 64) * U
     return (out, lse, float(v.abs().max()) * (4 * ds + 2 * w + 2 * acc),
             2 * ds + w + acc + 4 * U * float(lse.abs().max()))
