@@ -27,7 +27,8 @@ constexpr int kMaxOut = 64;     // n_out and K at most
 constexpr int kThreads = 256;
 constexpr int kPer = 16;        // logits of a thread per round
 constexpr int kRound = kThreads * kPer;
-constexpr int kList = 1024;     // collected keys of a part of a row
+constexpr int kWaves = kThreads / 64;
+constexpr int kList = 256;      // collected keys of a wave's share of a part of a row
 
 // Keys order like (value descending, token ascending) when compared as larger first.  No key of a
 // token is 0.
@@ -39,10 +40,10 @@ __device__ __forceinline__ float unordered(uint32_t u) {
     return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 __device__ __forceinline__ uint64_t key_of(float x, int token) {
-    return ((uint64_t)ordered(x) << 32) | (0xFFFFFFFFu - (uint32_t)token);
+    return ((uint64_t)ordered(x + 0.f) << 32) | (0xFFFFFFFFu - (uint32_t)token);
 }
-// NaN counts as -inf; -0 is +0
-__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : x + 0.f; }
+// NaN counts as -inf (the maximum's result is its other operand); -0 becomes +0 where a key is made
+__device__ __forceinline__ float clean(float x) { return fmaxf(x, -INFINITY); }
 
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int off) {
     const uint32_t lo = __shfl_xor((uint32_t)x, off, 64), hi = __shfl_xor((uint32_t)(x >> 32), off, 64);
@@ -58,10 +59,10 @@ struct SelectPlan {
 __host__ __device__ inline int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 inline SelectPlan select_plan(int64_t rows, int V) {
-    // about four workgroups per CU, and at least one round each; rounds begin at 16-byte boundaries,
+    // about eight workgroups per CU, and at least one round each; rounds begin at 16-byte boundaries,
     // up to 7 tokens before the row
     const int64_t rounds = div_up((int64_t)V + 7, kRound);
-    int64_t parts = div_up(1024, rows < 1 ? 1 : rows);
+    int64_t parts = div_up(2048, rows < 1 ? 1 : rows);
     parts = parts > rounds ? rounds : parts;
     const int64_t per = div_up(rounds, parts);
     return SelectPlan{(int)div_up(rounds, per), (int)(per * kRound)};
@@ -77,38 +78,74 @@ struct Round {
         return whole ? base + (i / W) * kThreads * W + (int)threadIdx.x * W + i % W
                      : base + i * kThreads + (int)threadIdx.x;
     }
+    static constexpr int NV = kPer / W;
+    static __device__ __forceinline__ void fetch(const T* row, int base, u32x4 (&raw)[NV]) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) raw[v] = *reinterpret_cast<const u32x4*>(row + token(base, v * W, true));
+    }
+    static __device__ __forceinline__ void values(const u32x4 (&raw)[NV], float (&x)[kPer]) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t word = raw[i / W][(i % W) * sizeof(T) / 4];
+            if (sizeof(T) == 4) x[i] = clean(__uint_as_float(word));
+            else x[i] = clean(__uint_as_float((i & 1) ? word & 0xFFFF0000u : word << 16));
+        }
+    }
+    static __device__ __forceinline__ void singles(const T* row, int base, int first, int last, float (&x)[kPer]) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int t = token(base, i, false);
+            x[i] = t >= first && t < last ? clean(ld_in(row, t)) : -INFINITY;
+        }
+    }
     static __device__ __forceinline__ void load(const T* row, int base, int first, int last, bool whole,
                                                 float (&x)[kPer]) {
         if (whole) {
-#pragma unroll
-            for (int v = 0; v < kPer / W; ++v) {
-                const u32x4 b = *reinterpret_cast<const u32x4*>(row + token(base, v * W, true));
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    if (sizeof(T) == 4) x[v * W + j] = clean(__uint_as_float(b[j]));
-                    else x[v * W + j] = clean(bf16_to_f32((uint16_t)(b[j >> 1] >> (16 * (j & 1)))));
-                }
-            }
+            u32x4 raw[NV];
+            fetch(row, base, raw);
+            values(raw, x);
         } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int t = token(base, i, false);
-                x[i] = t >= first && t < last ? clean(ld_in(row, t)) : -INFINITY;
-            }
+            singles(row, base, first, last, x);
         }
     }
 };
 
+// x of lane ^ 1, ^ 2, then mirrored in 8 and in 16 lanes, then of lane ^ 16 and ^ 32: six steps after
+// which a maximum or minimum covers the wave
+template <int LEVEL>
+__device__ __forceinline__ float other_lane(float x) {
+    if constexpr (LEVEL < 4) {
+        constexpr int ctrl = LEVEL == 0 ? 0xB1 : LEVEL == 1 ? 0x4E : LEVEL == 2 ? 0x141 : 0x140;
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), ctrl, 0xF, 0xF, true));
+    } else {
+        return __shfl_xor(x, LEVEL == 4 ? 16 : 32, 64);
+    }
+}
+template <int LEVEL>
+__device__ __forceinline__ float max_min_step(float x, int shift) {
+    const float y = other_lane<LEVEL>(x);
+    return LEVEL < shift ? fmaxf(x, y) : fminf(x, y);
+}
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, SelectPlan plan, int group_shift,
                                                              uint64_t* keys, float2* sums) {
-    __shared__ uint64_t s_list[kList];
-    __shared__ uint64_t s_key[kThreads / 64];
-    __shared__ float s_m[kThreads / 64], s_l[kThreads / 64];
-    __shared__ int s_count;
+    __shared__ uint64_t s_list[kWaves][kList + 8];
+    __shared__ uint64_t s_key[kWaves];
+    __shared__ float s_m[kWaves], s_l[kWaves], s_g[2][kWaves];
+    __shared__ int s_count[kWaves];
+    using R = Round<T>;
+    static_assert(kThreads == 256, "the groups' reduction below is written for four waves");
     const int64_t row = blockIdx.x / plan.parts;
     const int part = blockIdx.x % plan.parts, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     uint64_t* out = keys + (row * plan.parts + part) * a.n_out;
+    const T* x0 = static_cast<const T*>(a.logits) + row * a.row_stride;
+    // tokens of the part, from `begin` (aligned, before the row for part 0 of a row that is not)
+    const int begin = part * plan.per_part - (int)((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
+    const int first = begin < 0 ? 0 : begin, last = begin + plan.per_part < a.V ? begin + plan.per_part : a.V;
+    u32x4 next[R::NV];
+    bool ready = begin >= 0 && begin + kRound <= last;
+    if (ready) R::fetch(x0, begin, next);  // not behind the look at `finished`, whose latency it would add
     if (a.finished && a.finished[row]) {
         // the end token at log-probability 0, then the others in order at -inf
         if (tid < a.n_out) {
@@ -122,16 +159,16 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
         if (tid == 0) sums[row * plan.parts + part] = part == 0 ? make_float2(0.f, 1.f) : make_float2(-INFINITY, 0.f);
         return;
     }
-    const T* x0 = static_cast<const T*>(a.logits) + row * a.row_stride;
-    // tokens of the part, from `begin` (aligned, before the row for part 0 of a row that is not)
-    const int begin = part * plan.per_part - (int)((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
-    const int first = begin < 0 ? 0 : begin, last = begin + plan.per_part < a.V ? begin + plan.per_part : a.V;
-    if (tid == 0) s_count = 0;
+    int mine = 0;  // keys this wave has collected
     float m = -INFINITY, l = 0.f, bar = -INFINITY;  // running maximum and sum of this thread, threshold
-    for (int base = begin; base < last; base += kRound) {
-        const bool whole = base >= 0 && base + kRound <= last;
+    for (int base = begin, turn = 0; base < last; base += kRound, turn ^= 1) {
+        const bool whole = ready;
         float x[kPer];
-        Round<T>::load(x0, base, first, last, whole, x);
+        if (whole) R::values(next, x);
+        else R::singles(x0, base, first, last, x);
+        // the next round's logits are on their way while this one is worked on
+        ready = base + kRound >= 0 && base + 2 * kRound <= last;
+        if (ready) R::fetch(x0, base + kRound, next);
         float top = x[0];
 #pragma unroll
         for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
@@ -143,60 +180,77 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
         l = sum;
         // the least of the maxima of groups of 2^group_shift threads
         float g = top;
-        for (int off = 1; off < (1 << group_shift) && off < 64; off <<= 1) g = fmaxf(g, __shfl_xor(g, off, 64));
-        float least = g;
-        if (group_shift >= 6) {
-            if (lane == 0) s_m[wave] = g;
-            __syncthreads();
-            const int waves = 1 << (group_shift - 6);
-            least = INFINITY;
-            for (int w0 = 0; w0 < kThreads / 64; w0 += waves) {
-                float gm = s_m[w0];
-                for (int w = 1; w < waves; ++w) gm = fmaxf(gm, s_m[w0 + w]);
-                least = fminf(least, gm);
-            }
-        } else {
+        g = max_min_step<0>(g, group_shift);
+        g = max_min_step<1>(g, group_shift);
+        g = max_min_step<2>(g, group_shift);
+        g = max_min_step<3>(g, group_shift);
+        g = max_min_step<4>(g, group_shift);
+        g = max_min_step<5>(g, group_shift);
+        if (lane == 0) s_g[turn][wave] = g;
+        __syncthreads();
+        g = s_g[turn][0];
+        float h = s_g[turn][2];
+        g = group_shift > 6 ? fmaxf(g, s_g[turn][1]) : fminf(g, s_g[turn][1]);
+        h = group_shift > 6 ? fmaxf(h, s_g[turn][3]) : fminf(h, s_g[turn][3]);
+        bar = fmaxf(bar, group_shift > 7 ? fmaxf(g, h) : fminf(g, h));
+        // every wave appends to a list of its own, in step, which needs no atomics
+        if (__any(top >= bar && top > -INFINITY)) {
 #pragma unroll
-            for (int off = 32; off > 0; off >>= 1) least = fminf(least, __shfl_xor(least, off, 64));
-            if (lane == 0) s_m[wave] = least;
-            __syncthreads();
-            for (int w = 0; w < kThreads / 64; ++w) least = fminf(least, s_m[w]);
+            for (int i = 0; i < kPer; ++i) {
+                const bool in = x[i] >= bar && x[i] > -INFINITY;
+                const uint64_t mask = __ballot(in);
+                if (mask) {
+                    const int at = mine + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+                    if (in && at < kList) s_list[wave][at] = key_of(x[i], R::token(base, i, whole));
+                    mine += __popcll(mask);
+                }
+            }
         }
-        bar = fmaxf(bar, least);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (x[i] >= bar && x[i] > -INFINITY) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kList) s_list[at] = key_of(x[i], Round<T>::token(base, i, whole));
-            }
-        __syncthreads();  // s_m is written again in the next round
     }
     // log-sum of the part
     float M = m;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-    if (lane == 0) s_m[wave] = M;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 64; ++w) M = fmaxf(M, s_m[w]);
+    M = max_min_step<0>(M, 6);
+    M = max_min_step<1>(M, 6);
+    M = max_min_step<2>(M, 6);
+    M = max_min_step<3>(M, 6);
+    M = max_min_step<4>(M, 6);
+    M = max_min_step<5>(M, 6);
     float sum = l * fast_exp(m - (M == -INFINITY ? 0.f : M));
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    if (lane == 0) s_l[wave] = sum;
+    sum += other_lane<0>(sum);
+    sum += other_lane<1>(sum);
+    sum += other_lane<2>(sum);
+    sum += other_lane<3>(sum);
+    sum += other_lane<4>(sum);
+    sum += other_lane<5>(sum);
+    if (lane == 0) {
+        s_m[wave] = M;
+        s_l[wave] = sum;
+    }
+    if (lane == 0) s_count[wave] = mine;
+    if (mine < kList && lane < 8) s_list[wave][mine + lane] = 0;  // for the ranks' unrolled loop
     __syncthreads();
     if (tid == 0) {
+        for (int w = 1; w < kWaves; ++w) M = fmaxf(M, s_m[w]);
         sum = 0.f;
-        for (int w = 0; w < kThreads / 64; ++w) sum += s_l[w];
+        for (int w = 0; w < kWaves; ++w) sum += s_l[w] * fast_exp(s_m[w] - (M == -INFINITY ? 0.f : M));
         sums[row * plan.parts + part] = make_float2(M, sum);
     }
-    const int count = s_count;
-    if (count <= kList) {
+    int count = 0, most = 0;
+    for (int w = 0; w < kWaves; ++w) {
+        count += s_count[w];
+        most = most > s_count[w] ? most : s_count[w];
+    }
+    if (most <= kList) {
         if (count < a.n_out && wave == 0) {
-            // fewer logits than places are above -inf, and all of those are in the list: the first of
+            // fewer logits than places are above -inf, and all of those are in the lists: the first of
             // the part's other tokens follow at -inf
             int filled = count;
             for (int t0 = first; t0 < last && filled < a.n_out; t0 += 64) {
                 bool other = t0 + lane < last;
-                for (int j = 0; j < count; ++j) other = other && 0xFFFFFFFFu - (uint32_t)s_list[j] != (uint32_t)(t0 + lane);
+                for (int w = 0; w < kWaves; ++w)
+                    for (int j = 0; j < s_count[w]; ++j)
+                        other = other && 0xFFFFFFFFu - (uint32_t)s_list[w][j] != (uint32_t)(t0 + lane);
                 const uint64_t mask = __ballot(other);
                 const int at = filled + __popcll(mask & ((1ull << lane) - 1));
                 if (other && at < a.n_out) out[at] = key_of(-INFINITY, t0 + lane);
@@ -204,10 +258,17 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
             }
             if (lane >= filled && lane < a.n_out) out[lane] = 0;
         }
+        // the lists' keys one after another over the threads, so that few waves do it
         for (int i = tid; i < count; i += kThreads) {
-            const uint64_t k = s_list[i];
+            int j = i, in = 0;
+            while (j >= s_count[in]) j -= s_count[in++];
+            const uint64_t k = s_list[in][j];
             int rank = 0;
-            for (int j = 0; j < count; ++j) rank += s_list[j] > k;
+            for (int w = 0; w < kWaves; ++w)
+                for (int j0 = 0; j0 < s_count[w]; j0 += 8) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) rank += s_list[w][j0 + j] > k;
+                }
             if (rank < a.n_out) out[rank] = k;
         }
         return;
@@ -219,10 +280,10 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
         for (int base = begin; base < last; base += kRound) {
             const bool whole = base >= 0 && base + kRound <= last;
             float x[kPer];
-            Round<T>::load(x0, base, first, last, whole, x);
+            R::load(x0, base, first, last, whole, x);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int t = Round<T>::token(base, i, whole);
+                const int t = R::token(base, i, whole);
                 const uint64_t k = t >= first && t < last ? key_of(x[i], t) : 0;
                 if (k < limit && k > best) best = k;
             }
@@ -235,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
         __syncthreads();
         if (lane == 0) s_key[wave] = best;
         __syncthreads();
-        for (int w = 0; w < kThreads / 64; ++w) best = s_key[w] > best ? s_key[w] : best;
+        for (int w = 0; w < kWaves; ++w) best = s_key[w] > best ? s_key[w] : best;
         if (tid == 0) out[o] = best;
         limit = best;
     }
@@ -254,31 +315,37 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
     return a.key > b.key;
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256;  // >= kMaxOut
 constexpr int kJoinList = 1024;
 
-__global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs a, SelectPlan plan, int group_shift,
+__global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs a, SelectPlan plan,
                                                                  const uint64_t* keys, const float2* sums) {
-    __shared__ double s_lse[kMaxOut];
-    __shared__ Cand s_list[kJoinList];
+    __shared__ double s_lse[kMaxOut], s_score[kMaxOut], s_top[kJoinThreads];
+    __shared__ double s_c[kJoinList];
+    __shared__ uint64_t s_key[kJoinList];
+    __shared__ int s_beam[kJoinList];
     __shared__ Cand s_best[kJoinThreads / 64];
     __shared__ double s_m[kJoinThreads / 64];
     __shared__ int s_count;
     const int64_t b = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (tid == 0) s_count = 0;
-    // the beams' log-sums: a wave per beam, its lanes over the parts
-    for (int k = wave; k < a.K; k += kJoinThreads / 64) {
+    // the beams' log-sums: 16 lanes per beam over its parts
+    for (int k = tid >> 4; k < a.K; k += kJoinThreads / 16) {
         const float2* y = sums + (b * a.K + k) * plan.parts;
-        double M = -INFINITY, sum = 0.;
-        for (int p = lane; p < plan.parts; p += 64) M = fmax(M, (double)y[p].x);
+        float M = -INFINITY;
+        double sum = 0.;
+        for (int p = tid & 15; p < plan.parts; p += 16) M = fmaxf(M, y[p].x);
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1) M = fmax(M, __shfl_xor(M, off, 64));
-        for (int p = lane; p < plan.parts; p += 64)
-            if (y[p].y != 0.f) sum += exp((double)y[p].x - M) * (double)y[p].y;
+        for (int off = 8; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
+        for (int p = tid & 15; p < plan.parts; p += 16)
+            if (y[p].y != 0.f) sum += (double)fast_exp(y[p].x - M) * (double)y[p].y;
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
-        if (lane == 0) s_lse[k] = sum == 0. ? -INFINITY : M + log(sum);
+        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        if ((tid & 15) == 0) {
+            s_lse[k] = sum == 0. ? -INFINITY : (double)M + log(sum);
+            s_score[k] = (double)a.scores[b * a.K + k];
+        }
     }
     __syncthreads();
     const int per_beam = plan.parts * a.n_out, n = a.K * per_beam;
@@ -287,41 +354,50 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs 
         Cand x;
         x.beam = i / per_beam;
         x.key = ks[i];
-        double c = (double)a.scores[b * a.K + x.beam] + (double)unordered((uint32_t)(x.key >> 32)) - s_lse[x.beam];
+        const double c = s_score[x.beam] + (double)unordered((uint32_t)(x.key >> 32)) - s_lse[x.beam];
         x.c = c != c ? -INFINITY : c;
         return x;
     };
-    // threshold: the least of the maxima of n_out groups of threads
+    // Threshold: the n_out-th largest of at least n_out candidates.  These are the first `depth` of every
+    // part's list, which are in descending order, or their maxima per thread where there are more than
+    // threads.
+    const int lists = a.K * plan.parts, depth = (a.n_out + lists - 1) / lists, probes = lists * depth;
+    const int held = probes < kJoinThreads ? probes : kJoinThreads;
     double top = -INFINITY;
-    for (int i = tid; i < n; i += kJoinThreads) {
-        const Cand x = cand(i);
+    for (int i = tid; i < probes; i += kJoinThreads) {
+        const Cand x = cand(depth == 1 ? i * a.n_out : i / depth * a.n_out + i % depth);
         if (x.key) top = fmax(top, x.c);
     }
-    for (int off = 1; off < (1 << group_shift) && off < 64; off <<= 1) top = fmax(top, __shfl_xor(top, off, 64));
-    double bar = top;
-    if (group_shift >= 6) {
-        if (lane == 0) s_m[wave] = top;
-        __syncthreads();
-        const int waves = 1 << (group_shift - 6);
-        bar = INFINITY;
-        for (int w0 = 0; w0 < kJoinThreads / 64; w0 += waves) {
-            double gm = s_m[w0];
-            for (int w = 1; w < waves; ++w) gm = fmax(gm, s_m[w0 + w]);
-            bar = fmin(bar, gm);
-        }
-    } else {
+    s_top[tid] = top;
+    __syncthreads();
+    int larger = 0;
+    for (int i0 = 0; i0 < held; i0 += 8) {  // threads without a candidate hold -inf
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1) bar = fmin(bar, __shfl_xor(bar, off, 64));
-        if (lane == 0) s_m[wave] = bar;
-        __syncthreads();
-        for (int w = 0; w < kJoinThreads / 64; ++w) bar = fmin(bar, s_m[w]);
+        for (int i = 0; i < 8; ++i) larger += s_top[i0 + i] > top;
     }
-    for (int i = tid; i < n; i += kJoinThreads) {
-        const Cand x = cand(i);
-        if (x.key && x.c >= bar && x.c > -INFINITY) {
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kJoinList) s_list[at] = x;
+    double bar = tid < held && larger < a.n_out ? top : INFINITY;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) bar = fmin(bar, __shfl_xor(bar, off, 64));
+    if (lane == 0) s_m[wave] = bar;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 64; ++w) bar = fmin(bar, s_m[w]);
+    auto collect = [&](const Cand& x) {
+        if (!x.key || !(x.c >= bar && x.c > -INFINITY)) return false;
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kJoinList) {
+            s_c[at] = x.c;
+            s_key[at] = x.key;
+            s_beam[at] = x.beam;
         }
+        return true;
+    };
+    if (lists >= kJoinThreads) {  // a list per thread, down to its first candidate below the threshold
+        for (int i = tid; i < lists; i += kJoinThreads)
+            for (int r = 0; r < a.n_out; ++r)
+                if (!collect(cand(i * a.n_out + r))) break;
+    } else {
+        for (int i = tid; i < n; i += kJoinThreads) collect(cand(i));
     }
     __syncthreads();
     auto emit = [&](int o, const Cand& x) {
@@ -335,9 +411,15 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs 
     const int count = s_count;
     if (count >= a.n_out && count <= kJoinList) {
         for (int i = tid; i < count; i += kJoinThreads) {
-            const Cand x = s_list[i];
+            const Cand x{s_c[i], s_key[i], s_beam[i]};
             int rank = 0;
-            for (int j = 0; j < count; ++j) rank += before(s_list[j], x);
+            for (int j0 = 0; j0 < count; j0 += 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = j0 + j < count ? j0 + j : i;  // itself is not before itself
+                    rank += before(Cand{s_c[at], s_key[at], s_beam[at]}, x);
+                }
+            }
             if (rank < a.n_out) emit(rank, x);
         }
         return;
@@ -385,21 +467,28 @@ __global__ __launch_bounds__(kReorderThreads) void beam_reorder_kernel(PoolList 
     g /= groups;
     const int st = (int)(g % pl.count);
     const int64_t b = g / pl.count;
-    const int64_t bytes = pl.bytes[st], at = (cg * kReorderThreads + threadIdx.x) * 16;
+    const int64_t bytes = pl.bytes[st], at = cg * kReorderThreads * 16;
     if (at >= bytes) return;
+    const uint32_t left = bytes - at < kReorderThreads * 16 ? (uint32_t)(bytes - at) : kReorderThreads * 16;
     char* base = pl.base[st] + b * K * bytes + at;
     const int32_t* par = parents + b * K;
+    // Every row is loaded and stored, but through a descriptor of no bytes where it stays: nothing is
+    // read or written then, and there are no branches (the compiler made one path for each of the 2^K
+    // combinations of conditions, 234 registers for K = 8: 77 against 65 us for 128 states of 2 MiB)
     u32x4 x[KM];
+    bool moves[KM];
 #pragma unroll
     for (int k = 0; k < KM; ++k) {
-        const int p = k < K ? par[k] : k;
-        if (p != k && p >= 0 && p < K) x[k] = *reinterpret_cast<const u32x4*>(base + p * bytes);
+        int from = k < K ? __builtin_amdgcn_readfirstlane(par[k]) : k;
+        moves[k] = from != k && from >= 0 && from < K;
+        if (!moves[k]) from = 0;
+        x[k] = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(base + from * bytes, moves[k] ? left : 0),
+                                                     threadIdx.x * 16, 0, 0);
     }
 #pragma unroll
-    for (int k = 0; k < KM; ++k) {
-        const int p = k < K ? par[k] : k;
-        if (p != k && p >= 0 && p < K) *reinterpret_cast<u32x4*>(base + k * bytes) = x[k];
-    }
+    for (int k = 0; k < KM; ++k)
+        __builtin_amdgcn_raw_buffer_store_b128(x[k], make_rsrc(base + (moves[k] ? k : 0) * bytes, moves[k] ? left : 0),
+                                               threadIdx.x * 16, 0, 0);
 }
 
 // log2 of the threads per group when 256 threads make at least n_out groups
@@ -434,7 +523,7 @@ hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s) {
     if (timed) timed_end(s);
     if (e != hipSuccess) return e;
     if (timed) timed_begin(kKernelBeamJoin, s);
-    hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)a.B), dim3(kJoinThreads), 0, s, a, plan, shift, keys, sums);
+    hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)a.B), dim3(kJoinThreads), 0, s, a, plan, keys, sums);
     e = hipGetLastError();
     if (timed) timed_end(s);
     return e;

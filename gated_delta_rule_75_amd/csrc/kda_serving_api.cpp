@@ -39,6 +39,9 @@ struct Pool {
     Span span() const { return Span{p, p ? extent(n, stride, page) : 0}; }
 };
 
+// (a single page has no stride)
+Pool pool_of(const void* p, int64_t stride, int64_t page, int64_t n) { return Pool{p, n > 1 ? stride : page, page, n}; }
+
 // Whether two pools share bytes.  Pools that interleave in one buffer (equal strides) do not when
 // the pages of one lie between those of the other.
 bool overlap(const Pool& a, const Pool& b) {
@@ -183,7 +186,8 @@ int kda_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_s
     if (!sane_stride(k_page_stride) || !sane_stride(v_page_stride) || !sane_stride(k_stride) || !sane_stride(v_stride))
         return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
     const int64_t page = page_bytes_of(H_kv, page_size, d, es), row = (int64_t)H_kv * d * es;
-    const Pool kp{k_pages, k_page_stride * es, page, n_pages}, vp{v_pages, v_page_stride * es, page, n_pages};
+    const Pool kp = pool_of(k_pages, k_page_stride * es, page, n_pages);
+    const Pool vp = pool_of(v_pages, v_page_stride * es, page, n_pages);
     if (int rc = check_pages(name, kp, vp, page_size, H_kv, d, dtype)) return rc;
     if (T_total < 0 || T_total > kMaxGrid) return fail(KDA_ERR_INVALID_ARG, "%s: T_total must be in [0, 2^31)", name);
     if (!cu_seqlens && T_total != N)
@@ -242,7 +246,8 @@ int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const
     if (!sane_stride(k_page_stride) || !sane_stride(v_page_stride) || !sane_stride(q_stride))
         return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
     const int64_t page = page_bytes_of(H_kv, page_size, d, es), row = (int64_t)H_q * d * es;
-    const Pool kp{k_pages, k_page_stride * es, page, n_pages}, vp{v_pages, v_page_stride * es, page, n_pages};
+    const Pool kp = pool_of(k_pages, k_page_stride * es, page, n_pages);
+    const Pool vp = pool_of(v_pages, v_page_stride * es, page, n_pages);
     if (int rc = check_pages(name, kp, vp, page_size, H_kv, d, dtype)) return rc;
     if (H_q <= 0 || H_q % H_kv || H_q > 16384)
         return fail(KDA_ERR_INVALID_ARG, "%s: H_q must be a multiple of H_kv up to 16384", name);
@@ -250,6 +255,8 @@ int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const
     if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
         return fail(KDA_ERR_INVALID_ARG, "%s: window and sinks must be >= 0, and sinks 0 without a window", name);
     if (max_length < 0) return fail(KDA_ERR_INVALID_ARG, "%s: max_length must be >= 0", name);
+    if ((int64_t)N * H_q * ((int64_t)table_pages * page_size / 1024 + 2) > kMaxGrid)
+        return fail(KDA_ERR_INVALID_ARG, "%s: N * H_q times the table's tokens is too large", name);
     const int64_t room = (int64_t)table_pages * page_size;
     const int64_t most = max_length > 0 && max_length < room ? max_length : room;
     if (room > 0x7FFFFFFF) return fail(KDA_ERR_INVALID_ARG, "%s: table_pages * page_size must be below 2^31", name);

@@ -15,36 +15,58 @@ import ctypes
 
 import torch
 
-from . import _DT, _check, _lib, _ptr, _stream, _workspace
+from . import _DT, _check, _lib
 
-_GET_DEVICE = getattr(torch._C, "_cuda_getDevice", None)
+_T, _I32, _F32 = torch.Tensor, torch.int32, torch.float32
+_EMPTY = torch.empty
+_GET_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _MINUS_ONE = 2 ** 64 - 1
 _U8 = (torch.uint8, torch.bool)
+_LIB = None
 
 
-def _run(fn, dev, *args):
-    """Calls a library function on the current stream of `dev`, which is made the current device."""
-    if (_GET_DEVICE() if _GET_DEVICE is not None else torch.cuda.current_device()) == dev.index:
-        status = fn(*args, _stream(dev))
+def _lib_():
+    global _LIB
+    if _LIB is None:
+        _LIB = _lib.load()
+    return _LIB
+
+
+# The calls below take a few microseconds of host time, which is what the small ones cost, so each
+# tensor is tested in one expression (`_plain`: a contiguous GPU tensor of the type and device) and
+# described only when that fails (`_gpu`, `_rows`: the messages, and tensors with strides).
+def _run(fn, di, *args):
+    """Calls a library function on the current stream of device `di`, which is made the current one."""
+    if _GET_DEVICE() == di:
+        status = fn(*args, _stream_of(di))
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, _stream(dev))
+        with torch.cuda.device(di):
+            status = fn(*args, _stream_of(di))
     if status:
         _lib.check(status)
 
 
-def _gpu(t, name, dtype, dim, device=None):
-    """A GPU tensor of `dtype` and `dim` axes, with any strides."""
-    if not isinstance(t, torch.Tensor):
+def _stream_of(di):
+    return _RAW_STREAM(di) if _RAW_STREAM is not None else torch.cuda.current_stream(di).cuda_stream
+
+
+def _plain(t, dtype, di):
+    return type(t) is _T and t.dtype is dtype and t.get_device() == di and t.is_contiguous()
+
+
+def _gpu(t, name, dtype, dim, di):
+    """Raises unless t is a GPU tensor of `dtype` and `dim` axes on device `di`, with any strides."""
+    if not isinstance(t, _T):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() < 0:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != dim:
+    if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} must have {dim} axes, got {t.dim()}")
-    if device is not None and t.get_device() != device.index:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != di:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{di}")
 
 
 def _rows(t, name, shape):
@@ -59,30 +81,61 @@ def _rows(t, name, shape):
     return st[0] if shape[0] > 1 else want
 
 
-def _table(t, name, dev):
-    _gpu(t, name, torch.int32, 2, dev)
+def _row(t, name, dtype, dim, di):
+    """Elements between the rows of a tensor of `dim` axes whose rows are contiguous."""
+    if _plain(t, dtype, di) and t.dim() == dim:
+        return t.stride(0)
+    _gpu(t, name, dtype, dim, di)
     return _rows(t, name, t.shape)
 
 
-def _pools(k_pages, v_pages, dt, dev):
-    _gpu(k_pages, "k_pages", dt, 4, dev)
-    _gpu(v_pages, "v_pages", dt, 4, dev)
-    return _rows(k_pages, "k_pages", k_pages.shape), _rows(v_pages, "v_pages", k_pages.shape)
+def _vector(t, name, dtype, shape, di):
+    """Raises unless t is a contiguous GPU tensor of that type and shape (None: any of one axis)."""
+    if _plain(t, dtype, di) and (t.shape == shape if shape is not None else t.dim() == 1):
+        return
+    _gpu(t, name, dtype, 1 if shape is None else len(shape), di)
+    _check(t, name, dtype, shape, None)
 
 
-def _kind(t, name):
-    if not isinstance(t, torch.Tensor):
+def _lead(t, name):
+    """Type code and device index of the tensor that the others go by."""
+    if not isinstance(t, _T):
         raise TypeError(f"{name} must be a torch.Tensor")
     code = _DT.get(t.dtype)
     if code is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
-    return code
+    di = t.get_device()
+    if di < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return code, di
 
 
-def _scratch(nbytes, dev, workspace):
-    if nbytes == _MINUS_ONE:
-        raise _lib.KdaError(_lib.KDA_ERR_INVALID_ARG, "unsupported sizes")
-    return _workspace(nbytes, dev, workspace)
+def _table(t, name):
+    """Row stride and device index of a page table."""
+    if not isinstance(t, _T):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    di = t.get_device()
+    if di < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return _row(t, name, _I32, 2, di), di
+
+
+def _run_scratch(fn, di, workspace, size, *args):
+    """_run with the workspace's address and bytes behind args: the caller's when it is large enough (the
+    library says so), else a new one of size[0](*size[1:]) bytes."""
+    if workspace is not None:
+        _vector(workspace, "workspace", torch.uint8, None, di)
+        if _GET_DEVICE() == di:
+            status = fn(*args, workspace.data_ptr(), workspace.shape[0], _stream_of(di))
+            if status == 0:
+                return
+            if status != _lib.KDA_ERR_WORKSPACE:
+                _lib.check(status)
+    need = size[0](*size[1:])
+    if need == _MINUS_ONE:
+        need = 0  # the call says what is wrong
+    ws = _EMPTY(need, dtype=torch.uint8, device=torch.device("cuda", di)) if need else None
+    _run(fn, di, *args, ws.data_ptr() if need else None, need)
 
 
 def cache_append(k, v, k_pages, v_pages, page_table, start, *, cu_seqlens=None):
@@ -92,25 +145,26 @@ def cache_append(k, v, k_pages, v_pages, page_table, start, *, cu_seqlens=None):
     (pages of any stride), page_table int32 [N,P], start int32 [N]: the position of each sequence's first
     new token.  cu_seqlens None: one token per sequence (T = N); else int32 [N+1], packed segments.
     Positions without a page are dropped."""
-    dt = _kind(k, "k")
-    dev = k.device
-    _gpu(k, "k", k.dtype, 3)
-    _gpu(v, "v", k.dtype, 3, dev)
-    T, H, d = k.shape
-    ks, vs = _rows(k, "k", k.shape), _rows(v, "v", k.shape)
-    kps, vps = _pools(k_pages, v_pages, k.dtype, dev)
-    n_pages, _, page_size, _ = k_pages.shape
-    if k_pages.shape[1] != H or k_pages.shape[3] != d:
-        raise ValueError(f"pages of {tuple(k_pages.shape)} do not hold tokens of {tuple(k.shape)}")
-    ts = _table(page_table, "page_table", dev)
+    code, di = _lead(k, "k")
+    dt = k.dtype
+    ks, vs = _row(k, "k", dt, 3, di), _row(v, "v", dt, 3, di)
+    kps, vps = _row(k_pages, "k_pages", dt, 4, di), _row(v_pages, "v_pages", dt, 4, di)
+    shape, pages = k.shape, k_pages.shape
+    T, H, d = shape
+    n_pages, Hp, page_size, dp = pages
+    if v.shape != shape or v_pages.shape != pages or Hp != H or dp != d:
+        raise ValueError(f"k {tuple(shape)}, v {tuple(v.shape)}, k_pages {tuple(pages)} and v_pages "
+                         f"{tuple(v_pages.shape)} do not go together")
+    ts = _row(page_table, "page_table", _I32, 2, di)
     N, P = page_table.shape
-    _check(start, "start", torch.int32, (N,), dev)
-    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
-    if start is None:
-        raise TypeError("start must be a torch.Tensor")
-    _run(_lib.load().kda_cache_append, dev, k.data_ptr(), v.data_ptr(), ks, vs, _ptr(cu_seqlens), start.data_ptr(), N,
-         T, k_pages.data_ptr(), v_pages.data_ptr(), kps, vps, n_pages, page_size, page_table.data_ptr(), ts, P, H, d,
-         dt)
+    _vector(start, "start", _I32, (N,), di)
+    cu = None
+    if cu_seqlens is not None:
+        _vector(cu_seqlens, "cu_seqlens", _I32, (N + 1,), di)
+        cu = cu_seqlens.data_ptr()
+    _run(_lib_().kda_cache_append, di, k.data_ptr(), v.data_ptr(), ks, vs, cu, start.data_ptr(), N, T,
+         k_pages.data_ptr(), v_pages.data_ptr(), kps, vps, n_pages, page_size, page_table.data_ptr(), ts, P, H, d,
+         code)
 
 
 def paged_decode(q, k_pages, v_pages, page_table, lengths, *, scale=None, window=0, sinks=0, max_length=None,
@@ -123,47 +177,44 @@ def paged_decode(q, k_pages, v_pages, page_table, lengths, *, scale=None, window
     launch (P * page_size by default).
     Returns out [N,H_q,d] float32; with lse=True (or a tensor for it) (out, lse [N,H_q] float32).  A sequence
     with no visible token gives 0 and -inf."""
-    dt = _kind(q, "q")
+    code, di = _lead(q, "q")
+    dt = q.dtype
+    qs = _row(q, "q", dt, 3, di)
+    kps, vps = _row(k_pages, "k_pages", dt, 4, di), _row(v_pages, "v_pages", dt, 4, di)
+    shape, pages = q.shape, k_pages.shape
+    N, Hq, d = shape
+    n_pages, H, page_size, dp = pages
+    ts = _row(page_table, "page_table", _I32, 2, di)
+    rows, P = page_table.shape
+    if v_pages.shape != pages or dp != d or rows != N:
+        raise ValueError(f"q {tuple(shape)}, k_pages {tuple(pages)}, v_pages {tuple(v_pages.shape)} and page_table "
+                         f"{(rows, P)} do not go together")
+    _vector(lengths, "lengths", _I32, (N,), di)
     dev = q.device
-    _gpu(q, "q", q.dtype, 3)
-    N, Hq, d = q.shape
-    qs = _rows(q, "q", q.shape)
-    kps, vps = _pools(k_pages, v_pages, q.dtype, dev)
-    n_pages, H, page_size, dp = k_pages.shape
-    if dp != d:
-        raise ValueError(f"pages of {tuple(k_pages.shape)} do not go with queries of {tuple(q.shape)}")
-    ts = _table(page_table, "page_table", dev)
-    P = page_table.shape[1]
-    if page_table.shape[0] != N:
-        raise ValueError(f"page_table must have {N} rows, got {page_table.shape[0]}")
-    if lengths is None:
-        raise TypeError("lengths must be a torch.Tensor")
-    _check(lengths, "lengths", torch.int32, (N,), dev)
     if out is None:
-        out = torch.empty((N, Hq, d), dtype=torch.float32, device=dev)
+        out = _EMPTY(shape, dtype=_F32, device=dev)
     else:
-        _check(out, "out", torch.float32, (N, Hq, d), dev)
-    want = lse is not None and lse is not False
-    if not want:
-        lse = None
-    elif lse is True:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+        _vector(out, "out", _F32, shape, di)
+    if lse is None or lse is False:
+        lse = pl = None
     else:
-        _check(lse, "lse", torch.float32, (N, Hq), dev)
-    room = P * page_size
-    most = room if max_length is None or max_length > room else int(max_length)
-    if most < 0:
-        raise ValueError("max_length must be >= 0")
-    if most == 0 and room:  # 0 would mean no bound
-        most, max_length = 1, 1
-    L = _lib.load()
-    need = L.kda_paged_decode_workspace(N, Hq, H, d, dt, most, window, sinks)
-    ws = _scratch(need, dev, workspace) if need != _MINUS_ONE else None  # the call says what is wrong
-    _run(L.kda_paged_decode, dev, q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), kps, vps, n_pages,
-         page_size, page_table.data_ptr(), ts, P, lengths.data_ptr(), N, Hq, H, d, dt,
-         d ** -0.5 if scale is None else scale, window, sinks, most, out.data_ptr(), _ptr(lse), _ptr(ws),
-         need if ws is not None else 0)
-    return (out, lse) if want else out
+        if lse is True:
+            lse = _EMPTY((N, Hq), dtype=_F32, device=dev)
+        else:
+            _vector(lse, "lse", _F32, (N, Hq), di)
+        pl = lse.data_ptr()
+    most = P * page_size
+    if max_length is not None and max_length < most:
+        if max_length < 0:
+            raise ValueError("max_length must be >= 0")
+        most = max_length if max_length else 1  # 0 would mean no bound
+    L = _lib_()
+    _run_scratch(L.kda_paged_decode, di, workspace,
+                 (L.kda_paged_decode_workspace, N, Hq, H, d, code, most, window, sinks), q.data_ptr(), qs,
+                 k_pages.data_ptr(), v_pages.data_ptr(), kps, vps, n_pages, page_size, page_table.data_ptr(), ts, P,
+                 lengths.data_ptr(), N, Hq, H, d, code, d ** -0.5 if scale is None else scale, window, sinks, most,
+                 out.data_ptr(), pl)
+    return out if lse is None else (out, lse)
 
 
 def cache_fork(page_table, lengths, refcount, parents, *, table_out=None, lengths_out=None):
@@ -172,50 +223,38 @@ def cache_fork(page_table, lengths, refcount, parents, *, table_out=None, length
     reorders, keeps and drops sequences; refcount is updated in place.
 
     Returns (table_out [N_out,P], lengths_out [N_out])."""
-    _gpu(page_table, "page_table", torch.int32, 2)
-    dev = page_table.device
-    ts = _table(page_table, "page_table", dev)
+    ts, di = _table(page_table, "page_table")
     N, P = page_table.shape
-    _need(lengths=lengths, refcount=refcount, parents=parents)
-    _check(lengths, "lengths", torch.int32, (N,), dev)
-    _gpu(refcount, "refcount", torch.int32, 1, dev)
-    _check(refcount, "refcount", torch.int32, None, dev)
-    _gpu(parents, "parents", torch.int32, 1, dev)
-    _check(parents, "parents", torch.int32, None, dev)
+    _vector(lengths, "lengths", _I32, (N,), di)
+    _vector(refcount, "refcount", _I32, None, di)
+    _vector(parents, "parents", _I32, None, di)
     N_out = parents.shape[0]
+    dev = page_table.device
     if table_out is None:
-        table_out = torch.empty((N_out, P), dtype=torch.int32, device=dev)
-    os = _table(table_out, "table_out", dev)
-    if table_out.shape != (N_out, P):
-        raise ValueError(f"table_out must have shape {(N_out, P)}, got {tuple(table_out.shape)}")
+        table_out = _EMPTY((N_out, P), dtype=_I32, device=dev)
+        os = P
+    else:
+        os = _row(table_out, "table_out", _I32, 2, di)
+        if table_out.shape != (N_out, P):
+            raise ValueError(f"table_out must have shape {(N_out, P)}, got {tuple(table_out.shape)}")
     if lengths_out is None:
-        lengths_out = torch.empty(N_out, dtype=torch.int32, device=dev)
-    _check(lengths_out, "lengths_out", torch.int32, (N_out,), dev)
-    _run(_lib.load().kda_cache_fork, dev, page_table.data_ptr(), ts, lengths.data_ptr(), N, P, refcount.data_ptr(),
+        lengths_out = _EMPTY(N_out, dtype=_I32, device=dev)
+    else:
+        _vector(lengths_out, "lengths_out", _I32, (N_out,), di)
+    _run(_lib_().kda_cache_fork, di, page_table.data_ptr(), ts, lengths.data_ptr(), N, P, refcount.data_ptr(),
          refcount.shape[0], parents.data_ptr(), N_out, table_out.data_ptr(), os, lengths_out.data_ptr())
     return table_out, lengths_out
-
-
-def _need(**tensors):
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
 
 
 def cache_free(page_table, lengths, refcount, rows):
     """Drops sequences in place: the pages of every row in rows (int32 [R]) lose one reference, its entries
     become -1 and its length 0.  Rows outside the table are left out; one named twice is freed once."""
-    _gpu(page_table, "page_table", torch.int32, 2)
-    dev = page_table.device
-    ts = _table(page_table, "page_table", dev)
+    ts, di = _table(page_table, "page_table")
     N, P = page_table.shape
-    _need(lengths=lengths, refcount=refcount, rows=rows)
-    _check(lengths, "lengths", torch.int32, (N,), dev)
-    _gpu(refcount, "refcount", torch.int32, 1, dev)
-    _check(refcount, "refcount", torch.int32, None, dev)
-    _gpu(rows, "rows", torch.int32, 1, dev)
-    _check(rows, "rows", torch.int32, None, dev)
-    _run(_lib.load().kda_cache_free, dev, page_table.data_ptr(), ts, lengths.data_ptr(), N, P, refcount.data_ptr(),
+    _vector(lengths, "lengths", _I32, (N,), di)
+    _vector(refcount, "refcount", _I32, None, di)
+    _vector(rows, "rows", _I32, None, di)
+    _run(_lib_().kda_cache_free, di, page_table.data_ptr(), ts, lengths.data_ptr(), N, P, refcount.data_ptr(),
          refcount.shape[0], rows.data_ptr(), rows.shape[0])
 
 
@@ -227,26 +266,24 @@ def cache_reserve(page_table, lengths, refcount, new_tokens, page_size, *, copie
     Returns (copies int32 [N,2], granted int32 [N]).  copies: the page pair (old, new) that pages_copy has to
     copy for a sequence whose shared page was partly filled, else (-1, -1).  granted: new_tokens[n], or 0 for
     a sequence that was left as it was because pages (or table columns) ran out; lengths grow by it."""
-    _gpu(page_table, "page_table", torch.int32, 2)
-    dev = page_table.device
-    ts = _table(page_table, "page_table", dev)
+    ts, di = _table(page_table, "page_table")
     N, P = page_table.shape
-    _need(lengths=lengths, refcount=refcount, new_tokens=new_tokens)
-    _check(lengths, "lengths", torch.int32, (N,), dev)
-    _gpu(refcount, "refcount", torch.int32, 1, dev)
-    _check(refcount, "refcount", torch.int32, None, dev)
-    _check(new_tokens, "new_tokens", torch.int32, (N,), dev)
+    _vector(lengths, "lengths", _I32, (N,), di)
+    _vector(refcount, "refcount", _I32, None, di)
+    _vector(new_tokens, "new_tokens", _I32, (N,), di)
+    dev = page_table.device
     if copies is None:
-        copies = torch.empty((N, 2), dtype=torch.int32, device=dev)
-    _check(copies, "copies", torch.int32, (N, 2), dev)
+        copies = _EMPTY((N, 2), dtype=_I32, device=dev)
+    else:
+        _vector(copies, "copies", _I32, (N, 2), di)
     if granted is None:
-        granted = torch.empty(N, dtype=torch.int32, device=dev)
-    _check(granted, "granted", torch.int32, (N,), dev)
-    L = _lib.load()
-    need = L.kda_cache_workspace_size(N, refcount.shape[0])
-    ws = _scratch(need, dev, workspace)
-    _run(L.kda_cache_reserve, dev, page_table.data_ptr(), ts, lengths.data_ptr(), N, P, refcount.data_ptr(),
-         refcount.shape[0], page_size, new_tokens.data_ptr(), copies.data_ptr(), granted.data_ptr(), _ptr(ws), need)
+        granted = _EMPTY(N, dtype=_I32, device=dev)
+    else:
+        _vector(granted, "granted", _I32, (N,), di)
+    L, n_pages = _lib_(), refcount.shape[0]
+    _run_scratch(L.kda_cache_reserve, di, workspace, (L.kda_cache_workspace_size, N, n_pages), page_table.data_ptr(),
+                 ts, lengths.data_ptr(), N, P, refcount.data_ptr(), n_pages, page_size, new_tokens.data_ptr(),
+                 copies.data_ptr(), granted.data_ptr())
     return copies, granted
 
 
@@ -255,35 +292,31 @@ def cache_compact(page_table, refcount, *, table_out=None, refcount_out=None, mo
 
     Returns (table_out, refcount_out, moves int32 [n_pages // 2, 2]); table_out and refcount_out may be given
     as page_table and refcount themselves.  The pages are moved by pages_copy(pools, moves)."""
-    _gpu(page_table, "page_table", torch.int32, 2)
-    dev = page_table.device
-    ts = _table(page_table, "page_table", dev)
+    ts, di = _table(page_table, "page_table")
     N, P = page_table.shape
-    _need(refcount=refcount)
-    _gpu(refcount, "refcount", torch.int32, 1, dev)
-    _check(refcount, "refcount", torch.int32, None, dev)
+    _vector(refcount, "refcount", _I32, None, di)
     n_pages = refcount.shape[0]
+    dev = page_table.device
     if table_out is None:
-        table_out = torch.empty((N, P), dtype=torch.int32, device=dev)
-    os = _table(table_out, "table_out", dev)
-    if table_out.shape != (N, P):
-        raise ValueError(f"table_out must have shape {(N, P)}, got {tuple(table_out.shape)}")
+        table_out = _EMPTY((N, P), dtype=_I32, device=dev)
+        os = P
+    else:
+        os = _row(table_out, "table_out", _I32, 2, di)
+        if table_out.shape != (N, P):
+            raise ValueError(f"table_out must have shape {(N, P)}, got {tuple(table_out.shape)}")
     if refcount_out is None:
-        refcount_out = torch.empty(n_pages, dtype=torch.int32, device=dev)
-    _check(refcount_out, "refcount_out", torch.int32, (n_pages,), dev)
+        refcount_out = _EMPTY(n_pages, dtype=_I32, device=dev)
+    else:
+        _vector(refcount_out, "refcount_out", _I32, (n_pages,), di)
     if moves is None:
-        moves = torch.empty((n_pages // 2, 2), dtype=torch.int32, device=dev)
-    _check(moves, "moves", torch.int32, (n_pages // 2, 2), dev)
-    L = _lib.load()
-    need = L.kda_cache_workspace_size(N, n_pages)
-    ws = _scratch(need, dev, workspace)
-    _run(L.kda_cache_compact, dev, page_table.data_ptr(), ts, N, P, refcount.data_ptr(), n_pages, table_out.data_ptr(),
-         os, refcount_out.data_ptr(), moves.data_ptr(), _ptr(ws), need)
+        moves = _EMPTY((n_pages // 2, 2), dtype=_I32, device=dev)
+    else:
+        _vector(moves, "moves", _I32, (n_pages // 2, 2), di)
+    L = _lib_()
+    _run_scratch(L.kda_cache_compact, di, workspace, (L.kda_cache_workspace_size, N, n_pages), page_table.data_ptr(),
+                 ts, N, P, refcount.data_ptr(), n_pages, table_out.data_ptr(), os, refcount_out.data_ptr(),
+                 moves.data_ptr())
     return table_out, refcount_out, moves
-
-
-def _list_of(x, name):
-    return [x] if isinstance(x, torch.Tensor) else list(x)
 
 
 def pages_copy(pools, pairs):
@@ -293,25 +326,32 @@ def pages_copy(pools, pairs):
 
     pools: a tensor [n_pages, ...] or a list of them (any dtypes and sizes, the same n_pages; pages
     contiguous, of any stride), for instance key and value pages, or recurrent states [n_pages,H,dk,dv]."""
-    pools = _list_of(pools, "pools")
-    _need(pairs=pairs)
-    if not pools:
+    if isinstance(pools, _T):
+        pools = (pools,)
+    n = len(pools)
+    if n == 0:
         return
-    _need(**{f"pools[{i}]": t for i, t in enumerate(pools)})
-    dev = pools[0].device
-    _gpu(pairs, "pairs", torch.int32, 2, dev)
-    _check(pairs, "pairs", torch.int32, (pairs.shape[0], 2), dev)
-    n, n_pages = len(pools), pools[0].shape[0] if pools[0].dim() else 0
-    base, stride, size = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int64 * n)()
+    if not isinstance(pools[0], _T):
+        raise TypeError("pools[0] must be a torch.Tensor")
+    di = pools[0].get_device()
+    if di < 0:
+        raise ValueError("pools[0] must be a GPU tensor")
+    _vector(pairs, "pairs", _I32, (pairs.shape[0] if isinstance(pairs, _T) and pairs.dim() else 0, 2), di)
+    base, stride, size, n_pages = [], [], [], pools[0].shape[0] if pools[0].dim() else 0
     for i, t in enumerate(pools):
-        _gpu(t, f"pools[{i}]", t.dtype, t.dim(), dev)
-        if t.dim() < 2 or t.shape[0] != n_pages:
+        if not (type(t) is _T and t.get_device() == di and t.is_contiguous() and t.dim() > 1):
+            _gpu(t, f"pools[{i}]", getattr(t, "dtype", None), None, di)
+            if t.dim() < 2:
+                raise ValueError(f"pools[{i}] must be [{n_pages}, ...], got {tuple(t.shape)}")
+        if t.shape[0] != n_pages:
             raise ValueError(f"pools[{i}] must be [{n_pages}, ...], got {tuple(t.shape)}")
         es = t.element_size()
-        row = _rows(t, f"pools[{i}]", t.shape)
-        base[i], stride[i] = t.data_ptr(), row * es
-        size[i] = t[0].numel() * es if n_pages else 0
-    _run(_lib.load().kda_pages_copy, dev, base, stride, size, n, n_pages, pairs.data_ptr(), pairs.shape[0])
+        row = t.numel() // n_pages * es if n_pages else 0
+        base.append(t.data_ptr())
+        size.append(row)
+        stride.append(row if t.is_contiguous() else _rows(t, f"pools[{i}]", t.shape) * es)
+    _run(_lib_().kda_pages_copy, di, (ctypes.c_void_p * n)(*base), (ctypes.c_int64 * n)(*stride),
+         (ctypes.c_int64 * n)(*size), n, n_pages, pairs.data_ptr(), pairs.shape[0])
 
 
 def beam_select(logits, scores, *, n_out=None, finished=None, eos=-1, workspace=None):
@@ -322,34 +362,36 @@ def beam_select(logits, scores, *, n_out=None, finished=None, eos=-1, workspace=
     finished uint8 or bool [B,K]: such a beam goes on with `eos` alone at its own score.
     Returns (scores [B,n_out] float32 descending, parents int32 [B,n_out], tokens int32 [B,n_out],
     finished [B,n_out] or None).  Ties go to the lower beam and token; NaN logits count as -inf."""
-    dt = _kind(logits, "logits")
-    dev = logits.device
-    _gpu(logits, "logits", logits.dtype, 3)
+    code, di = _lead(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError(f"logits must have 3 axes, got {logits.dim()}")
     B, K, V = logits.shape
-    st = logits.stride()
-    row = st[1] if K > 1 else st[0] if B > 1 else V
-    if (V > 1 and st[2] != 1) or (K > 1 and B > 1 and st[0] != K * st[1]):
-        raise ValueError(f"logits must have contiguous rows of one stride, got strides {st}")
-    _need(scores=scores)
-    _check(scores, "scores", torch.float32, (B, K), dev)
+    if logits.is_contiguous():
+        row = V
+    else:
+        st = logits.stride()
+        row = st[1] if K > 1 else st[0] if B > 1 else V
+        if (V > 1 and st[2] != 1) or (K > 1 and B > 1 and st[0] != K * st[1]):
+            raise ValueError(f"logits must have contiguous rows of one stride, got strides {st}")
+    _vector(scores, "scores", _F32, (B, K), di)
     if n_out is None:
         n_out = K
-    over = None
+    if n_out < 0:
+        raise ValueError("n_out must be positive")
+    L = _lib_()
+    dev = logits.device
+    over = pf = po = None
     if finished is not None:
-        if not isinstance(finished, torch.Tensor) or finished.dtype not in _U8:
+        if not isinstance(finished, _T) or finished.dtype not in _U8:
             raise ValueError("finished must be a uint8 or bool tensor")
-        _check(finished, "finished", finished.dtype, (B, K), dev)
-        over = torch.empty((B, n_out), dtype=finished.dtype, device=dev)
-    L = _lib.load()
-    need = L.kda_beam_select_workspace(B, K, V, n_out)
-    if need == _MINUS_ONE:
-        raise _lib.KdaError(_lib.KDA_ERR_INVALID_ARG, f"kda_beam_select: unsupported B={B} K={K} V={V} n_out={n_out}")
-    ws = _scratch(need, dev, workspace)
-    best = torch.empty((B, n_out), dtype=torch.float32, device=dev)
-    parents = torch.empty((B, n_out), dtype=torch.int32, device=dev)
-    tokens = torch.empty((B, n_out), dtype=torch.int32, device=dev)
-    _run(L.kda_beam_select, dev, logits.data_ptr(), row, scores.data_ptr(), _ptr(finished), B, K, V, n_out, eos, dt,
-         best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), _ptr(over), _ptr(ws), need)
+        _vector(finished, "finished", finished.dtype, (B, K), di)
+        over = _EMPTY((B, n_out), dtype=finished.dtype, device=dev)
+        pf, po = finished.data_ptr(), over.data_ptr()
+    best = _EMPTY((B, n_out), dtype=_F32, device=dev)
+    parents, tokens = _EMPTY((2, B, n_out), dtype=_I32, device=dev).unbind()
+    _run_scratch(L.kda_beam_select, di, workspace, (L.kda_beam_select_workspace, B, K, V, n_out), logits.data_ptr(),
+                 row, scores.data_ptr(), pf, B, K, V, n_out, eos, code, best.data_ptr(), parents.data_ptr(),
+                 tokens.data_ptr(), po)
     return best, parents, tokens, over
 
 
@@ -359,20 +401,29 @@ def beam_reorder(states, parents):
 
     states: a contiguous tensor [B*K, ...] or a list of them (the layers' recurrent states, for instance
     [B*K,H,dk,dv])."""
-    states = _list_of(states, "states")
-    _need(parents=parents)
-    if not states:
-        return
-    _need(**{f"states[{i}]": t for i, t in enumerate(states)})
-    dev = states[0].device
-    _gpu(parents, "parents", torch.int32, 2, dev)
-    _check(parents, "parents", torch.int32, None, dev)
-    B, K = parents.shape
+    if isinstance(states, _T):
+        states = (states,)
     n = len(states)
-    base, size = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
+    if n == 0:
+        return
+    if not isinstance(states[0], _T):
+        raise TypeError("states[0] must be a torch.Tensor")
+    di = states[0].get_device()
+    if di < 0:
+        raise ValueError("states[0] must be a GPU tensor")
+    if not (_plain(parents, _I32, di) and parents.dim() == 2):
+        _gpu(parents, "parents", _I32, 2, di)
+        _check(parents, "parents", _I32)
+    B, K = parents.shape
+    rows = B * K
+    base, size = [], []
     for i, t in enumerate(states):
-        _check(t, f"states[{i}]", None, None, dev)
-        if t.dim() < 1 or t.shape[0] != B * K:
-            raise ValueError(f"states[{i}] must be [{B * K}, ...], got {tuple(t.shape)}")
-        base[i], size[i] = t.data_ptr(), (t.numel() // (B * K)) * t.element_size() if B * K else 0
-    _run(_lib.load().kda_beam_reorder, dev, base, size, n, parents.data_ptr(), B, K)
+        if not (type(t) is _T and t.get_device() == di and t.is_contiguous()):
+            _gpu(t, f"states[{i}]", getattr(t, "dtype", None), None, di)
+            _check(t, f"states[{i}]")
+        if t.dim() < 1 or t.shape[0] != rows:
+            raise ValueError(f"states[{i}] must be [{rows}, ...], got {tuple(t.shape)}")
+        base.append(t.data_ptr())
+        size.append(t.numel() // rows * t.element_size() if rows else 0)
+    _run(_lib_().kda_beam_reorder, di, (ctypes.c_void_p * n)(*base), (ctypes.c_int64 * n)(*size), n,
+         parents.data_ptr(), B, K)

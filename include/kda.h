@@ -494,7 +494,7 @@ int kda_pages_copy(void* const* pools, const int64_t* page_strides, const int64_
  *   scores     [B, K] float, the beams' sums of log-probabilities so far (-inf: a
  *              beam that does not take part yet)
  *   finished   uint8 [B, K] or NULL.  A beam with finished != 0 goes on with token
- *              `eos` alone, at its own score; its logits are not read.
+ *              `eos` alone, at its own score; its logits are not used.
  *   scores_out, parents, tokens  [B, n_out] float, int32, int32: the chosen c in
  *              descending order, the beam k it continues (0 .. K-1) and its token
  *   finished_out  uint8 [B, n_out], with finished only: the parent was finished, or
