@@ -82,8 +82,10 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(CacheAppendArgs 
         const int64_t at = (int64_t)(r >> vph_shift) * head_bytes + (r & vmask) * 16;
         const u32x4 kv = *reinterpret_cast<const u32x4*>(ks + t * kst + (int64_t)r * 16);
         const u32x4 vv = *reinterpret_cast<const u32x4*>(vs + t * vst + (int64_t)r * 16);
-        *reinterpret_cast<u32x4*>(static_cast<char*>(a.kp) + ko + at) = kv;
-        *reinterpret_cast<u32x4*>(static_cast<char*>(a.vp) + vo + at) = vv;
+        // past the caches: 5.4 against 5.1 TB/s for 131072 tokens of 8 heads (loads past them: 5.5, but 4.5
+        // against 5.1 for a call that fits them)
+        __builtin_nontemporal_store(kv, reinterpret_cast<u32x4*>(static_cast<char*>(a.kp) + ko + at));
+        __builtin_nontemporal_store(vv, reinterpret_cast<u32x4*>(static_cast<char*>(a.vp) + vo + at));
     }
 }
 
@@ -256,6 +258,61 @@ __device__ __forceinline__ int32_t bits_before(const CacheWs& w, const int32_t* 
 
 __device__ __forceinline__ bool bit_of(const CacheWs& w, int32_t p) { return (w.bits[p >> 6] >> (p & 63)) & 1; }
 
+// The scan of a small pool by one workgroup, in LDS.
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallBlocks = 2, kSmallPages = kSmallBlocks * kBlockPages;
+constexpr int kSmallRows = 32;        // sequences of a small reserve: two per wave
+constexpr int kSmallEntries = 16384;  // table entries of a small compaction: sixteen per thread
+struct SmallScan {
+    uint64_t bits[kSmallBlocks * kBlockWords];
+    uint32_t before[kSmallBlocks * kBlockWords];
+    int32_t block[kSmallBlocks];
+    int32_t prefix[kSmallBlocks + 1];
+    int32_t aux[kSmallPages / 2];
+};
+
+// Every thread of the workgroup; a barrier has to follow before anything but `bits` of its own wave is
+// read.
+template <bool FREE>
+__device__ __forceinline__ CacheWs small_scan(const int32_t* refs, int n_pages, SmallScan& s) {
+    constexpr int kWords = kSmallBlocks * kBlockWords, kPer = kWords / (kSmallThreads / 64);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    CacheWs w{s.bits, s.before, s.block, s.aux, kWords, kSmallBlocks};
+    int32_t r[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int p = (i * (kSmallThreads / 64) + wave) * 64 + lane;
+        r[i] = p < n_pages ? refs[p] : (FREE ? 1 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const uint64_t m = __ballot(FREE ? r[i] <= 0 : r[i] > 0);
+        if (lane == 0) s.bits[i * (kSmallThreads / 64) + wave] = m;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        int32_t carry = 0;
+        for (int b = 0; b < kSmallBlocks; ++b) {
+            const uint32_t own = __popcll(s.bits[b * kBlockWords + lane]);
+            uint32_t x = own;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const uint32_t y = __shfl_up(x, off, 64);
+                if (lane >= off) x += y;
+            }
+            s.before[b * kBlockWords + lane] = x - own;
+            const int32_t total = __shfl((int32_t)x, 63, 64);
+            if (lane == 0) {
+                s.block[b] = total;
+                s.prefix[b] = carry;
+                s.prefix[b + 1] = carry + total;
+            }
+            carry += total;
+        }
+    }
+    return w;
+}
+
 // ------------------------------------------------------------------------------------------
 // reserve
 // ------------------------------------------------------------------------------------------
@@ -285,15 +342,9 @@ __device__ __forceinline__ Span64 new_columns(int32_t len, int32_t add, int page
     return s;
 }
 
-__global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserveArgs a) {
-    const CacheWs w = cache_ws(a.ws, a.n_pages);
-    if ((int)blockIdx.x < w.blocks) {
-        scan_block<true>(a.refs, a.n_pages, w, blockIdx.x);
-        return;
-    }
+// pages that sequence n needs, marked in its row; -1 where the row is too narrow (one wave)
+__device__ __forceinline__ int32_t count_need(const CacheReserveArgs& a, int64_t n) {
     const int lane = threadIdx.x & 63;
-    const int64_t n = (int64_t)(blockIdx.x - w.blocks) * kRowsPerGroup + (threadIdx.x >> 6);
-    if (n >= a.N) return;
     const Span64 s = new_columns(a.lengths[n], a.new_tokens[n], a.page_size, a.width);
     int32_t need = 0;
     if (!s.none)
@@ -309,29 +360,14 @@ __global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserve
             }
             need += __popcll(__ballot(want));
         }
-    if (lane == 0) w.aux[n] = s.bad ? -1 : need;
+    return s.bad ? -1 : need;
 }
 
-// Second launch: one wave per sequence.  Its first page is the free one whose rank is the sum of the
-// needs before it; a sequence that is not served gets its marks taken back.
-__global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs a) {
-    __shared__ int32_t s_prefix[kMaxBlocks + 1];
-    __shared__ int64_t s_sum[kRowsPerGroup];
-    const CacheWs w = cache_ws(a.ws, a.n_pages);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n0 = (int64_t)blockIdx.x * kRowsPerGroup, n = n0 + wave;
-    // pages needed by the sequences before this group
-    int64_t sum = 0;
-    for (int64_t i = threadIdx.x; i < n0; i += kScanThreads) sum += w.aux[i] > 0 ? w.aux[i] : 0;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    if (lane == 0) s_sum[wave] = sum;
-    block_prefix(w, s_prefix);  // ends with a barrier
-    if (n >= a.N) return;
-    int64_t base = 0;
-    for (int i = 0; i < kRowsPerGroup; ++i) base += s_sum[i];
-    for (int i = 0; i < wave; ++i) base += w.aux[n0 + i] > 0 ? w.aux[n0 + i] : 0;
-    const int32_t need = w.aux[n], len = a.lengths[n], add = a.new_tokens[n];
+// hands out the pages to sequence n, whose first has rank `base` among the free ones (one wave)
+__device__ __forceinline__ void take_pages(const CacheReserveArgs& a, const CacheWs& w, const int32_t* s_prefix,
+                                           int64_t n, int32_t need, int64_t base) {
+    const int lane = threadIdx.x & 63;
+    const int32_t len = a.lengths[n], add = a.new_tokens[n];
     const Span64 s = new_columns(len, add, a.page_size, a.width);
     const bool served = add > 0 && need >= 0 && base + need <= s_prefix[w.blocks];
     int32_t from = -1, to = -1;
@@ -369,6 +405,60 @@ __global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs 
     }
 }
 
+__global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserveArgs a) {
+    const CacheWs w = cache_ws(a.ws, a.n_pages);
+    if ((int)blockIdx.x < w.blocks) {
+        scan_block<true>(a.refs, a.n_pages, w, blockIdx.x);
+        return;
+    }
+    const int64_t n = (int64_t)(blockIdx.x - w.blocks) * kRowsPerGroup + (threadIdx.x >> 6);
+    if (n >= a.N) return;
+    const int32_t need = count_need(a, n);
+    if ((threadIdx.x & 63) == 0) w.aux[n] = need;
+}
+
+// Second launch: one wave per sequence.  Its first page is the free one whose rank is the sum of the
+// needs before it; a sequence that is not served gets its marks taken back.
+__global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs a) {
+    __shared__ int32_t s_prefix[kMaxBlocks + 1];
+    __shared__ int64_t s_sum[kRowsPerGroup];
+    const CacheWs w = cache_ws(a.ws, a.n_pages);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n0 = (int64_t)blockIdx.x * kRowsPerGroup, n = n0 + wave;
+    // pages needed by the sequences before this group
+    int64_t sum = 0;
+    for (int64_t i = threadIdx.x; i < n0; i += kScanThreads) sum += w.aux[i] > 0 ? w.aux[i] : 0;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    if (lane == 0) s_sum[wave] = sum;
+    block_prefix(w, s_prefix);  // ends with a barrier
+    if (n >= a.N) return;
+    int64_t base = 0;
+    for (int i = 0; i < kRowsPerGroup; ++i) base += s_sum[i];
+    for (int i = 0; i < wave; ++i) base += w.aux[n0 + i] > 0 ? w.aux[n0 + i] : 0;
+    take_pages(a, w, s_prefix, n, w.aux[n], base);
+}
+
+// Small pools and few sequences: both steps in one workgroup, with the scan in LDS.  It does not run
+// faster than the two launches (about 10 us each way for 32 sequences), but the second one costs its
+// caller 2.5 us, which is what bounds a small call.
+__global__ __launch_bounds__(kSmallThreads) void reserve_small_kernel(CacheReserveArgs a) {
+    __shared__ SmallScan s;
+    __shared__ int32_t s_need[kSmallRows];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const CacheWs w = small_scan<true>(a.refs, a.n_pages, s);
+    for (int n = wave; n < a.N; n += kSmallThreads / 64) {
+        const int32_t need = count_need(a, n);
+        if (lane == 0) s_need[n] = need;
+    }
+    __syncthreads();  // the scan too, and every look at a count before the first change
+    for (int n = wave; n < a.N; n += kSmallThreads / 64) {
+        int64_t base = 0;
+        for (int i = 0; i < n; ++i) base += s_need[i] > 0 ? s_need[i] : 0;
+        take_pages(a, w, s.prefix, n, s_need[n], base);
+    }
+}
+
 // ------------------------------------------------------------------------------------------
 // compact
 // ------------------------------------------------------------------------------------------
@@ -379,28 +469,46 @@ __global__ __launch_bounds__(kScanThreads) void compact_scan_kernel(CacheCompact
     scan_block<false>(a.refs, a.pt.n_pages, cache_ws(a.ws, a.pt.n_pages), blockIdx.x);
 }
 
+// page p's part in the moves (pages before p, and before the number L of used pages: `front`)
+__device__ __forceinline__ void plan_page(const CacheCompactArgs& a, const CacheWs& w, const int32_t* s_prefix, int p,
+                                          int32_t L, int32_t front) {
+    const bool used = bit_of(w, p);
+    if (used != (p < L)) {
+        const int32_t before = bits_before(w, s_prefix, p);
+        if (!used) {
+            a.moves[2 * (int64_t)(p - before) + 1] = p;
+        } else {
+            a.moves[2 * (int64_t)(before - front)] = p;
+            w.aux[before - front] = a.refs[p];
+        }
+    }
+    if (p < a.pt.n_pages / 2 && p >= L - front) {
+        a.moves[2 * (int64_t)p] = -1;
+        a.moves[2 * (int64_t)p + 1] = -1;
+    }
+}
+
+__device__ __forceinline__ void remap_count(const CacheCompactArgs& a, const CacheWs& w, const int32_t* s_prefix, int p,
+                                            int32_t L) {
+    int32_t r = 0;
+    if (p < L) r = bit_of(w, p) ? a.refs[p] : w.aux[p - bits_before(w, s_prefix, p)];
+    a.refs_out[p] = r;
+}
+
+__device__ __forceinline__ void remap_entry(const CacheCompactArgs& a, const CacheWs& w, const int32_t* s_prefix,
+                                            int64_t row, int j, int32_t L, int32_t front) {
+    int32_t e = a.pt.table[row * a.pt.stride + j];
+    if (e >= L && e < a.pt.n_pages && bit_of(w, e)) e = a.moves[2 * (int64_t)(bits_before(w, s_prefix, e) - front) + 1];
+    a.table_out[row * a.out_stride + j] = e;
+}
+
 __global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(CacheCompactArgs a) {
     __shared__ int32_t s_prefix[kMaxBlocks + 1];
     const CacheWs w = cache_ws(a.ws, a.pt.n_pages);
     block_prefix(w, s_prefix);
-    const int32_t L = s_prefix[w.blocks], front = bits_before(w, s_prefix, L), count = L - front;
+    const int32_t L = s_prefix[w.blocks], front = bits_before(w, s_prefix, L);
     const int p = blockIdx.x * kScanThreads + threadIdx.x;
-    if (p < a.pt.n_pages) {
-        const bool used = bit_of(w, p);
-        if (used != (p < L)) {
-            const int32_t before = bits_before(w, s_prefix, p);
-            if (!used) {
-                a.moves[2 * (int64_t)(p - before) + 1] = p;
-            } else {
-                a.moves[2 * (int64_t)(before - front)] = p;
-                w.aux[before - front] = a.refs[p];
-            }
-        }
-    }
-    if (p < a.pt.n_pages / 2 && p >= count) {
-        a.moves[2 * (int64_t)p] = -1;
-        a.moves[2 * (int64_t)p + 1] = -1;
-    }
+    if (p < a.pt.n_pages) plan_page(a, w, s_prefix, p, L, front);
 }
 
 __global__ __launch_bounds__(kScanThreads) void compact_remap_kernel(CacheCompactArgs a, int count_groups,
@@ -411,21 +519,26 @@ __global__ __launch_bounds__(kScanThreads) void compact_remap_kernel(CacheCompac
     const int32_t L = s_prefix[w.blocks];
     if ((int)blockIdx.x < count_groups) {
         const int p = blockIdx.x * kScanThreads + threadIdx.x;
-        if (p < a.pt.n_pages) {
-            int32_t r = 0;
-            if (p < L) r = bit_of(w, p) ? a.refs[p] : w.aux[p - bits_before(w, s_prefix, p)];
-            a.refs_out[p] = r;
-        }
+        if (p < a.pt.n_pages) remap_count(a, w, s_prefix, p, L);
         return;
     }
     const int g = blockIdx.x - count_groups;
-    const int64_t row = g / col_groups;
     const int j = (g % col_groups) * kScanThreads + threadIdx.x;
-    if (j >= a.pt.width) return;
-    int32_t e = a.pt.table[row * a.pt.stride + j];
-    if (e >= L && e < a.pt.n_pages && bit_of(w, e))
-        e = a.moves[2 * (int64_t)(bits_before(w, s_prefix, e) - bits_before(w, s_prefix, L)) + 1];
-    a.table_out[row * a.out_stride + j] = e;
+    if (j < a.pt.width) remap_entry(a, w, s_prefix, g / col_groups, j, L, bits_before(w, s_prefix, L));
+}
+
+// Small pools and tables: the three steps in one workgroup, with the scan in LDS.
+__global__ __launch_bounds__(kSmallThreads) void compact_small_kernel(CacheCompactArgs a) {
+    __shared__ SmallScan s;
+    const CacheWs w = small_scan<false>(a.refs, a.pt.n_pages, s);
+    __syncthreads();
+    const int32_t L = s.prefix[w.blocks], front = bits_before(w, s.prefix, L);
+    for (int p = threadIdx.x; p < a.pt.n_pages; p += kSmallThreads) plan_page(a, w, s.prefix, p, L, front);
+    __syncthreads();  // `aux`, and the moves, which no thread has read before
+    for (int p = threadIdx.x; p < a.pt.n_pages; p += kSmallThreads) remap_count(a, w, s.prefix, p, L);
+    const int entries = (int)a.N * a.pt.width;
+    for (int i = threadIdx.x; i < entries; i += kSmallThreads)
+        remap_entry(a, w, s.prefix, i / a.pt.width, i % a.pt.width, L, front);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -436,7 +549,8 @@ __global__ __launch_bounds__(kScanThreads) void compact_remap_kernel(CacheCompac
 // of 64 of its workgroup's items at once and steps over the ones without a page.
 constexpr int kCopyThreads = 256;
 constexpr int64_t kCopyPiece = 32768;
-constexpr int kCopyGroups = 2048;
+constexpr int kCopyGroups = 8192;
+constexpr int kCopyUnroll = 8;  // 16-byte vectors of a thread in flight
 
 __global__ __launch_bounds__(kCopyThreads) void pages_copy_kernel(PoolList pl, int n_pages, const int32_t* pairs,
                                                                   int64_t n_pairs, int pieces, int64_t items) {
@@ -464,17 +578,17 @@ __global__ __launch_bounds__(kCopyThreads) void pages_copy_kernel(PoolList pl, i
             const int vecs = (int)((left < kCopyPiece ? left : kCopyPiece) >> 4);
             const u32x4* s = reinterpret_cast<const u32x4*>(pl.base[pool] + __shfl(src, l, 64) * pl.stride[pool] + off);
             u32x4* d = reinterpret_cast<u32x4*>(pl.base[pool] + __shfl(dst, l, 64) * pl.stride[pool] + off);
-            for (int v0 = 0; v0 < vecs; v0 += 4 * kCopyThreads) {
-                u32x4 x[4];
+            for (int v0 = 0; v0 < vecs; v0 += kCopyUnroll * kCopyThreads) {
+                u32x4 x[kCopyUnroll];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kCopyUnroll; ++i) {
                     const int v = v0 + i * kCopyThreads + threadIdx.x;
                     if (v < vecs) x[i] = s[v];
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kCopyUnroll; ++i) {
                     const int v = v0 + i * kCopyThreads + threadIdx.x;
-                    if (v < vecs) d[v] = x[i];
+                    if (v < vecs) __builtin_nontemporal_store(x[i], d + v);
                 }
             }
         }
@@ -538,6 +652,10 @@ size_t cache_workspace(int64_t N, int64_t n_pages) {
 
 hipError_t launch_cache_reserve(const CacheReserveArgs& a, hipStream_t s) {
     if (a.N == 0) return hipSuccess;
+    if (a.n_pages <= kSmallPages && a.N <= kSmallRows)
+        return timed_launch(kKernelCacheReserve, s, [&] {
+            hipLaunchKernelGGL(reserve_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, a);
+        });
     const int64_t blocks = div_up(a.n_pages, kBlockPages), groups = div_up(a.N, kRowsPerGroup);
     hipError_t e = timed_launch(kKernelCacheScan, s, [&] {
         hipLaunchKernelGGL(reserve_scan_kernel, dim3((unsigned)(blocks + groups)), dim3(kScanThreads), 0, s, a);
@@ -551,13 +669,14 @@ hipError_t launch_cache_reserve(const CacheReserveArgs& a, hipStream_t s) {
 hipError_t launch_cache_compact(const CacheCompactArgs& a, hipStream_t s) {
     const int64_t blocks = div_up(a.pt.n_pages, kBlockPages), groups = div_up(a.pt.n_pages, kScanThreads);
     const int64_t cols = div_up(a.pt.width, kScanThreads);
-    if (groups + a.N * cols == 0) return hipSuccess;
-    hipError_t e = hipSuccess;
-    if (blocks)
-        e = timed_launch(kKernelCacheScan, s, [&] {
-            hipLaunchKernelGGL(compact_scan_kernel, dim3((unsigned)blocks), dim3(kScanThreads), 0, s, a);
+    if (a.pt.n_pages <= kSmallPages && a.N * a.pt.width <= kSmallEntries)
+        return timed_launch(kKernelCachePlan, s, [&] {
+            hipLaunchKernelGGL(compact_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, a);
         });
-    if (e == hipSuccess && groups)
+    hipError_t e = timed_launch(kKernelCacheScan, s, [&] {
+        hipLaunchKernelGGL(compact_scan_kernel, dim3((unsigned)blocks), dim3(kScanThreads), 0, s, a);
+    });
+    if (e == hipSuccess)
         e = timed_launch(kKernelCachePlan, s, [&] {
             hipLaunchKernelGGL(compact_plan_kernel, dim3((unsigned)groups), dim3(kScanThreads), 0, s, a);
         });

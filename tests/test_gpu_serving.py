@@ -411,7 +411,8 @@ def random_tables(rng, n, width, n_pages, page, share=0.4):
 
 
 @pytest.mark.parametrize("seed,n,width,n_pages,page", [(1, 5, 4, 40, 16), (2, 70, 9, 300, 16), (3, 33, 300, 9000, 48),
-                                                       (4, 1, 1, 2, 64), (5, 20, 6, 60, 32), (6, 300, 70, 20000, 16)])
+                                                       (4, 1, 1, 2, 64), (5, 20, 6, 60, 32), (6, 300, 70, 20000, 16),
+                                                       (7, 12, 40, 8192, 16), (8, 12, 40, 8193, 16)])
 def test_fork_reserve_free_match_a_plain_cache(seed, n, width, n_pages, page):
     """A life of a cache: forks (rows dropped, kept, repeated, moved, wrong indices), reservations until the
     pages run out, drops (rows named twice, wrong indices); tables, lengths and counts after each step."""
@@ -483,7 +484,8 @@ def test_cache_calls_leave_the_rest_of_wider_buffers_alone():
 
 @pytest.mark.parametrize("n_pages,live,rows,width", [(1, 1.0, 1, 1), (2, 0.5, 1, 3), (64, 0.5, 3, 20), (65, 0.9, 2, 40),
                                                      (4096, 0.3, 40, 40), (4097, 0.7, 7, 600), (20000, 0.05, 300, 7),
-                                                     (9001, 1.0, 4, 3000), (777, 0.0, 3, 4)])
+                                                     (9001, 1.0, 4, 3000), (777, 0.0, 3, 4), (300, 0.6, 60, 300),
+                                                     (8192, 0.6, 3, 700), (8193, 0.6, 3, 700)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_compact_matches_plain(n_pages, live, rows, width, in_place):
     import random
