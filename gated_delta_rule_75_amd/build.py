@@ -1,4 +1,4 @@
-"""Build the HIP library ``_kda.so`` (gfx950) in-tree with hipcc.
+"""Build the HIP library ``_kda.so`` (gfx950) and the binding's ``_kda_marshal.so`` in-tree.
 
 Every source under ``csrc/`` is compiled for gfx950 only.  Packed-fp32 instructions are
 disabled (``-packed-fp32-ops``).  The library links the HIP runtime by soname, so when
@@ -16,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "_kda.so")
+MARSHAL = os.path.join(PKG, "_kda_marshal.so")
 ARCH = "gfx950"
 
 
@@ -62,6 +63,27 @@ def build_library(verbose: bool = False, jobs: int = 8) -> str:
     return LIB
 
 
+def build_marshal(verbose: bool = False) -> str:
+    """Compile binding/kda_marshal.cpp (host code against torch's headers) to ``_kda_marshal.so``."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(PKG, "binding", "kda_marshal.cpp"), "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def _wait(item):
     src, p = item
     out, _ = p.communicate()
@@ -75,3 +97,4 @@ def _wait(item):
 
 if __name__ == "__main__":
     print(build_library(verbose=True))
+    print(build_marshal(verbose=True))

@@ -24,18 +24,27 @@ _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _MINUS_ONE = 2 ** 64 - 1
 _U8 = (torch.uint8, torch.bool)
 _LIB = None
+_M = None  # the marshalling module (binding/kda_marshal.cpp) once the library is loaded, if it is built
 
 
 def _lib_():
-    global _LIB
+    global _LIB, _M
     if _LIB is None:
         _LIB = _lib.load()
+        try:
+            from . import _kda_marshal
+        except ImportError:
+            return _LIB
+        _kda_marshal.setup(_RAW_STREAM or _stream_of, _lib.check,
+                           {n: ctypes.cast(getattr(_LIB, n), ctypes.c_void_p).value for n in _lib.EXPORTS})
+        _M = _kda_marshal
     return _LIB
 
 
-# The calls below take a few microseconds of host time, which is what the small ones cost, so each
-# tensor is tested in one expression (`_plain`: a contiguous GPU tensor of the type and device) and
-# described only when that fails (`_gpu`, `_rows`: the messages, and tensors with strides).
+# A small call costs what its host side takes, so the usual one (plain contiguous tensors on the current
+# device) is marshalled in C (`_M`), which returns False for any other.  Those are checked here, each
+# tensor in one expression first (`_plain`: a contiguous GPU tensor of the type and device) and described
+# only when that fails (`_gpu`, `_rows`: the messages, and tensors with strides).
 def _run(fn, di, *args):
     """Calls a library function on the current stream of device `di`, which is made the current one."""
     if _GET_DEVICE() == di:
@@ -97,6 +106,13 @@ def _vector(t, name, dtype, shape, di):
     _check(t, name, dtype, shape, None)
 
 
+def _int32(**values):
+    """Raises for a whole number that the library's 32-bit arguments do not hold (ctypes would cut it)."""
+    for name, x in values.items():
+        if not -2 ** 31 <= int(x) < 2 ** 31:
+            raise ValueError(f"{name} must be a 32-bit whole number, got {x}")
+
+
 def _lead(t, name):
     """Type code and device index of the tensor that the others go by."""
     if not isinstance(t, _T):
@@ -145,6 +161,10 @@ def cache_append(k, v, k_pages, v_pages, page_table, start, *, cu_seqlens=None):
     (pages of any stride), page_table int32 [N,P], start int32 [N]: the position of each sequence's first
     new token.  cu_seqlens None: one token per sequence (T = N); else int32 [N+1], packed segments.
     Positions without a page are dropped."""
+    if _M is not None:
+        done = _M.cache_append(k, v, k_pages, v_pages, page_table, start, cu_seqlens)
+        if done is not False:
+            return
     code, di = _lead(k, "k")
     dt = k.dtype
     ks, vs = _row(k, "k", dt, 3, di), _row(v, "v", dt, 3, di)
@@ -177,6 +197,12 @@ def paged_decode(q, k_pages, v_pages, page_table, lengths, *, scale=None, window
     launch (P * page_size by default).
     Returns out [N,H_q,d] float32; with lse=True (or a tensor for it) (out, lse [N,H_q] float32).  A sequence
     with no visible token gives 0 and -inf."""
+    if _M is not None:
+        done = _M.paged_decode(q, k_pages, v_pages, page_table, lengths, scale, window, sinks, max_length, out, lse,
+                               workspace)
+        if done is not False:
+            return done
+    _int32(window=window, sinks=sinks)
     code, di = _lead(q, "q")
     dt = q.dtype
     qs = _row(q, "q", dt, 3, di)
@@ -223,6 +249,10 @@ def cache_fork(page_table, lengths, refcount, parents, *, table_out=None, length
     reorders, keeps and drops sequences; refcount is updated in place.
 
     Returns (table_out [N_out,P], lengths_out [N_out])."""
+    if _M is not None:
+        done = _M.cache_fork(page_table, lengths, refcount, parents, table_out, lengths_out)
+        if done is not False:
+            return done
     ts, di = _table(page_table, "page_table")
     N, P = page_table.shape
     _vector(lengths, "lengths", _I32, (N,), di)
@@ -249,6 +279,10 @@ def cache_fork(page_table, lengths, refcount, parents, *, table_out=None, length
 def cache_free(page_table, lengths, refcount, rows):
     """Drops sequences in place: the pages of every row in rows (int32 [R]) lose one reference, its entries
     become -1 and its length 0.  Rows outside the table are left out; one named twice is freed once."""
+    if _M is not None:
+        done = _M.cache_free(page_table, lengths, refcount, rows)
+        if done is not False:
+            return
     ts, di = _table(page_table, "page_table")
     N, P = page_table.shape
     _vector(lengths, "lengths", _I32, (N,), di)
@@ -266,6 +300,11 @@ def cache_reserve(page_table, lengths, refcount, new_tokens, page_size, *, copie
     Returns (copies int32 [N,2], granted int32 [N]).  copies: the page pair (old, new) that pages_copy has to
     copy for a sequence whose shared page was partly filled, else (-1, -1).  granted: new_tokens[n], or 0 for
     a sequence that was left as it was because pages (or table columns) ran out; lengths grow by it."""
+    if _M is not None:
+        done = _M.cache_reserve(page_table, lengths, refcount, new_tokens, page_size, copies, granted, workspace)
+        if done is not False:
+            return done
+    _int32(page_size=page_size)
     ts, di = _table(page_table, "page_table")
     N, P = page_table.shape
     _vector(lengths, "lengths", _I32, (N,), di)
@@ -292,6 +331,10 @@ def cache_compact(page_table, refcount, *, table_out=None, refcount_out=None, mo
 
     Returns (table_out, refcount_out, moves int32 [n_pages // 2, 2]); table_out and refcount_out may be given
     as page_table and refcount themselves.  The pages are moved by pages_copy(pools, moves)."""
+    if _M is not None:
+        done = _M.cache_compact(page_table, refcount, table_out, refcount_out, moves, workspace)
+        if done is not False:
+            return done
     ts, di = _table(page_table, "page_table")
     N, P = page_table.shape
     _vector(refcount, "refcount", _I32, None, di)
@@ -326,6 +369,10 @@ def pages_copy(pools, pairs):
 
     pools: a tensor [n_pages, ...] or a list of them (any dtypes and sizes, the same n_pages; pages
     contiguous, of any stride), for instance key and value pages, or recurrent states [n_pages,H,dk,dv]."""
+    if _M is not None:
+        done = _M.pages_copy(pools, pairs)
+        if done is not False:
+            return
     if isinstance(pools, _T):
         pools = (pools,)
     n = len(pools)
@@ -362,6 +409,10 @@ def beam_select(logits, scores, *, n_out=None, finished=None, eos=-1, workspace=
     finished uint8 or bool [B,K]: such a beam goes on with `eos` alone at its own score.
     Returns (scores [B,n_out] float32 descending, parents int32 [B,n_out], tokens int32 [B,n_out],
     finished [B,n_out] or None).  Ties go to the lower beam and token; NaN logits count as -inf."""
+    if _M is not None:
+        done = _M.beam_select(logits, scores, n_out, finished, eos, workspace)
+        if done is not False:
+            return done
     code, di = _lead(logits, "logits")
     if logits.dim() != 3:
         raise ValueError(f"logits must have 3 axes, got {logits.dim()}")
@@ -376,6 +427,7 @@ def beam_select(logits, scores, *, n_out=None, finished=None, eos=-1, workspace=
     _vector(scores, "scores", _F32, (B, K), di)
     if n_out is None:
         n_out = K
+    _int32(n_out=n_out, eos=eos)
     if n_out < 0:
         raise ValueError("n_out must be positive")
     L = _lib_()
@@ -401,6 +453,10 @@ def beam_reorder(states, parents):
 
     states: a contiguous tensor [B*K, ...] or a list of them (the layers' recurrent states, for instance
     [B*K,H,dk,dv])."""
+    if _M is not None:
+        done = _M.beam_reorder(states, parents)
+        if done is not False:
+            return
     if isinstance(states, _T):
         states = (states,)
     n = len(states)

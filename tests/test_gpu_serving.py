@@ -880,6 +880,78 @@ def test_debug_check_of_tables(monkeypatch):
         kda.paged_decode(q, cache.kp, cache.vp, cache.table, cache.len)
 
 
+def test_the_marshalling_module_serves_the_usual_calls(monkeypatch):
+    """The calls of a plain program go through the C marshalling; with it taken away the results are the
+    same, and what it does not know (strides, other types) goes the Python way and is refused there."""
+    from gated_delta_rule_75_amd import serving
+
+    cache = Cache([200, 70], 2, 64, 16, BF16, seed=71, extra_cols=3, spare=30)
+    refs = i32(counts(cache.table.tolist(), cache.kp.shape[0]))
+    q, k, v = queries(2, 8, 64, BF16), queries(2, 2, 64, BF16, seed=2), queries(2, 2, 64, BF16, seed=3)
+    logits, scores = torch.randn(2, 3, 5000, generator=gen(4)).to(DEV), torch.zeros(2, 3, device=DEV)
+    done = i32([[0, 1, 0], [0, 0, 0]]).to(torch.uint8)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+
+    def everything():
+        t, n, r, kp, vp = (x.clone() for x in (cache.table, cache.len, refs, cache.kp, cache.vp))
+        state = torch.arange(6 * 8, device=DEV, dtype=F32).view(6, 8)
+        res = []
+        t2, n2 = kda.cache_fork(t, n, r, i32([0, 1, 0, 1, -1]))
+        res += [t2, n2, *kda.cache_reserve(t2, n2, r, i32([1, 2, 3, 40, 5]), 16)]
+        res += [*kda.cache_reserve(t2, n2, r, i32([1, 0, 0, 0, 5]), 16, workspace=ws)]
+        kda.pages_copy([kp, vp], res[2])
+        kda.pages_copy(kp, res[4])
+        kda.cache_append(k, v, kp, vp, t, n - 1)
+        kda.cache_append(k, v, kp, vp, t2, n2 - 1, cu_seqlens=i32([0, 1, 1, 2, 2, 2]))
+        kda.cache_free(t2, n2, r, i32([1, 1]))
+        res += [*kda.cache_compact(t2, r), *kda.cache_compact(t2, r, workspace=ws)]
+        res.append(kda.paged_decode(q, kp, vp, t, n))
+        res += kda.paged_decode(q, kp, vp, t, n, scale=0.2, window=9, sinks=2, max_length=250, lse=True, workspace=ws,
+                                out=torch.empty(2, 8, 64, device=DEV))
+        res += kda.paged_decode(q, kp, vp, t, n, lse=torch.empty(2, 8, device=DEV))
+        a, b, c, d = kda.beam_select(logits, scores)
+        assert d is None
+        res += [a, b, c, *kda.beam_select(logits, scores, n_out=5, finished=done, eos=7, workspace=ws)]
+        kda.beam_reorder([state], b)
+        return res + [r, kp, vp, state]
+
+    first = everything()
+    assert serving._M is not None
+    for name in ("cache_append", "paged_decode", "cache_fork", "cache_free", "cache_reserve", "cache_compact",
+                 "pages_copy", "beam_select", "beam_reorder"):
+        assert hasattr(serving._M, name)
+    calls = []
+    real = serving._run
+    monkeypatch.setattr(serving, "_run", lambda *a: calls.append(a) or real(*a))
+    everything()
+    assert not calls  # nothing went the Python way
+    monkeypatch.setattr(serving, "_M", None)
+    for x, y in zip(first, everything()):
+        assert x.dtype == y.dtype and torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert calls
+    monkeypatch.undo()
+    with pytest.raises(kda.KdaError, match="sinks"):
+        kda.paged_decode(q, cache.kp, cache.vp, cache.table, cache.len, sinks=3)
+    with pytest.raises(ValueError, match="window"):
+        kda.paged_decode(q, cache.kp, cache.vp, cache.table, cache.len, window=2 ** 32)
+    with pytest.raises(ValueError, match="page_size"):
+        kda.cache_reserve(cache.table, cache.len, refs, i32([1, 1]), 2 ** 32)
+    with pytest.raises(ValueError, match="lengths"):
+        kda.paged_decode(q, cache.kp, cache.vp, cache.table, cache.len[:1])
+    with pytest.raises(ValueError, match="torch.int32"):
+        kda.cache_append(k, v, cache.kp, cache.vp, cache.table, cache.len.long())
+    with pytest.raises(ValueError, match="expected|GPU tensor"):
+        kda.cache_fork(cache.table, cache.len.cpu(), refs, i32([0]))
+    with pytest.raises(ValueError, match="contiguous"):
+        kda.paged_decode(q.transpose(1, 2).contiguous().transpose(1, 2), cache.kp, cache.vp, cache.table, cache.len)
+    with pytest.raises(ValueError, match="must be"):
+        kda.beam_reorder(torch.zeros(5, 4, device=DEV), i32([[0, 1, 2], [0, 1, 2]]))
+    with pytest.raises(ValueError, match="must be"):
+        kda.pages_copy([cache.kp, cache.vp[:3]], i32([[0, 1]]))
+    with pytest.raises(kda.KdaError, match="multiples of 16"):
+        kda.pages_copy(torch.zeros(5, 3, device=DEV), i32([[0, 1]]))
+
+
 def test_kernel_timing_names_the_kernels():
     cache = Cache([4000, 40], 1, 64, 16, BF16, seed=63)
     q = queries(2, 2, 64, BF16)
