@@ -29,18 +29,53 @@ constexpr int kBlockWords = kBlockPages / 64;  // 64-bit words per block
 constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxTokens = 16;
 
+constexpr int kAppendUnroll = 4;
+
 template <bool PACKED>
 __global__ __launch_bounds__(kAppendThreads) void append_kernel(CacheAppendArgs a, int tb, int vpt, int vph_shift,
                                                                 uint32_t vpt_magic) {
     __shared__ int64_t s_k[kAppendMaxTokens], s_v[kAppendMaxTokens];  // slot offsets in bytes, -1: dropped
     const int64_t t0 = (int64_t)blockIdx.x * tb;
     const int nt = (int)(a.T_total - t0 < tb ? a.T_total - t0 : tb);
-    const int row_bytes = a.d * a.esz;
-    if ((int)threadIdx.x < nt) {
+    const int row_bytes = a.d * a.esz, total = nt * vpt;
+    const char* ks = static_cast<const char*>(a.k) + t0 * a.k_stride * a.esz;
+    const char* vs = static_cast<const char*>(a.v) + t0 * a.v_stride * a.esz;
+    const int64_t kst = a.k_stride * a.esz, vst = a.v_stride * a.esz;
+    u32x4 kv[kAppendUnroll], vv[kAppendUnroll];
+    int tok[kAppendUnroll];
+    auto fetch = [&](int x0) {
+#pragma unroll
+        for (int i = 0; i < kAppendUnroll; ++i) {
+            const int x = x0 + i * kAppendThreads + threadIdx.x;
+            tok[i] = (int)__umulhi((uint32_t)x, vpt_magic);  // x / vpt (exact: x * vpt < 2^32)
+            if (x < total) {
+                const int64_t r = x - tok[i] * vpt;
+                kv[i] = *reinterpret_cast<const u32x4*>(ks + tok[i] * kst + r * 16);
+                vv[i] = *reinterpret_cast<const u32x4*>(vs + tok[i] * vst + r * 16);
+            }
+        }
+    };
+    fetch(0);  // on their way while the slots are looked up
+    if ((int)threadIdx.x < nt || (PACKED && a.N <= 64 && threadIdx.x < 64)) {
         const int64_t t = t0 + threadIdx.x;
         int64_t n = t, i = 0;
-        bool in = true;
-        if (PACKED) {  // the last segment that begins at or before t (empty ones begin where the next does)
+        bool in = (int)threadIdx.x < nt;
+        if (PACKED && a.N <= 64) {
+            // the segment ends in the lanes of one wave: the tokens' segments are counts of the ends at or
+            // before them, one load instead of a binary search's chain
+            const int lane = threadIdx.x;
+            const int64_t end = lane < a.N ? a.cu[lane + 1] : INT64_MAX;
+            n = 0;
+            for (int j = 0; j < nt; ++j) {
+                const int c = __popcll(__ballot(end <= t0 + j));
+                if (j == lane) n = c;
+            }
+            if (n >= a.N) n = a.N - 1;
+            if (in) {
+                i = t - a.cu[n];
+                in = i >= 0 && t < a.cu[n + 1];
+            }
+        } else if (PACKED) {  // the last segment that begins at or before t (empty ones begin where the next does)
             int64_t lo = 0, hi = a.N - 1;
             while (lo < hi) {
                 const int64_t mid = (lo + hi + 1) >> 1;
@@ -48,13 +83,12 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(CacheAppendArgs 
             }
             n = lo;
             i = t - a.cu[n];
-            in = i >= 0 && t < a.cu[n + 1];
+            in = in && i >= 0 && t < a.cu[n + 1];
         }
         int64_t ko = -1, vo = -1;
-        const int64_t pos = (int64_t)a.start[n] + i;
-        if (in && pos >= 0) {
-            const int64_t col = pos / a.page_size;
-            if (col < a.pt.width) {
+        if (in) {
+            const int64_t pos = (int64_t)a.start[n] + i, col = pos / a.page_size;
+            if (pos >= 0 && col < a.pt.width) {
                 const int32_t p = a.pt.table[n * a.pt.stride + col];
                 if (p >= 0 && p < a.pt.n_pages) {
                     const int64_t slot = (pos - col * a.page_size) * row_bytes;
@@ -63,29 +97,29 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(CacheAppendArgs 
                 }
             }
         }
-        s_k[threadIdx.x] = ko;
-        s_v[threadIdx.x] = vo;
+        if ((int)threadIdx.x < nt) {
+            s_k[threadIdx.x] = ko;
+            s_v[threadIdx.x] = vo;
+        }
     }
     __syncthreads();
-    const char* ks = static_cast<const char*>(a.k) + t0 * a.k_stride * a.esz;
-    const char* vs = static_cast<const char*>(a.v) + t0 * a.v_stride * a.esz;
-    const int64_t kst = a.k_stride * a.esz, vst = a.v_stride * a.esz;
     const int64_t head_bytes = (int64_t)a.page_size * row_bytes;
-    const int total = nt * vpt;
     const int vmask = (1 << vph_shift) - 1;
-#pragma unroll 4
-    for (int x = threadIdx.x; x < total; x += kAppendThreads) {
-        const int t = (int)__umulhi((uint32_t)x, vpt_magic);  // x / vpt (exact: x * vpt < 2^32)
-        const int r = x - t * vpt;
-        const int64_t ko = s_k[t], vo = s_v[t];
-        if (ko < 0) continue;
-        const int64_t at = (int64_t)(r >> vph_shift) * head_bytes + (r & vmask) * 16;
-        const u32x4 kv = *reinterpret_cast<const u32x4*>(ks + t * kst + (int64_t)r * 16);
-        const u32x4 vv = *reinterpret_cast<const u32x4*>(vs + t * vst + (int64_t)r * 16);
-        // past the caches: 5.4 against 5.1 TB/s for 131072 tokens of 8 heads (loads past them: 5.5, but 4.5
-        // against 5.1 for a call that fits them)
-        __builtin_nontemporal_store(kv, reinterpret_cast<u32x4*>(static_cast<char*>(a.kp) + ko + at));
-        __builtin_nontemporal_store(vv, reinterpret_cast<u32x4*>(static_cast<char*>(a.vp) + vo + at));
+    for (int x0 = 0; x0 < total; x0 += kAppendUnroll * kAppendThreads) {
+        if (x0 > 0) fetch(x0);
+#pragma unroll
+        for (int i = 0; i < kAppendUnroll; ++i) {
+            const int x = x0 + i * kAppendThreads + threadIdx.x;
+            if (x >= total) continue;
+            const int64_t ko = s_k[tok[i]], vo = s_v[tok[i]];
+            if (ko < 0) continue;
+            const int r = x - tok[i] * vpt;
+            const int64_t at = (int64_t)(r >> vph_shift) * head_bytes + (r & vmask) * 16;
+            // past the caches: 5.4 against 5.1 TB/s for 131072 tokens of 8 heads (loads past them: 5.5, but
+            // 4.5 against 5.1 for a call that fits them)
+            __builtin_nontemporal_store(kv[i], reinterpret_cast<u32x4*>(static_cast<char*>(a.kp) + ko + at));
+            __builtin_nontemporal_store(vv[i], reinterpret_cast<u32x4*>(static_cast<char*>(a.vp) + vo + at));
+        }
     }
 }
 
@@ -342,67 +376,54 @@ __device__ __forceinline__ Span64 new_columns(int32_t len, int32_t add, int page
     return s;
 }
 
-// pages that sequence n needs, marked in its row; -1 where the row is too narrow (one wave)
-__device__ __forceinline__ int32_t count_need(const CacheReserveArgs& a, int64_t n) {
+// pages that sequence n needs from column first + skip on, marked in its row (one wave)
+__device__ __forceinline__ int32_t count_need(const CacheReserveArgs& a, int64_t n, const Span64& s, int skip) {
     const int lane = threadIdx.x & 63;
-    const Span64 s = new_columns(a.lengths[n], a.new_tokens[n], a.page_size, a.width);
     int32_t need = 0;
-    if (!s.none)
-        for (int64_t j0 = s.first; j0 <= s.last; j0 += 64) {
-            const int64_t j = j0 + lane;
-            bool want = false;
-            if (j <= s.last) {
-                int32_t* e = a.table + n * a.stride + j;
-                const int32_t p = *e;
-                const bool page = is_page(p, a.n_pages);
-                want = !page || a.refs[p] > 1;
-                if (want) *e = page ? -2 - p : -1;
-            }
-            need += __popcll(__ballot(want));
+    for (int64_t j0 = s.first + skip; j0 <= s.last; j0 += 64) {
+        const int64_t j = j0 + lane;
+        bool want = false;
+        if (j <= s.last) {
+            int32_t* e = a.table + n * a.stride + j;
+            const int32_t p = *e;
+            const bool page = is_page(p, a.n_pages);
+            want = !page || a.refs[p] > 1;
+            if (want) *e = page ? -2 - p : -1;
         }
-    return s.bad ? -1 : need;
+        need += __popcll(__ballot(want));
+    }
+    return need;
 }
 
-// hands out the pages to sequence n, whose first has rank `base` among the free ones (one wave)
-__device__ __forceinline__ void take_pages(const CacheReserveArgs& a, const CacheWs& w, const int32_t* s_prefix,
-                                           int64_t n, int32_t need, int64_t base) {
+// hands out the pages to the marked columns from first + skip on, or takes the marks back; the first has
+// rank `base` among the free pages (one wave).  Returns the pair of the first column in lane 0: the
+// page it had and the one it has got, or -1.
+__device__ __forceinline__ int2 take_pages(const CacheReserveArgs& a, const CacheWs& w, const int32_t* s_prefix,
+                                           int64_t n, const Span64& s, int skip, bool served, int64_t base) {
     const int lane = threadIdx.x & 63;
-    const int32_t len = a.lengths[n], add = a.new_tokens[n];
-    const Span64 s = new_columns(len, add, a.page_size, a.width);
-    const bool served = add > 0 && need >= 0 && base + need <= s_prefix[w.blocks];
-    int32_t from = -1, to = -1;
-    if (!s.none)
-        for (int64_t j0 = s.first; j0 <= s.last; j0 += 64) {
-            const int64_t j = j0 + lane;
-            int32_t* e = a.table + n * a.stride + j;
-            const int32_t mark = j <= s.last ? *e : 0;
-            const uint64_t m = __ballot(mark < 0);
-            if (mark < 0) {
-                const int32_t old = -2 - mark;  // -1: no page before
-                if (served) {
-                    const int32_t p = select_page(w, s_prefix, (int32_t)(base + __popcll(m & ((1ull << lane) - 1))));
-                    *e = p;
-                    a.refs[p] = 1;
-                    if (old >= 0) {
-                        atomicSub(a.refs + old, 1);
-                        if (j == s.first && len % a.page_size) {
-                            from = old;
-                            to = p;
-                        }
-                    }
-                } else if (old >= 0) {
-                    *e = old;
+    int2 pair = make_int2(-1, -1);
+    for (int64_t j0 = s.first + skip; j0 <= s.last; j0 += 64) {
+        const int64_t j = j0 + lane;
+        int32_t* e = a.table + n * a.stride + j;
+        const int32_t mark = j <= s.last ? *e : 0;
+        const uint64_t m = __ballot(mark < 0);
+        if (mark < 0) {
+            const int32_t old = -2 - mark;  // -1: no page before
+            if (served) {
+                const int32_t p = select_page(w, s_prefix, (int32_t)(base + __popcll(m & ((1ull << lane) - 1))));
+                *e = p;
+                a.refs[p] = 1;
+                if (old >= 0) {
+                    atomicSub(a.refs + old, 1);
+                    if (j == s.first) pair = make_int2(old, p);
                 }
+            } else if (old >= 0) {
+                *e = old;
             }
-            base += __popcll(m);
         }
-    // the copied page, if any, is the first column's: lane 0 of the first round
-    if (lane == 0) {
-        a.copies[2 * n] = from;
-        a.copies[2 * n + 1] = to;
-        a.granted[n] = served ? add : 0;
-        if (served) a.lengths[n] = len + add;
+        base += __popcll(m);
     }
+    return pair;
 }
 
 __global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserveArgs a) {
@@ -413,8 +434,9 @@ __global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserve
     }
     const int64_t n = (int64_t)(blockIdx.x - w.blocks) * kRowsPerGroup + (threadIdx.x >> 6);
     if (n >= a.N) return;
-    const int32_t need = count_need(a, n);
-    if ((threadIdx.x & 63) == 0) w.aux[n] = need;
+    const Span64 s = new_columns(a.lengths[n], a.new_tokens[n], a.page_size, a.width);
+    const int32_t need = s.none ? 0 : count_need(a, n, s, 0);
+    if ((threadIdx.x & 63) == 0) w.aux[n] = s.bad ? -1 : need;
 }
 
 // Second launch: one wave per sequence.  Its first page is the free one whose rank is the sum of the
@@ -436,26 +458,97 @@ __global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs 
     int64_t base = 0;
     for (int i = 0; i < kRowsPerGroup; ++i) base += s_sum[i];
     for (int i = 0; i < wave; ++i) base += w.aux[n0 + i] > 0 ? w.aux[n0 + i] : 0;
-    take_pages(a, w, s_prefix, n, w.aux[n], base);
+    const int32_t len = a.lengths[n], add = a.new_tokens[n], need = w.aux[n];
+    const Span64 s = new_columns(len, add, a.page_size, a.width);
+    const bool served = add > 0 && need >= 0 && base + need <= s_prefix[w.blocks];
+    int2 pair = make_int2(-1, -1);
+    if (!s.none) pair = take_pages(a, w, s_prefix, n, s, 0, served, base);
+    if (lane == 0) {  // the first column's page is the only one that can be partly filled
+        const bool part = pair.x >= 0 && len % a.page_size;
+        a.copies[2 * n] = part ? pair.x : -1;
+        a.copies[2 * n + 1] = part ? pair.y : -1;
+        a.granted[n] = served ? add : 0;
+        if (served) a.lengths[n] = len + add;
+    }
 }
 
-// Small pools and few sequences: both steps in one workgroup, with the scan in LDS.  It does not run
-// faster than the two launches (about 10 us each way for 32 sequences), but the second one costs its
-// caller 2.5 us, which is what bounds a small call.
+// Small pools and few sequences: both steps in one workgroup, with the scan in LDS and the first 64
+// columns of each sequence in registers in between (further ones go by the marks in the table).  The
+// second launch costs the caller 2.5 us, which is what bounds a small call.
 __global__ __launch_bounds__(kSmallThreads) void reserve_small_kernel(CacheReserveArgs a) {
+    constexpr int R = kSmallRows / (kSmallThreads / 64);
     __shared__ SmallScan s;
     __shared__ int32_t s_need[kSmallRows];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int32_t len[R], add[R], e[R], need[R];
+    Span64 span[R];
+    bool want[R];
+    // the sequences' loads and the scan's overlap
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int n = wave + i * (kSmallThreads / 64);
+        len[i] = n < a.N ? a.lengths[n] : 0;
+        add[i] = n < a.N ? a.new_tokens[n] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int n = wave + i * (kSmallThreads / 64);
+        span[i] = new_columns(len[i], add[i], a.page_size, a.width);
+        e[i] = -1;
+        want[i] = !span[i].none && span[i].first + lane <= span[i].last;
+        if (want[i]) e[i] = a.table[n * a.stride + span[i].first + lane];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (!is_page(e[i], a.n_pages)) e[i] = -1;
+        if (e[i] >= 0 && a.refs[e[i]] <= 1) want[i] = false;
+    }
     const CacheWs w = small_scan<true>(a.refs, a.n_pages, s);
-    for (int n = wave; n < a.N; n += kSmallThreads / 64) {
-        const int32_t need = count_need(a, n);
-        if (lane == 0) s_need[n] = need;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int n = wave + i * (kSmallThreads / 64);
+        need[i] = __popcll(__ballot(want[i]));
+        if (!span[i].none && span[i].last >= span[i].first + 64) need[i] += count_need(a, n, span[i], 64);
+        if (lane == 0 && n < a.N) s_need[n] = span[i].bad ? -1 : need[i];
     }
     __syncthreads();  // the scan too, and every look at a count before the first change
-    for (int n = wave; n < a.N; n += kSmallThreads / 64) {
-        int64_t base = 0;
-        for (int i = 0; i < n; ++i) base += s_need[i] > 0 ? s_need[i] : 0;
-        take_pages(a, w, s.prefix, n, s_need[n], base);
+    // running sums of the needs, in the lanes of every wave
+    int64_t before = lane < a.N && s_need[lane < kSmallRows ? lane : 0] > 0 ? s_need[lane] : 0;
+    const int64_t own = before;
+#pragma unroll
+    for (int off = 1; off < kSmallRows; off <<= 1) {
+        const int64_t y = __shfl_up(before, off, 64);
+        if (lane >= off) before += y;
+    }
+    before -= own;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int n = wave + i * (kSmallThreads / 64);
+        if (n >= a.N) continue;
+        const int64_t base = __shfl(before, n, 64);
+        const bool served = add[i] > 0 && !span[i].bad && base + need[i] <= s.prefix[w.blocks];
+        const uint64_t m = __ballot(want[i]);
+        int32_t p = -1;
+        if (want[i]) {
+            int32_t* at = a.table + n * a.stride + span[i].first + lane;
+            if (served) {
+                p = select_page(w, s.prefix, (int32_t)(base + __popcll(m & ((1ull << lane) - 1))));
+                *at = p;
+                a.refs[p] = 1;
+                if (e[i] >= 0) atomicSub(a.refs + e[i], 1);
+            } else if (e[i] < 0) {
+                *at = -1;
+            }
+        }
+        if (!span[i].none && span[i].last >= span[i].first + 64)
+            take_pages(a, w, s.prefix, n, span[i], 64, served, base + __popcll(m));
+        if (lane == 0) {  // the first column's page is the only one that can be partly filled
+            const bool part = p >= 0 && e[i] >= 0 && len[i] % a.page_size;
+            a.copies[2 * n] = part ? e[i] : -1;
+            a.copies[2 * n + 1] = part ? p : -1;
+            a.granted[n] = served ? add[i] : 0;
+            if (served) a.lengths[n] = len[i] + add[i];
+        }
     }
 }
 
@@ -613,6 +706,7 @@ hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t s) {
     if (a.T_total == 0) return hipSuccess;
     const int vph = a.d * a.esz / 16, vpt = a.H * vph;
     int tb = (4 * kAppendThreads) / vpt;  // about four vectors of keys per thread
+    if (tb > a.T_total / 512) tb = (int)(a.T_total / 512);  // few tokens: spread over the chip
     tb = tb < 1 ? 1 : tb > kAppendMaxTokens ? kAppendMaxTokens : tb;
     const uint32_t magic = (uint32_t)(((1ull << 32) + vpt - 1) / vpt);
     const unsigned grid = (unsigned)div_up(a.T_total, tb);

@@ -151,42 +151,49 @@ __global__ __launch_bounds__(kThreads, HT == 2 && D == 128 ? 1 : 2) void paged_d
     const int h = (int)(g % a.Hkv);
     const int64_t n = g / a.Hkv;
 
-    const Visible vis = visible(a, n);
-    const int t0 = part * plan.part_tiles;
-    if (t0 >= vis.tiles && part > 0) return;  // the join does not look at it
-    const int t1 = t0 + plan.part_tiles < vis.tiles ? t0 + plan.part_tiles : vis.tiles;
-
-    // page and place of this wave's tiles, one per lane: the lane's tile is NT * (w + 4 * (lane / NT)) + lane % NT
-    const int tiles_per_page = a.page_size / kTile;
-    int my_page = -1, my_slot = 0, my_lo = 0, my_hi = 0;
-    {
-        const int t = t0 + NT * (w + kWaves * (lane / NT)) + lane % NT;
-        if (t < t1) {
-            const bool sink = t < vis.head_tiles;
-            const int tile = sink ? t : vis.first + t - vis.head_tiles;
-            const int col = tile / tiles_per_page;
-            const int32_t p = a.pt.table[n * a.pt.stride + col];
-            const int lo = (sink ? 0 : vis.near) - tile * kTile, hi = (sink ? vis.head : vis.len) - tile * kTile;
-            my_slot = (tile - col * tiles_per_page) * kTile;
-            my_lo = lo > 0 ? lo : 0;
-            my_hi = hi < kTile ? hi : kTile;
-            if (p >= 0 && p < a.pt.n_pages) my_page = p;
-        }
-    }
-    const int steps = (t1 - t0 + NT * kWaves - 1) / (NT * kWaves);  // of the workgroup; some waves' last are empty
-
-    // queries: columns of the first product
+    // The loads that need nothing but the indexes go first: the queries (columns of the first product),
+    // and without a window the page numbers of this wave's tiles, whose places do not depend on the
+    // length (with one, the length's latency comes before theirs).
     u32x4 q[HT][KS];
 #pragma unroll
     for (int t = 0; t < HT; ++t) {
         const int hq = g0 + 16 * t + lr;
         const T* row = static_cast<const T*>(a.q) + n * a.q_stride + (int64_t)(h * G + (hq < G ? hq : 0)) * D;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
+        for (int ks = 0; ks < KS; ++ks)
             q[t][ks] = *reinterpret_cast<const u32x4*>(row + ks * (D / KS) + lg * (16 / ES));
-            if (hq >= G) q[t][ks] = u32x4{0, 0, 0, 0};
-        }
     }
+    // one tile per lane: NT * (w + 4 * (lane / NT)) + lane % NT of the part
+    const int t0 = part * plan.part_tiles, my_tile = t0 + NT * (w + kWaves * (lane / NT)) + lane % NT;
+    const int tiles_per_page = a.page_size / kTile;
+    const int32_t* row = a.pt.table + n * a.pt.stride;
+    int32_t my_page = -1;
+    if (a.window == 0 && my_tile / tiles_per_page < a.pt.width) my_page = row[my_tile / tiles_per_page];
+    const Visible vis = visible(a, n);
+    if (t0 >= vis.tiles && part > 0) return;  // the join does not look at it
+    const int t1 = t0 + plan.part_tiles < vis.tiles ? t0 + plan.part_tiles : vis.tiles;
+
+    int my_slot = 0, my_lo = 0, my_hi = 0;
+    if (my_tile < t1) {
+        const bool sink = my_tile < vis.head_tiles;
+        const int tile = sink ? my_tile : vis.first + my_tile - vis.head_tiles;
+        const int col = tile / tiles_per_page;
+        if (a.window != 0) my_page = row[col];
+        const int lo = (sink ? 0 : vis.near) - tile * kTile, hi = (sink ? vis.head : vis.len) - tile * kTile;
+        my_slot = (tile - col * tiles_per_page) * kTile;
+        my_lo = lo > 0 ? lo : 0;
+        my_hi = hi < kTile ? hi : kTile;
+        if (my_page >= a.pt.n_pages) my_page = -1;
+    } else {
+        my_page = -1;
+    }
+    const int steps = (t1 - t0 + NT * kWaves - 1) / (NT * kWaves);  // of the workgroup; some waves' last are empty
+#pragma unroll
+    for (int t = 0; t < HT; ++t)
+        if (g0 + 16 * t + lr >= G) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) q[t][ks] = u32x4{0, 0, 0, 0};
+        }
 
     auto load = [&](S& s, int step) {
 #pragma unroll
@@ -415,24 +422,46 @@ __global__ __launch_bounds__(kThreads) void paged_join_kernel(PagedDecodeArgs a,
     __shared__ float s_o[kWaves][D], s_l[kWaves];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = blockIdx.x;
-    const Visible vis = visible(a, row / a.Hq);
-    const int parts = vis.tiles > 0 ? (vis.tiles + plan.part_tiles - 1) / plan.part_tiles : 1;
     const float2* ml = part_ml + row * plan.parts;
     const float* po = part_o + row * plan.parts * D + lane * CH;
-    float M = -INFINITY;
-    for (int p = lane; p < parts; p += 64) M = fmaxf(M, ml[p].x);
+    // The first loads do not wait for the number of parts: they stay inside the row's share of the
+    // workspace, and what was not written for this call is replaced by 0 below.
+    constexpr int kFirst = 8;
+    float2 y0 = ml[lane < plan.parts ? lane : plan.parts - 1];
+    float x0[kFirst][CH];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int p = w + kWaves * i < plan.parts ? w + kWaves * i : plan.parts - 1;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) x0[i][c] = po[(int64_t)p * D + c];
+    }
+    const Visible vis = visible(a, row / a.Hq);
+    const int parts = vis.tiles > 0 ? (vis.tiles + plan.part_tiles - 1) / plan.part_tiles : 1;
+    if (lane >= parts) y0 = make_float2(-INFINITY, 0.f);
+    float M = y0.x;
+    for (int p = 64 + lane; p < parts; p += 64) M = fmaxf(M, ml[p].x);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
     const float base = M == -INFINITY ? 0.f : M;
     float L = 0.f, acc[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) acc[c] = 0.f;
-    for (int p0 = w; p0 < parts; p0 += 64 * kWaves) {  // lane i: part p0 + 4 i
-        float wgt = 0.f;
+    // weights of the first 64 parts in the lanes; part w + 4 i is wave w's
+    float wgt = exp2_hw(y0.x - base);
+    if ((lane & (kWaves - 1)) == w) L = y0.y * wgt;
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int p = w + kWaves * i;
+        const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wgt), p));
+#pragma unroll
+        for (int c = 0; c < CH; ++c) acc[c] += p < parts ? f * x0[i][c] : 0.f;
+    }
+    for (int p0 = w + kWaves * kFirst; p0 < parts; p0 += 64 * kWaves) {  // lane i: part p0 + 4 i
+        wgt = 0.f;
         if (p0 + kWaves * lane < parts) {
             const float2 y = ml[p0 + kWaves * lane];
             wgt = exp2_hw(y.x - base);
-            L += y.y * wgt;
+            if (p0 + kWaves * lane >= 64) L += y.y * wgt;  // the first 64 are in already
         }
         const int left = (parts - p0 + kWaves - 1) / kWaves, count = left < 64 ? left : 64;
         for (int i0 = 0; i0 < count; i0 += 8) {  // eight loads in flight; parts behind the last have weight 0
