@@ -239,16 +239,22 @@ __global__ __launch_bounds__(kThreads, HT == 2 && D == 128 ? 1 : 2) void paged_d
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 floatx4 x = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (kBf16) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    if constexpr (kBf16) {
-                        x = mfma_bf16(s.k[t][ks], q[ht][ks], x);
-                    } else {
+                    for (int ks = 0; ks < KS; ++ks) x = mfma_bf16(s.k[t][ks], q[ht][ks], x);
+                } else {
+                    // four sums side by side: a quarter of the chain of dependent steps, and of its rounding
+                    floatx4 y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            x = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(s.k[t][ks][i]),
-                                                                     __uint_as_float(q[ht][ks][i]), x, 0, 0, 0);
-                    }
+                            y[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(s.k[t][ks][i]),
+                                                                        __uint_as_float(q[ht][ks][i]), y[i], 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = (y[0][i] + y[1][i]) + (y[2][i] + y[3][i]);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
