@@ -106,7 +106,7 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
 bool workspace_of(PyObject* o, size_t need, int dev, const Tensor& like, Tensor& keep, void*& p, size_t& bytes) {
     if (need == (size_t)-1) return false;
     if (o != Py_None) {
-        const Tensor* t = plain(o, at::kByte, 1, dev);
+        const Tensor* t = plain(o, at::kByte, -1, dev);
         if (!t) return false;
         if ((size_t)t->numel() >= need) {
             p = t->data_ptr();

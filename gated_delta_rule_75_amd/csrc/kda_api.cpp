@@ -280,7 +280,7 @@ int kda_validate_gates(const float* g, int64_t n_g, const float* beta, int64_t n
     return ok();
 }
 
-const char* kda_version(void) { return "kda-mi355x 0.2.0 (gfx950)"; }
+const char* kda_version(void) { return "kda-mi355x 0.3.0 (gfx950)"; }
 
 int kda_timing_begin(void) {
     g_timing.on = true;

@@ -69,7 +69,7 @@ Span table_span(const int32_t* t, int64_t stride, int64_t N, int32_t width) {
 }
 
 int check_pages(const char* name, const Pool& k, const Pool& v, int32_t page_size, int32_t H, int32_t d,
-                int32_t dtype) {
+                int32_t dtype, bool written) {
     if (!valid_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, "%s: dtype must be KDA_F32 or KDA_BF16", name);
     if (H <= 0 || H > 1024) return fail(KDA_ERR_INVALID_ARG, "%s: H_kv must be in [1, 1024]", name);
     if (!kda::paged_decode_supported(d)) return fail(KDA_ERR_UNSUPPORTED, "%s: d=%d not implemented", name, d);
@@ -80,7 +80,7 @@ int check_pages(const char* name, const Pool& k, const Pool& v, int32_t page_siz
         return fail(KDA_ERR_INVALID_ARG, "%s: pages overlap (stride below the page)", name);
     if (!aligned16(k.p) || !aligned16(v.p) || k.stride % 16 || v.stride % 16)
         return fail(KDA_ERR_MISALIGNED, "%s: pages must be 16-byte aligned", name);
-    if (overlap(k, v)) return fail(KDA_ERR_ALIAS, "%s: k_pages and v_pages overlap", name);
+    if (written && overlap(k, v)) return fail(KDA_ERR_ALIAS, "%s: k_pages and v_pages overlap", name);
     return KDA_OK;
 }
 
@@ -188,7 +188,7 @@ int kda_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_s
     const int64_t page = page_bytes_of(H_kv, page_size, d, es), row = (int64_t)H_kv * d * es;
     const Pool kp = pool_of(k_pages, k_page_stride * es, page, n_pages);
     const Pool vp = pool_of(v_pages, v_page_stride * es, page, n_pages);
-    if (int rc = check_pages(name, kp, vp, page_size, H_kv, d, dtype)) return rc;
+    if (int rc = check_pages(name, kp, vp, page_size, H_kv, d, dtype, true)) return rc;
     if (T_total < 0 || T_total > kMaxGrid) return fail(KDA_ERR_INVALID_ARG, "%s: T_total must be in [0, 2^31)", name);
     if (!cu_seqlens && T_total != N)
         return fail(KDA_ERR_INVALID_ARG, "%s: without cu_seqlens T_total must be N", name);
@@ -248,7 +248,7 @@ int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const
     const int64_t page = page_bytes_of(H_kv, page_size, d, es), row = (int64_t)H_q * d * es;
     const Pool kp = pool_of(k_pages, k_page_stride * es, page, n_pages);
     const Pool vp = pool_of(v_pages, v_page_stride * es, page, n_pages);
-    if (int rc = check_pages(name, kp, vp, page_size, H_kv, d, dtype)) return rc;
+    if (int rc = check_pages(name, kp, vp, page_size, H_kv, d, dtype, false)) return rc;
     if (H_q <= 0 || H_q % H_kv || H_q > 16384)
         return fail(KDA_ERR_INVALID_ARG, "%s: H_q must be a multiple of H_kv up to 16384", name);
     if (!std::isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "%s: scale must be finite", name);
@@ -259,7 +259,8 @@ int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const
         return fail(KDA_ERR_INVALID_ARG, "%s: N * H_q times the table's tokens is too large", name);
     const int64_t room = (int64_t)table_pages * page_size;
     const int64_t most = max_length > 0 && max_length < room ? max_length : room;
-    if (room > 0x7FFFFFFF) return fail(KDA_ERR_INVALID_ARG, "%s: table_pages * page_size must be below 2^31", name);
+    if (room > 0x7FFFFFFF - 4096)
+        return fail(KDA_ERR_INVALID_ARG, "%s: table_pages * page_size must be below 2^31 - 4096", name);
     if (N > 0 && (!q || !lengths || !out)) return fail(KDA_ERR_INVALID_ARG, "%s: q, lengths and out are required", name);
     if (N > 1 && q_stride * es < row) return fail(KDA_ERR_INVALID_ARG, "%s: queries overlap (stride below H_q * d)", name);
     if (!aligned16(q) || (N > 1 && q_stride * es % 16))

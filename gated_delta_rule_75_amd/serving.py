@@ -140,9 +140,11 @@ def _run_scratch(fn, di, workspace, size, *args):
     """_run with the workspace's address and bytes behind args: the caller's when it is large enough (the
     library says so), else a new one of size[0](*size[1:]) bytes."""
     if workspace is not None:
-        _vector(workspace, "workspace", torch.uint8, None, di)
+        if not _plain(workspace, torch.uint8, di):
+            _gpu(workspace, "workspace", torch.uint8, None, di)
+            _check(workspace, "workspace")
         if _GET_DEVICE() == di:
-            status = fn(*args, workspace.data_ptr(), workspace.shape[0], _stream_of(di))
+            status = fn(*args, workspace.data_ptr(), workspace.numel(), _stream_of(di))
             if status == 0:
                 return
             if status != _lib.KDA_ERR_WORKSPACE:

@@ -357,7 +357,8 @@ int kda_validate_gates(const float* g, int64_t n_g, const float* beta, int64_t n
  * Token i of sequence n goes to position start[n] + i.  A position without a
  * page (before 0, behind the table, or at an entry that names none) is dropped.
  * The pages written must belong to one sequence each (kda_cache_reserve sees to
- * that); two sequences that write the same slot leave either value.
+ * that); two sequences that write the same slot leave either value.  k_pages and
+ * v_pages must not overlap (they may for kda_paged_decode, which only reads them).
  * d in {64, 128, 256}.
  */
 int kda_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens,
@@ -377,7 +378,8 @@ int kda_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_s
  *   window  0, or only the last `window` tokens are visible ...
  *   sinks   ... and the first `sinks` tokens (0 without a window)
  *   max_length  an upper bound of lengths that sizes the launch; 0: the table's
- *           table_pages * page_size.  A longer sequence is cut there.
+ *           table_pages * page_size (which has to be below 2^31 - 4096).  A longer
+ *           sequence is cut there.
  *   out     [N, H_q, d] float; lse [N, H_q] float or NULL
  * A sequence without a visible token (or whose every visible score is -inf)
  * gives out = 0 and lse = -inf.  Tokens that are not visible are never used,
@@ -398,8 +400,9 @@ int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const
                      int64_t max_length, float* out, float* lse, void* workspace, size_t workspace_bytes,
                      void* hip_stream);
 
-/* Workspace bytes of kda_paged_decode (max_length > 0: the bound given, or
- * table_pages * page_size); (size_t)-1 for an unsupported or invalid combination. */
+/* Workspace bytes of kda_paged_decode, max_length being the smaller of the bound
+ * given and table_pages * page_size (not 0 for "no bound" here); (size_t)-1 for an
+ * unsupported or invalid combination. */
 size_t kda_paged_decode_workspace(int32_t N, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype, int64_t max_length,
                                   int32_t window, int32_t sinks);
 

@@ -262,6 +262,33 @@ def test_paged_decode_is_deterministic_and_does_not_depend_on_the_workspace(dtyp
         assert torch.equal(x, y) and torch.equal(x, z)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_paged_decode_may_read_one_pool_as_keys_and_values(dtype):
+    cache = Cache([90, 33], 2, 64, 16, dtype, seed=26)
+    cache.v, cache.vp = cache.k, cache.kp
+    check_attention(cache, queries(2, 4, 64, dtype), workspace=torch.empty(1 << 10, 1 << 10, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,hkv,group", [(64, 3, 5), (128, 2, 40), (256, 1, 17)])
+def test_paged_decode_every_length_around_tiles_and_parts(dtype, d, hkv, group):
+    """Lengths 0 .. 70 and around the ends of steps and parts of a longer batch, in one call."""
+    lengths = list(range(71)) + [127, 128, 129, 255, 256, 257, 511, 513, 1023, 1025, 2047, 2048, 2049, 2303]
+    cache = Cache(lengths, hkv, d, 16, dtype, seed=d)
+    q = queries(len(lengths), hkv * group, d, dtype)
+    check_attention(cache, q)
+    check_attention(cache, q, window=37, sinks=3)
+
+
+def test_paged_decode_table_without_columns():
+    q = queries(3, 4, 64, F32)
+    pages = torch.zeros(2, 2, 16, 64, device=DEV)
+    out, lse = kda.paged_decode(q, pages, pages, torch.zeros(3, 0, dtype=torch.int32, device=DEV), i32([0, 5, 9]), lse=True)
+    assert not out.any() and bool(torch.isneginf(lse).all())
+    out = kda.paged_decode(q[:0], pages, pages, torch.zeros(0, 3, dtype=torch.int32, device=DEV), i32([]))
+    assert tuple(out.shape) == (0, 4, 64)
+
+
 def test_paged_decode_offsets_beyond_32_bits():
     """Pages whose byte offset (and element offset) passes 2^32, in a pool reserved but mostly untouched."""
     page, hkv, d = 64, 8, 128
