@@ -83,12 +83,13 @@ struct Round {
 #pragma unroll
         for (int v = 0; v < NV; ++v) raw[v] = *reinterpret_cast<const u32x4*>(row + token(base, v * W, true));
     }
+    // as they are: NaN stays NaN, which no comparison below lets through
     static __device__ __forceinline__ void values(const u32x4 (&raw)[NV], float (&x)[kPer]) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const uint32_t word = raw[i / W][(i % W) * sizeof(T) / 4];
-            if (sizeof(T) == 4) x[i] = clean(__uint_as_float(word));
-            else x[i] = clean(__uint_as_float((i & 1) ? word & 0xFFFF0000u : word << 16));
+            if (sizeof(T) == 4) x[i] = __uint_as_float(word);
+            else x[i] = __uint_as_float((i & 1) ? word & 0xFFFF0000u : word << 16);
         }
     }
     static __device__ __forceinline__ void singles(const T* row, int base, int first, int last, float (&x)[kPer]) {
@@ -104,11 +105,24 @@ struct Round {
             u32x4 raw[NV];
             fetch(row, base, raw);
             values(raw, x);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = clean(x[i]);
         } else {
             singles(row, base, first, last, x);
         }
     }
 };
+
+// sum of exp(x - m), m the maximum (-inf: nothing is above it).  One product and sum per logit: with r =
+// fl(m log2 e), exp(x - m) = 2^(x log2 e - r) 2^(r - m log2 e), the last factor once for all.
+__device__ __forceinline__ float exp_sum(const float (&x)[kPer], float m) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float ref = m == -INFINITY ? 0.f : m, r = ref * kLog2e, rest = -__builtin_fmaf(ref, kLog2e, -r);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kLog2e, -r));
+    return sum * __builtin_amdgcn_exp2f(rest);
+}
 
 // x of lane ^ 1, ^ 2, then mirrored in 8 and in 16 lanes, then of lane ^ 16 and ^ 32: six steps after
 // which a maximum or minimum covers the wave
@@ -169,15 +183,15 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
         // the next round's logits are on their way while this one is worked on
         ready = base + kRound >= 0 && base + 2 * kRound <= last;
         if (ready) R::fetch(x0, base + kRound, next);
-        float top = x[0];
+        float four[kPer / 4], top = -INFINITY;  // maxima of four logits each, and of all
 #pragma unroll
-        for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
-        const float now = fmaxf(m, top), ref = now == -INFINITY ? 0.f : now;
-        float sum = l * fast_exp(m - ref);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) sum += fast_exp(x[i] - ref);
+        for (int i = 0; i < kPer / 4; ++i) {
+            four[i] = fmaxf(fmaxf(fmaxf(-INFINITY, x[4 * i]), x[4 * i + 1]), fmaxf(x[4 * i + 2], x[4 * i + 3]));
+            top = fmaxf(top, four[i]);
+        }
+        const float now = fmaxf(m, top);
+        l = l * fast_exp(m - (now == -INFINITY ? 0.f : now)) + exp_sum(x, now);
         m = now;
-        l = sum;
         // the least of the maxima of groups of 2^group_shift threads
         float g = top;
         g = max_min_step<0>(g, group_shift);
@@ -193,11 +207,14 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
         g = group_shift > 6 ? fmaxf(g, s_g[turn][1]) : fminf(g, s_g[turn][1]);
         h = group_shift > 6 ? fmaxf(h, s_g[turn][3]) : fminf(h, s_g[turn][3]);
         bar = fmaxf(bar, group_shift > 7 ? fmaxf(g, h) : fminf(g, h));
-        // every wave appends to a list of its own, in step, which needs no atomics
-        if (__any(top >= bar && top > -INFINITY)) {
+        // every wave appends to a list of its own, in step, which needs no atomics (-inf is not collected)
+        const float least = bar == -INFINITY ? -3.402823466e38f : bar;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const bool in = x[i] >= bar && x[i] > -INFINITY;
+        for (int q = 0; q < kPer / 4; ++q) {
+            if (!__any(four[q] >= least)) continue;
+#pragma unroll
+            for (int i = 4 * q; i < 4 * q + 4; ++i) {
+                const bool in = x[i] >= least;
                 const uint64_t mask = __ballot(in);
                 if (mask) {
                     const int at = mine + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
@@ -206,6 +223,21 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
                     mine += __popcll(mask);
                 }
             }
+        }
+    }
+    if (__syncthreads_or(l != l)) {  // a NaN (which counts as -inf), an infinite or a huge logit: the sum once more
+        m = -INFINITY;
+        l = 0.f;
+        for (int base = begin; base < last; base += kRound) {
+            float x[kPer], now = m;
+            R::load(x0, base, first, last, base >= 0 && base + kRound <= last, x);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) now = fmaxf(now, x[i]);
+            const float ref = now == -INFINITY ? 0.f : now;
+            l *= fast_exp(m - ref);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) l += fast_exp(x[i] - ref);
+            m = now;
         }
     }
     // log-sum of the part
@@ -317,6 +349,7 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
 
 constexpr int kJoinThreads = 256;  // >= kMaxOut
 constexpr int kJoinList = 1024;
+constexpr int kPassing = 64;       // lists followed one by one
 
 __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs a, SelectPlan plan,
                                                                  const uint64_t* keys, const float2* sums) {
@@ -326,10 +359,10 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs 
     __shared__ int s_beam[kJoinList];
     __shared__ Cand s_best[kJoinThreads / 64];
     __shared__ double s_m[kJoinThreads / 64];
-    __shared__ int s_count;
+    __shared__ int s_count, s_lists, s_pass[kPassing];
     const int64_t b = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (tid == 0) s_count = 0;
+    if (tid == 0) s_count = s_lists = 0;
     // the beams' log-sums: 16 lanes per beam over its parts
     for (int k = tid >> 4; k < a.K; k += kJoinThreads / 16) {
         const float2* y = sums + (b * a.K + k) * plan.parts;
@@ -363,9 +396,10 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs 
     // threads.
     const int lists = a.K * plan.parts, depth = (a.n_out + lists - 1) / lists, probes = lists * depth;
     const int held = probes < kJoinThreads ? probes : kJoinThreads;
+    auto probe = [&](int i) { return cand(depth == 1 ? i * a.n_out : i / depth * a.n_out + i % depth); };
     double top = -INFINITY;
     for (int i = tid; i < probes; i += kJoinThreads) {
-        const Cand x = cand(depth == 1 ? i * a.n_out : i / depth * a.n_out + i % depth);
+        const Cand x = probe(i);
         if (x.key) top = fmax(top, x.c);
     }
     s_top[tid] = top;
@@ -383,19 +417,31 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamSelectArgs 
 #pragma unroll
     for (int w = 0; w < kJoinThreads / 64; ++w) bar = fmin(bar, s_m[w]);
     auto collect = [&](const Cand& x) {
-        if (!x.key || !(x.c >= bar && x.c > -INFINITY)) return false;
+        if (!x.key || !(x.c >= bar && x.c > -INFINITY)) return;
         const int at = atomicAdd(&s_count, 1);
         if (at < kJoinList) {
             s_c[at] = x.c;
             s_key[at] = x.key;
             s_beam[at] = x.beam;
         }
-        return true;
     };
-    if (lists >= kJoinThreads) {  // a list per thread, down to its first candidate below the threshold
-        for (int i = tid; i < lists; i += kJoinThreads)
-            for (int r = 0; r < a.n_out; ++r)
-                if (!collect(cand(i * a.n_out + r))) break;
+    if (depth == 1) {
+        // only the lists whose first candidate reaches the threshold can have others that do: about n_out
+        for (int i = tid; i < lists; i += kJoinThreads) {
+            const Cand x = lists <= kJoinThreads && top < bar ? Cand{-INFINITY, 0, 0} : probe(i);
+            if (x.key && x.c >= bar && x.c > -INFINITY) {
+                const int at = atomicAdd(&s_lists, 1);
+                if (at < kPassing) s_pass[at] = i;
+            }
+        }
+        __syncthreads();
+        const int found = s_lists;
+        if (found <= kPassing) {
+            for (int i = tid; i < found * a.n_out; i += kJoinThreads)
+                collect(cand(s_pass[i / a.n_out] * a.n_out + i % a.n_out));
+        } else {
+            for (int i = tid; i < n; i += kJoinThreads) collect(cand(i));
+        }
     } else {
         for (int i = tid; i < n; i += kJoinThreads) collect(cand(i));
     }

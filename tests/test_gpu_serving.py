@@ -682,6 +682,16 @@ def test_beam_select_ties_and_masks(dtype):
     check_select(logits, first.to(DEV), 8)
     steps = torch.arange(2 * 2 * 30000, dtype=F32).view(2, 2, 30000) * 1e-4  # ascending
     check_select(steps.to(dtype).to(DEV), torch.zeros(2, 2, device=DEV), 16)
+    wild = (torch.randn(2, 4, 40000, generator=g) * 3).to(dtype)  # NaN and infinities here and there, huge values
+    wild[0, 0, 12345], wild[0, 1, 7] = math.nan, -math.inf
+    wild[0, 2, ::2] = math.nan
+    wild[0, 3] = math.nan
+    wild[0, 3, 39999] = -2.0
+    wild[1, 0, 30000], wild[1, 1, 30001] = 3.2e38, math.inf
+    wild[1, 2] = -3e38
+    wild[1, 2, 5] = -2.9e38
+    for n_out in (4, 40):
+        check_select(wild.to(DEV), torch.tensor([[0.0, -1.0, 0.5, 0.2]] * 2, device=DEV), n_out)
     zeros = torch.where(torch.arange(8192) % 2 == 0, torch.tensor(-0.0), torch.tensor(0.0))
     check_select(zeros.expand(1, 2, 8192).contiguous().to(dtype).to(DEV), torch.zeros(1, 2, device=DEV), 4)
 
