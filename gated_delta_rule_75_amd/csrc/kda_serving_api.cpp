@@ -125,7 +125,7 @@ int read_pools(const char* name, void* const* base, const int64_t* strides, cons
     if (count > 0 && (!base || !bytes)) return fail(KDA_ERR_INVALID_ARG, "%s: the buffers' arrays are required", name);
     for (int32_t i = 0; i < count; ++i) {
         const int64_t st = strides ? strides[i] : bytes[i];
-        if (bytes[i] < 0 || st < bytes[i] || !sane_stride(st))
+        if (bytes[i] < 0 || bytes[i] >= ((int64_t)1 << 32) || st < bytes[i] || !sane_stride(st))
             return fail(KDA_ERR_INVALID_ARG, "%s: buffer %d: bad row size or stride", name, i);
         if (rows > 0 && bytes[i] > 0 && !base[i]) return fail(KDA_ERR_INVALID_ARG, "%s: buffer %d is NULL", name, i);
         if (!aligned16(base[i]) || bytes[i] % 16 || st % 16)

@@ -481,7 +481,7 @@ size_t kda_cache_workspace_size(int32_t N, int32_t n_pages);
  * another (the pairs of kda_cache_reserve and kda_cache_compact are such).
  *   pools, page_strides, page_bytes  HOST arrays of n_pools entries: the pool's
  *            device address, bytes between pages, bytes of a page (all multiples
- *            of 16).  Read before the call returns.
+ *            of 16; a page below 4 GiB).  Read before the call returns.
  * Any rows of equal size are pages here, for instance recurrent states
  * [n_pages, H, d_k, d_v].
  */
@@ -524,8 +524,8 @@ size_t kda_beam_select_workspace(int32_t B, int32_t K, int32_t V, int32_t n_out)
  * Rows whose parent is their own index are neither read nor written for
  * themselves; a parent outside [0, K) leaves its row as it is.
  *   states, row_bytes  HOST arrays of n_states entries: the device address of
- *            [B * K] contiguous rows and the bytes of a row (multiples of 16).
- *            Read before the call returns.
+ *            [B * K] contiguous rows and the bytes of a row (multiples of 16,
+ *            below 4 GiB).  Read before the call returns.
  *   parents  DEVICE int32 [B, K]; 1 <= K <= 64
  */
 int kda_beam_reorder(void* const* states, const int64_t* row_bytes, int32_t n_states, const int32_t* parents,

@@ -156,6 +156,7 @@ def test_buffer_lists_are_checked():
     assert copy([(P[0], 4096, 4088)]) == _l.KDA_ERR_MISALIGNED
     assert copy([(P[0] + 4, 4096, 4096)]) == _l.KDA_ERR_MISALIGNED
     assert copy([(P[0], 4080, 4096)]) == _l.KDA_ERR_INVALID_ARG  # stride below the page
+    assert copy([(P[0], 1 << 32, 1 << 32)]) == _l.KDA_ERR_INVALID_ARG
     assert copy([(None, 4096, 4096)]) == _l.KDA_ERR_INVALID_ARG and b"NULL" in L.kda_last_error()
     assert copy([good, (P[0] + 4096, 4096, 4096)]) == _l.KDA_ERR_ALIAS
     assert copy([good], pairs=P[0] + 64) == _l.KDA_ERR_ALIAS
