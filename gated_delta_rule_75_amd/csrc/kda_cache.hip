@@ -639,8 +639,8 @@ __global__ __launch_bounds__(kSmallThreads) void compact_small_kernel(CacheCompa
 // ------------------------------------------------------------------------------------------
 // Traffic only.  A workgroup of one wave copies 4 KiB and is done: workgroups start in order, so that
 // the chip works through the pages as one stream.  Larger pieces and loops over them spread it over more
-// of the memory and are slower (a plain copy of 2 GiB: 6.3 to 6.7 TB/s with 1 to 4 KiB a workgroup, 6.0
-// with 16, 5.4 with 32, 4.7 to 5.8 in loops of 512 to 16384 workgroups).
+// of the memory and are slower (a plain copy of 2 GiB: 6.3 to 6.7 TB/s with 1 to 4 KiB a workgroup, 5.8
+// to 6.0 with 16, 5.2 to 5.8 with 32, 4.5 to 5.8 in loops of 512 to 16384 workgroups).
 //
 // A long list may be mostly empty (a compaction's has room for every second page).  There a workgroup
 // takes one piece of kFar pairs, which stand a kFar-th of the list apart, so that an empty

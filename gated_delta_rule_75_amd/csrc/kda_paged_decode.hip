@@ -518,9 +518,9 @@ PartPlan part_plan(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_leng
     if ((window > 0 && max_length > window) || N <= 2) {
         // Sequences behind their window all have the same tiles, and so has a lone one: the part length with
         // the fewest rounds of resident workgroups times steps, where a workgroup's start and end count as
-        // three steps and the join as four.  Against the rule below, whole calls: 13.3 and 17.1 us for 100
-        // sequences with a window of 512, 8.3 and 11.2 for 16 with 256, 8.4 and 9.3 for a lone one of 300
-        // tokens; 25.9 and 25.0 at worst.
+        // three steps and the join as four.  Against the rule below, whole calls: 13.4 and 21.3 us for 100
+        // sequences with a window of 512, 14.1 and 17.7 for a lone one of 9000 tokens, 20.6 and 33.9 for one
+        // of 30000 in fp32; at worst 25.9 and 24.4, for 48 with a window of 1024 in fp32.
         const int64_t slots = 256 * (d == 64 && p.heads == 16 ? 3 : d == 128 && p.heads == 32 ? 1 : 2);
         int64_t best = 0;
         for (int64_t steps = 1; steps * step_tiles <= kMaxPartTiles; ++steps) {
