@@ -155,6 +155,15 @@ def test_paged_decode_window_and_sinks(dtype, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1)])
+def test_paged_decode_largest_windows_and_sinks(dtype, window, sinks):
+    """The largest 32-bit window and sinks: every token is visible, without a sum that leaves 32 bits."""
+    print(f"window {window} sinks {sinks} {dtype}", flush=True)
+    cache = Cache([0, 1, 5, 6, 64, 700], 2, 64, 32, dtype, seed=13)
+    check_attention(cache, queries(6, 8, 64, dtype), window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_paged_decode_pages_given_back(dtype):
     """Entries without a page (-1, or beyond the pool) leave their tokens out, inside the sequence too; a
     sequence that has none left gives 0 and -inf."""
