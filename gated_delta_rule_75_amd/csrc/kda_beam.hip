@@ -114,11 +114,20 @@ struct Round {
 };
 
 // sum of exp(x - m), m the maximum (-inf: nothing is above it).  One product and sum per logit: with r =
-// fl(m log2 e), exp(x - m) = 2^(x log2 e - r) 2^(r - m log2 e), the last factor once for all.
+// fl(m log2 e), exp(x - m) = 2^(x log2 e - r) 2^(r - m log2 e), the last factor once for all.  That needs a small
+// r - m log2 e, which is half a unit in the last place of r and grows with m: up to |m| = 2^24 it is 1 at most.
+// Beyond (at 2.1e9 it reaches 128, where the hardware's exponential is 0 for one factor and finite for the
+// other) the wave takes the difference first.  m infinite goes there too, and inf - inf makes the sum NaN.
 __device__ __forceinline__ float exp_sum(const float (&x)[kPer], float m) {
     constexpr float kLog2e = 1.4426950408889634f;
-    const float ref = m == -INFINITY ? 0.f : m, r = ref * kLog2e, rest = -__builtin_fmaf(ref, kLog2e, -r);
+    const float ref = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
+    if (__any(fabsf(ref) > 16777216.f)) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum += fast_exp(x[i] - ref);
+        return sum;
+    }
+    const float r = ref * kLog2e, rest = -__builtin_fmaf(ref, kLog2e, -r);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kLog2e, -r));
     return sum * __builtin_amdgcn_exp2f(rest);
@@ -225,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a, S
             }
         }
     }
-    if (__syncthreads_or(l != l)) {  // a NaN (which counts as -inf), an infinite or a huge logit: the sum once more
+    if (__syncthreads_or(l != l)) {  // a NaN (which counts as -inf) or a logit of +inf: the sum once more
         m = -INFINITY;
         l = 0.f;
         for (int base = begin; base < last; base += kRound) {

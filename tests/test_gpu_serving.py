@@ -705,6 +705,53 @@ def test_beam_select_ties_and_masks(dtype):
     check_select(zeros.expand(1, 2, 8192).contiguous().to(dtype).to(DEV), torch.zeros(1, 2, device=DEV), 4)
 
 
+def far_rows(tops, V, g):
+    """Rows that have their maximum at every hundredth token and values a few steps below it elsewhere."""
+    m = torch.tensor(tops, dtype=F32).view(-1, 4, 1)
+    below = m - m.abs() * torch.randint(1, 40, (1, 1, V), generator=g) * 2.0 ** -22
+    assert bool((below < m).all())
+    return torch.where(torch.arange(V) % 100 == 7, m, below)
+
+
+def both_signs(n, e, g):
+    return ((1 + torch.rand(n, generator=g)) * 2.0 ** e * torch.tensor([1.0, -1.0] * (n // 2))).tolist()
+
+
+def test_beam_select_row_maxima_far_beyond_one():
+    """Row maxima m of 2^20 .. 2^33 of both signs: m log2 e and its fp32 rounding then differ by 2^-5 .. 2^9, so
+    a factor that makes up for the rounding leaves the range of the exponential (at 2119338368 and
+    -1621624704 one of two factors is 0 and the other finite, and the log-sum -inf).  Bounds as in check_select:
+    its fp64 sums of score, logit and log-sum are off by 6 * 2^-53 * 2^33 < 6e-6 at most, within its 3 tol."""
+    g = gen(12)
+    tops = [2119338368.0, -1621624704.0, 2.0 ** 24, -2.0 ** 24, 2.0 ** 24 - 1, 1.0 - 2.0 ** 24, 1e6, -1e6]
+    for e in range(20, 33):
+        tops += both_signs(8, e, g)
+    logits = far_rows(tops, 300, g)
+    scores = (torch.randn(logits.shape[0], 4, generator=g) - 3).to(DEV)
+    check_select(logits.to(DEV), scores, 4)
+    check_select(logits.to(BF16).to(DEV), scores, 4)
+
+
+def test_beam_select_row_maxima_up_to_2_to_40():
+    """As above for 2^28 .. 2^40, where a step of the logits is 64 or more: only the three maxima of a row have
+    weight, and c = score - log 3 for each.  The fp64 sum score + m - (m + log 3) is off by 4 roundings of
+    2^-53 |m|, the log of the fp32 sum by (100 + 2) u (check_select's tol without its rounds), the fp32 result
+    by u |c|."""
+    g = gen(13)
+    tops = [1e10, -1e10, 2119338368.0, -1621624704.0]
+    for e in range(28, 40):
+        tops += both_signs(64, e, g)
+    logits = far_rows(tops, 300, g)
+    scores = torch.randn(logits.shape[0], 4, generator=g) - 3
+    got = kda.beam_select(logits.to(DEV), scores.to(DEV))[0].cpu().double()
+    top = torch.sort(scores.double(), dim=1, descending=True).values
+    want = torch.stack([top[:, 0], top[:, 0], top[:, 0], top[:, 1]], 1) - math.log(3.0)
+    far = logits.abs().amax((1, 2)).double()[:, None]
+    tol = 4 * 2.0 ** -53 * far + 102 * U + U * want.abs()
+    worst = float(((got - want).abs() / tol).max())
+    assert worst <= 1, worst
+
+
 @pytest.mark.parametrize("kind", [torch.uint8, torch.bool])
 def test_beam_select_finished_beams(kind):
     g = gen(5)
