@@ -167,11 +167,12 @@ __global__ __launch_bounds__(kTableThreads) void free_kernel(CacheFreeArgs a, ui
 // scan of the counts
 // ------------------------------------------------------------------------------------------
 // Workspace of reserve and compact.  `bits`: one bit per page (free pages for reserve, used ones
-// for compact); `before`: set bits of the word's block before the word; `block`: set bits of the
-// block; `aux`: per sequence the number of pages needed (reserve), or the counts of the moved
-// pages (compact).
+// for compact); `shared`: one bit per page with more than one reference when the call began (reserve);
+// `before`: set bits of the word's block before the word; `block`: set bits of the block; `aux`: per
+// sequence the number of pages needed (reserve), or the counts of the moved pages (compact).
 struct CacheWs {
     uint64_t* bits;
+    uint64_t* shared;
     uint32_t* before;
     int32_t* block;
     int32_t* aux;
@@ -185,9 +186,10 @@ __host__ __device__ inline CacheWs cache_ws(void* ws, int64_t n_pages) {
     const int64_t blocks = up(n_pages, kBlockPages) / kBlockPages, words = blocks * kBlockWords;
     char* p = static_cast<char*>(ws);
     w.bits = reinterpret_cast<uint64_t*>(p);
-    w.before = reinterpret_cast<uint32_t*>(p + words * 8);
-    w.block = reinterpret_cast<int32_t*>(p + words * 12);
-    w.aux = reinterpret_cast<int32_t*>(p + words * 12 + up(blocks * 4, 16));
+    w.shared = reinterpret_cast<uint64_t*>(p + words * 8);
+    w.before = reinterpret_cast<uint32_t*>(p + words * 16);
+    w.block = reinterpret_cast<int32_t*>(p + words * 20);
+    w.aux = reinterpret_cast<int32_t*>(p + words * 20 + up(blocks * 4, 16));
     w.words = (int)words;
     w.blocks = (int)blocks;
     return w;
@@ -209,9 +211,10 @@ __device__ __forceinline__ void scan_block(const int32_t* refs, int n_pages, con
     }
 #pragma unroll
     for (int i = 0; i < kBlockWords / 4; ++i) {
-        const uint64_t m = __ballot(FREE ? r[i] <= 0 : r[i] > 0);
+        const uint64_t m = __ballot(FREE ? r[i] <= 0 : r[i] > 0), more = FREE ? __ballot(r[i] > 1) : 0;
         if (lane == 0) {
             w.bits[b * kBlockWords + i * 4 + wave] = m;
+            if (FREE) w.shared[b * kBlockWords + i * 4 + wave] = more;
             s_pop[i * 4 + wave] = __popcll(m);
         }
     }
@@ -290,7 +293,7 @@ __device__ __forceinline__ int32_t bits_before(const CacheWs& w, const int32_t* 
     return s_prefix[b] + (int32_t)w.before[word] + __popcll(w.bits[word] & ((1ull << (p & 63)) - 1));
 }
 
-__device__ __forceinline__ bool bit_of(const CacheWs& w, int32_t p) { return (w.bits[p >> 6] >> (p & 63)) & 1; }
+__device__ __forceinline__ bool bit_of(const uint64_t* bits, int32_t p) { return (bits[p >> 6] >> (p & 63)) & 1; }
 
 // The scan of a small pool by one workgroup, in LDS.
 constexpr int kSmallThreads = 1024;
@@ -299,6 +302,7 @@ constexpr int kSmallRows = 32;        // sequences of a small reserve: two per w
 constexpr int kSmallEntries = 16384;  // table entries of a small compaction: sixteen per thread
 struct SmallScan {
     uint64_t bits[kSmallBlocks * kBlockWords];
+    uint64_t shared[kSmallBlocks * kBlockWords];
     uint32_t before[kSmallBlocks * kBlockWords];
     int32_t block[kSmallBlocks];
     int32_t prefix[kSmallBlocks + 1];
@@ -311,7 +315,7 @@ template <bool FREE>
 __device__ __forceinline__ CacheWs small_scan(const int32_t* refs, int n_pages, SmallScan& s) {
     constexpr int kWords = kSmallBlocks * kBlockWords, kPer = kWords / (kSmallThreads / 64);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    CacheWs w{s.bits, s.before, s.block, s.aux, kWords, kSmallBlocks};
+    CacheWs w{s.bits, s.shared, s.before, s.block, s.aux, kWords, kSmallBlocks};
     int32_t r[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -320,8 +324,11 @@ __device__ __forceinline__ CacheWs small_scan(const int32_t* refs, int n_pages, 
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const uint64_t m = __ballot(FREE ? r[i] <= 0 : r[i] > 0);
-        if (lane == 0) s.bits[i * (kSmallThreads / 64) + wave] = m;
+        const uint64_t m = __ballot(FREE ? r[i] <= 0 : r[i] > 0), more = FREE ? __ballot(r[i] > 1) : 0;
+        if (lane == 0) {
+            s.bits[i * (kSmallThreads / 64) + wave] = m;
+            if (FREE) s.shared[i * (kSmallThreads / 64) + wave] = more;
+        }
     }
     __syncthreads();
     if (wave == 0) {
@@ -350,10 +357,10 @@ __device__ __forceinline__ CacheWs small_scan(const int32_t* refs, int n_pages, 
 // ------------------------------------------------------------------------------------------
 // reserve
 // ------------------------------------------------------------------------------------------
-// First launch: the blocks' scans, and one wave per sequence that counts the pages it needs and
-// marks them in its row: -1 where there is no page, -2 - e where page e is shared.  The marks carry
-// the verdict on the counts as they were when the call began over to the second launch, which
-// changes them.
+// First launch: the blocks' scans, and one wave per sequence that counts the pages it needs.  The scan
+// also keeps a bit for every shared page, which carries the verdict on the counts as they were when
+// the call began over to the second launch, which changes them.  Nothing of a table is written before it
+// is known whether its sequence is served, so one that is not keeps every entry, whatever it holds.
 constexpr int kRowsPerGroup = kScanThreads / 64;
 
 // columns that hold the new tokens' positions; none where nothing is to be reserved, bad where the
@@ -376,7 +383,7 @@ __device__ __forceinline__ Span64 new_columns(int32_t len, int32_t add, int page
     return s;
 }
 
-// pages that sequence n needs from column first + skip on, marked in its row (one wave)
+// pages that sequence n needs from column first + skip on, by the counts before any has changed (one wave)
 __device__ __forceinline__ int32_t count_need(const CacheReserveArgs& a, int64_t n, const Span64& s, int skip) {
     const int lane = threadIdx.x & 63;
     int32_t need = 0;
@@ -384,41 +391,34 @@ __device__ __forceinline__ int32_t count_need(const CacheReserveArgs& a, int64_t
         const int64_t j = j0 + lane;
         bool want = false;
         if (j <= s.last) {
-            int32_t* e = a.table + n * a.stride + j;
-            const int32_t p = *e;
-            const bool page = is_page(p, a.n_pages);
-            want = !page || a.refs[p] > 1;
-            if (want) *e = page ? -2 - p : -1;
+            const int32_t p = a.table[n * a.stride + j];
+            want = !is_page(p, a.n_pages) || a.refs[p] > 1;
         }
         need += __popcll(__ballot(want));
     }
     return need;
 }
 
-// hands out the pages to the marked columns from first + skip on, or takes the marks back; the first has
-// rank `base` among the free pages (one wave).  Returns the pair of the first column in lane 0: the
-// page it had and the one it has got, or -1.
+// hands out the pages to the columns from first + skip on that need one; the first has rank `base` among the
+// free pages (one wave).  Returns the pair of the first column in lane 0: the page it had and the one it
+// has got, or -1.
 __device__ __forceinline__ int2 take_pages(const CacheReserveArgs& a, const CacheWs& w, const int32_t* s_prefix,
-                                           int64_t n, const Span64& s, int skip, bool served, int64_t base) {
+                                           int64_t n, const Span64& s, int skip, int64_t base) {
     const int lane = threadIdx.x & 63;
     int2 pair = make_int2(-1, -1);
     for (int64_t j0 = s.first + skip; j0 <= s.last; j0 += 64) {
         const int64_t j = j0 + lane;
         int32_t* e = a.table + n * a.stride + j;
-        const int32_t mark = j <= s.last ? *e : 0;
-        const uint64_t m = __ballot(mark < 0);
-        if (mark < 0) {
-            const int32_t old = -2 - mark;  // -1: no page before
-            if (served) {
-                const int32_t p = select_page(w, s_prefix, (int32_t)(base + __popcll(m & ((1ull << lane) - 1))));
-                *e = p;
-                a.refs[p] = 1;
-                if (old >= 0) {
-                    atomicSub(a.refs + old, 1);
-                    if (j == s.first) pair = make_int2(old, p);
-                }
-            } else if (old >= 0) {
-                *e = old;
+        const int32_t old = j <= s.last ? *e : -1;
+        const bool page = is_page(old, a.n_pages), want = j <= s.last && (!page || bit_of(w.shared, old));
+        const uint64_t m = __ballot(want);
+        if (want) {
+            const int32_t p = select_page(w, s_prefix, (int32_t)(base + __popcll(m & ((1ull << lane) - 1))));
+            *e = p;
+            a.refs[p] = 1;
+            if (page) {
+                atomicSub(a.refs + old, 1);
+                if (j == s.first) pair = make_int2(old, p);
             }
         }
         base += __popcll(m);
@@ -440,7 +440,7 @@ __global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserve
 }
 
 // Second launch: one wave per sequence.  Its first page is the free one whose rank is the sum of the
-// needs before it; a sequence that is not served gets its marks taken back.
+// needs before it.
 __global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs a) {
     __shared__ int32_t s_prefix[kMaxBlocks + 1];
     __shared__ int64_t s_sum[kRowsPerGroup];
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs 
     const Span64 s = new_columns(len, add, a.page_size, a.width);
     const bool served = add > 0 && need >= 0 && base + need <= s_prefix[w.blocks];
     int2 pair = make_int2(-1, -1);
-    if (!s.none) pair = take_pages(a, w, s_prefix, n, s, 0, served, base);
+    if (served) pair = take_pages(a, w, s_prefix, n, s, 0, base);
     if (lane == 0) {  // the first column's page is the only one that can be partly filled
         const bool part = pair.x >= 0 && len % a.page_size;
         a.copies[2 * n] = part ? pair.x : -1;
@@ -473,8 +473,8 @@ __global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs 
 }
 
 // Small pools and few sequences: both steps in one workgroup, with the scan in LDS and the first 64
-// columns of each sequence in registers in between (further ones go by the marks in the table).  The
-// second launch costs the caller 2.5 us, which is what bounds a small call.
+// columns of each sequence in registers in between (further ones are read again).  The second launch
+// costs the caller 2.5 us, which is what bounds a small call.
 __global__ __launch_bounds__(kSmallThreads) void reserve_small_kernel(CacheReserveArgs a) {
     constexpr int R = kSmallRows / (kSmallThreads / 64);
     __shared__ SmallScan s;
@@ -529,19 +529,14 @@ __global__ __launch_bounds__(kSmallThreads) void reserve_small_kernel(CacheReser
         const bool served = add[i] > 0 && !span[i].bad && base + need[i] <= s.prefix[w.blocks];
         const uint64_t m = __ballot(want[i]);
         int32_t p = -1;
-        if (want[i]) {
-            int32_t* at = a.table + n * a.stride + span[i].first + lane;
-            if (served) {
-                p = select_page(w, s.prefix, (int32_t)(base + __popcll(m & ((1ull << lane) - 1))));
-                *at = p;
-                a.refs[p] = 1;
-                if (e[i] >= 0) atomicSub(a.refs + e[i], 1);
-            } else if (e[i] < 0) {
-                *at = -1;
-            }
+        if (served && want[i]) {
+            p = select_page(w, s.prefix, (int32_t)(base + __popcll(m & ((1ull << lane) - 1))));
+            a.table[n * a.stride + span[i].first + lane] = p;
+            a.refs[p] = 1;
+            if (e[i] >= 0) atomicSub(a.refs + e[i], 1);
         }
-        if (!span[i].none && span[i].last >= span[i].first + 64)
-            take_pages(a, w, s.prefix, n, span[i], 64, served, base + __popcll(m));
+        if (served && span[i].last >= span[i].first + 64)
+            take_pages(a, w, s.prefix, n, span[i], 64, base + __popcll(m));
         if (lane == 0) {  // the first column's page is the only one that can be partly filled
             const bool part = p >= 0 && e[i] >= 0 && len[i] % a.page_size;
             a.copies[2 * n] = part ? e[i] : -1;
@@ -565,7 +560,7 @@ __global__ __launch_bounds__(kScanThreads) void compact_scan_kernel(CacheCompact
 // page p's part in the moves (pages before p, and before the number L of used pages: `front`)
 __device__ __forceinline__ void plan_page(const CacheCompactArgs& a, const CacheWs& w, const int32_t* s_prefix, int p,
                                           int32_t L, int32_t front) {
-    const bool used = bit_of(w, p);
+    const bool used = bit_of(w.bits, p);
     if (used != (p < L)) {
         const int32_t before = bits_before(w, s_prefix, p);
         if (!used) {
@@ -584,14 +579,14 @@ __device__ __forceinline__ void plan_page(const CacheCompactArgs& a, const Cache
 __device__ __forceinline__ void remap_count(const CacheCompactArgs& a, const CacheWs& w, const int32_t* s_prefix, int p,
                                             int32_t L) {
     int32_t r = 0;
-    if (p < L) r = bit_of(w, p) ? a.refs[p] : w.aux[p - bits_before(w, s_prefix, p)];
+    if (p < L) r = bit_of(w.bits, p) ? a.refs[p] : w.aux[p - bits_before(w, s_prefix, p)];
     a.refs_out[p] = r;
 }
 
 __device__ __forceinline__ void remap_entry(const CacheCompactArgs& a, const CacheWs& w, const int32_t* s_prefix,
                                             int64_t row, int j, int32_t L, int32_t front) {
     int32_t e = a.pt.table[row * a.pt.stride + j];
-    if (e >= L && e < a.pt.n_pages && bit_of(w, e)) e = a.moves[2 * (int64_t)(bits_before(w, s_prefix, e) - front) + 1];
+    if (e >= L && e < a.pt.n_pages && bit_of(w.bits, e)) e = a.moves[2 * (int64_t)(bits_before(w, s_prefix, e) - front) + 1];
     a.table_out[row * a.out_stride + j] = e;
 }
 
@@ -740,7 +735,7 @@ hipError_t launch_cache_free(const CacheFreeArgs& a, hipStream_t s) {
 
 size_t cache_workspace(int64_t N, int64_t n_pages) {
     const int64_t blocks = div_up(n_pages, kBlockPages), aux = N > n_pages / 2 ? N : n_pages / 2;
-    return (size_t)up(blocks * kBlockWords * 12 + up(blocks * 4, 16) + aux * 4, 256);
+    return (size_t)up(blocks * kBlockWords * 20 + up(blocks * 4, 16) + aux * 4, 256);
 }
 
 hipError_t launch_cache_reserve(const CacheReserveArgs& a, hipStream_t s) {

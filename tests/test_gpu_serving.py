@@ -503,6 +503,40 @@ def test_reserve_when_pages_or_columns_run_out():
     assert T.tolist()[1] == [0, 1, -1] and L.tolist()[1] == 20
 
 
+@pytest.mark.parametrize("n,width,n_pages", [(5, 9, 40), (5, 200, 600), (40, 200, 2500), (5, 200, 9000)])
+def test_reserve_leaves_a_sequence_that_is_not_served_as_it_was(n, width, n_pages):
+    """Entries that name no page (-1, other negative numbers, those of pages that there are and not, numbers
+    beyond the pool) stand in the columns to come of every sequence, next to shared and own pages.  Two
+    sequences are served, the third needs more pages than there are, so it and those behind it keep every
+    entry; so does one whose row is too narrow.  One workgroup and two launches, columns behind the 64th."""
+    page, half = 16, width // 2
+    none = [-1, -2, -3, -2147483648, n_pages, 2147483647, -2 - (n_pages - 1), -7]
+    free = 2 * width + 3
+    own = list(range(free, n_pages))  # the others are in use: each row has two of its own, shared ones twice
+    table, refs = [], [0] * n_pages
+    for r in range(n):
+        row = [none[(r + j) % len(none)] for j in range(width)]
+        row[half], row[half + 1] = own[0], own[1 + r]
+        table.append(row)
+    for p in own:
+        refs[p] = 1
+    refs[own[0]] = n
+    lengths = [3] * n
+    new = [width * page - 3] * n  # every column: a sequence takes all but its own page
+    new[1] = (width - 1) * page
+    new[3] = width * page - 2  # one token too many for the row
+    if n > 5:
+        new[5:] = [page] * (n - 5)
+    want_table, want_len, want_refs = [list(r) for r in table], list(lengths), list(refs)
+    want_c, want_g = reserve_plain(want_table, want_len, want_refs, new, page)
+    assert want_g[0] == new[0] and want_g[1:4] == [new[1], 0, 0] and not any(want_g[3:])
+    assert want_table[2:] == table[2:]
+    T, L, R = i32(table), i32(lengths), i32(refs)
+    C, G = kda.cache_reserve(T, L, R, i32(new), page)
+    assert C.tolist() == want_c and G.tolist() == want_g and L.tolist() == want_len
+    assert T.tolist() == want_table and R.tolist() == want_refs
+
+
 def test_cache_calls_leave_the_rest_of_wider_buffers_alone():
     wide = torch.full((4, 20), 77, dtype=torch.int32, device=DEV)
     T = wide[:, 4:9]
