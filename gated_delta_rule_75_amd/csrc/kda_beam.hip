@@ -555,6 +555,8 @@ int group_shift_of(int n_out) {
 
 }  // namespace
 
+int64_t beam_select_groups(int64_t B, int K, int V) { return B * K * select_plan(B * K, V).parts; }
+
 size_t beam_select_workspace(int64_t B, int K, int V, int n_out) {
     const SelectPlan p = select_plan(B * K, V);
     return (size_t)div_up(B * K * p.parts * ((int64_t)n_out + 1) * 8, 256) * 256;
@@ -584,11 +586,8 @@ hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s) {
     return e;
 }
 
-hipError_t launch_beam_reorder(const PoolList& p, const int32_t* parents, int B, int K, hipStream_t s) {
-    int64_t most = 0;
-    for (int i = 0; i < p.count; ++i) most = p.bytes[i] > most ? p.bytes[i] : most;
-    if (B == 0 || K <= 1 || most == 0) return hipSuccess;
-    const int64_t groups = div_up(most, kReorderThreads * 16);
+static hipError_t launch_reorder_slice(const PoolList& p, const int32_t* parents, int64_t B, int K, int64_t groups,
+                                       hipStream_t s) {
     const dim3 grid((unsigned)(groups * p.count * B)), block(kReorderThreads);
     const bool timed = timing_on();
     if (timed) timed_begin(kKernelBeamReorder, s);
@@ -599,6 +598,28 @@ hipError_t launch_beam_reorder(const PoolList& p, const int32_t* parents, int B,
     else hipLaunchKernelGGL(beam_reorder_kernel<64>, grid, block, 0, s, p, parents, K, groups);
     const hipError_t e = hipGetLastError();
     if (timed) timed_end(s);
+    return e;
+}
+
+hipError_t launch_beam_reorder(const PoolList& p, const int32_t* parents, int B, int K, hipStream_t s) {
+    int64_t most = 0;
+    for (int i = 0; i < p.count; ++i) most = p.bytes[i] > most ? p.bytes[i] : most;
+    if (B == 0 || K <= 1 || most == 0) return hipSuccess;
+    // in slices of the states and of the groups of beams where a grid does not hold them
+    const int64_t groups = div_up(most, kReorderThreads * 16), fit = max_groups(kReorderThreads) / groups;
+    hipError_t e = hipSuccess;
+    for (int i0 = 0; i0 < p.count && e == hipSuccess; i0 += (int)fit) {
+        PoolList part = p;
+        part.count = p.count - i0 < fit ? p.count - i0 : (int)fit;
+        const int64_t step = fit / part.count;
+        for (int64_t b0 = 0; b0 < B && e == hipSuccess; b0 += step) {
+            for (int i = 0; i < part.count; ++i) {
+                part.bytes[i] = p.bytes[i0 + i];
+                part.base[i] = p.base[i0 + i] + b0 * K * part.bytes[i];
+            }
+            e = launch_reorder_slice(part, parents + b0 * K, B - b0 < step ? B - b0 : step, K, groups, s);
+        }
+    }
     return e;
 }
 

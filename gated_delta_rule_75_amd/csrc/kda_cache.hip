@@ -696,12 +696,19 @@ int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 }  // namespace
 
+static int append_tokens(int64_t T_total, int vpt) {
+    int tb = (4 * kAppendThreads) / vpt;  // about four vectors of keys per thread
+    if (tb > T_total / 512) tb = (int)(T_total / 512);  // few tokens: spread over the chip
+    return tb < 1 ? 1 : tb > kAppendMaxTokens ? kAppendMaxTokens : tb;
+}
+
+int64_t cache_append_groups(int64_t T_total, int H, int d, int esz) {
+    return div_up(T_total, append_tokens(T_total, H * (d * esz / 16)));
+}
+
 hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t s) {
     if (a.T_total == 0) return hipSuccess;
-    const int vph = a.d * a.esz / 16, vpt = a.H * vph;
-    int tb = (4 * kAppendThreads) / vpt;  // about four vectors of keys per thread
-    if (tb > a.T_total / 512) tb = (int)(a.T_total / 512);  // few tokens: spread over the chip
-    tb = tb < 1 ? 1 : tb > kAppendMaxTokens ? kAppendMaxTokens : tb;
+    const int vph = a.d * a.esz / 16, vpt = a.H * vph, tb = append_tokens(a.T_total, vpt);
     const uint32_t magic = (uint32_t)(((1ull << 32) + vpt - 1) / vpt);
     const unsigned grid = (unsigned)div_up(a.T_total, tb);
     return timed_launch(kKernelCacheAppend, s, [&] {
@@ -714,10 +721,16 @@ hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t s) {
     });
 }
 
+int64_t cache_rows_groups(int64_t rows, int width) { return rows * (width ? div_up(width, kTableThreads) : 1); }
+
+int64_t cache_compact_groups(int64_t N, int width, int64_t n_pages) {
+    return div_up(n_pages, kScanThreads) + N * div_up(width, kScanThreads);
+}
+
 hipError_t launch_cache_fork(const CacheForkArgs& a, hipStream_t s) {
     const int64_t rows = a.N > a.N_out ? a.N : a.N_out;
     if (rows == 0) return hipSuccess;
-    const int64_t cols = a.pt.width ? div_up(a.pt.width, kTableThreads) : 1;
+    const int64_t cols = cache_rows_groups(1, a.pt.width);
     return timed_launch(kKernelCacheFork, s, [&] {
         hipLaunchKernelGGL(fork_kernel, dim3((unsigned)(cols * rows)), dim3(kTableThreads), 0, s, a,
                            (uint32_t)cols);
@@ -726,7 +739,7 @@ hipError_t launch_cache_fork(const CacheForkArgs& a, hipStream_t s) {
 
 hipError_t launch_cache_free(const CacheFreeArgs& a, hipStream_t s) {
     if (a.n_rows == 0) return hipSuccess;
-    const int64_t cols = a.width ? div_up(a.width, kTableThreads) : 1;
+    const int64_t cols = cache_rows_groups(1, a.width);
     return timed_launch(kKernelCacheFree, s, [&] {
         hipLaunchKernelGGL(free_kernel, dim3((unsigned)(cols * a.n_rows)), dim3(kTableThreads), 0, s, a,
                            (uint32_t)cols);
@@ -783,7 +796,7 @@ hipError_t launch_pages_copy(const PoolList& p, int n_pages, const int32_t* pair
     const bool many = n_pairs * per_pair > kManyPieces && n_pairs >= 4 * kFar;
     const int64_t apart = many ? div_up(n_pairs, kFar) : n_pairs;
     // in slices of the list where a grid does not hold it
-    const int64_t most_pairs = 0x7FFFFFFF / per_pair;
+    const int64_t most_pairs = max_groups(kCopyThreads) / per_pair;
     hipError_t e = hipSuccess;
     for (int64_t p0 = 0; p0 < apart && e == hipSuccess; p0 += most_pairs) {
         const int64_t groups = apart - p0 < most_pairs ? apart - p0 : most_pairs;

@@ -132,6 +132,10 @@ hipError_t launch_decode(const DecodeArgs& a, hipStream_t s);
 // ---------------------------------------------------------------------------------------
 // paged key-value cache and beam search
 // ---------------------------------------------------------------------------------------
+// A launch holds fewer than 2^32 threads along an axis of its grid: the workgroups of `threads` it may have.
+// The `*_groups` functions below give the most workgroups (of 256 threads) of a call's launches.
+constexpr int64_t max_groups(int threads) { return 0xFFFFFFFFll / threads; }
+
 // Pages [n_pages, H_kv, page_size, d] and the table that names them (include/kda.h).
 struct PageTable {
     const int32_t* table;
@@ -153,6 +157,7 @@ struct CacheAppendArgs {
     PageTable pt;
     int page_size, H, d, esz;
 };
+int64_t cache_append_groups(int64_t T_total, int H, int d, int esz);
 hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t s);
 
 struct PagedDecodeArgs {
@@ -173,7 +178,9 @@ struct PagedDecodeArgs {
     void* ws;
 };
 bool paged_decode_supported(int d);
-size_t paged_decode_workspace(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_length, int window, int sinks);
+// the same, and in `workspace` (0 where they do not fit a launch) the bytes of the partial results
+int64_t paged_decode_groups(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_length, int window, int sinks,
+                            size_t* workspace);
 hipError_t launch_paged_decode(const PagedDecodeArgs& a, hipStream_t s);
 
 struct CacheForkArgs {
@@ -187,6 +194,7 @@ struct CacheForkArgs {
     int64_t out_stride;
     int32_t* lengths_out;
 };
+int64_t cache_rows_groups(int64_t rows, int width);  // fork and free
 hipError_t launch_cache_fork(const CacheForkArgs& a, hipStream_t s);
 
 struct CacheFreeArgs {
@@ -225,6 +233,7 @@ struct CacheCompactArgs {
     int32_t* moves;
     void* ws;
 };
+int64_t cache_compact_groups(int64_t N, int width, int64_t n_pages);
 hipError_t launch_cache_compact(const CacheCompactArgs& a, hipStream_t s);
 size_t cache_workspace(int64_t N, int64_t n_pages);
 
@@ -251,6 +260,7 @@ struct BeamSelectArgs {
     uint8_t* finished_out;
     void* ws;
 };
+int64_t beam_select_groups(int64_t B, int K, int V);
 size_t beam_select_workspace(int64_t B, int K, int V, int n_out);
 hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s);
 

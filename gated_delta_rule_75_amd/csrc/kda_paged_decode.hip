@@ -504,6 +504,11 @@ int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 // registers for that)
 int head_tiles_of(int G, int d, int bf16) { return bf16 && d <= 128 && G > 16 ? 2 : 1; }
 
+// workgroups of a part
+int64_t part_groups(int64_t N, int Hq, int Hkv, int d, int bf16) {
+    return N * Hkv * div_up(Hq / Hkv, 16 * head_tiles_of(Hq / Hkv, d, bf16));
+}
+
 PartPlan part_plan(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_length, int window, int sinks) {
     const int step_tiles = kWaves * (bf16 ? 2 : 1);
     int64_t tiles = div_up(max_length, kTile);
@@ -513,7 +518,7 @@ PartPlan part_plan(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_leng
     }
     PartPlan p;
     p.heads = 16 * head_tiles_of(Hq / Hkv, d, bf16);
-    const int64_t groups = N * Hkv * div_up(Hq / Hkv, p.heads);
+    const int64_t groups = part_groups(N, Hq, Hkv, d, bf16);
     int64_t per = 0;
     if ((window > 0 && max_length > window) || N <= 2) {
         // Sequences behind their window all have the same tiles, and so has a lone one: the part length with
@@ -548,15 +553,23 @@ PartPlan part_plan(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_leng
 
 bool paged_decode_supported(int d) { return d == 64 || d == 128 || d == 256; }
 
-size_t paged_decode_workspace(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_length, int window, int sinks) {
-    const PartPlan p = part_plan(N, Hq, Hkv, d, bf16, max_length, window, sinks);
-    if (p.parts == 1) return 0;
-    return (size_t)(div_up(N * Hq * p.parts * 8, 256) * 256 + N * Hq * p.parts * (int64_t)d * 4);
+int64_t paged_decode_groups(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_length, int window, int sinks,
+                            size_t* workspace) {
+    *workspace = 0;
+    int64_t groups = part_groups(N, Hq, Hkv, d, bf16);
+    if (groups > max_groups(kThreads)) return groups;  // (the plan's products stay within 64 bits below that)
+    const int parts = part_plan(N, Hq, Hkv, d, bf16, max_length, window, sinks).parts;
+    groups *= parts;
+    if (parts == 1) return groups;
+    if (N * Hq > groups) groups = N * Hq;  // the join's
+    if (groups <= max_groups(kThreads))
+        *workspace = (size_t)(div_up(N * Hq * parts * 8, 256) * 256 + N * Hq * parts * (int64_t)d * 4);
+    return groups;
 }
 
 template <typename T, int D>
 static void launch_typed(const PagedDecodeArgs& a, const PartPlan& p, float2* ml, float* po, hipStream_t s) {
-    const unsigned grid = (unsigned)(a.N * a.Hkv * div_up(a.Hq / a.Hkv, p.heads) * p.parts);
+    const unsigned grid = (unsigned)(part_groups(a.N, a.Hq, a.Hkv, a.d, a.bf16) * p.parts);
     if constexpr (std::is_same<T, uint16_t>::value && D <= 128) {
         if (p.heads == 32) {
             hipLaunchKernelGGL((paged_decode_kernel<T, D, 2>), dim3(grid), dim3(kThreads), 0, s, a, p, ml, po);

@@ -14,7 +14,7 @@ namespace {
 
 using namespace kda::api;
 
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+constexpr int64_t kMaxCount = 0x7FFFFFFF;
 constexpr int32_t kMaxPages = 1 << 24;
 
 // Bytes from the first to the end of the last of n rows of `row` bytes, `stride` apart (at most 2^62).
@@ -60,7 +60,6 @@ int check_table(const char* name, const int32_t* table, int64_t stride, int64_t 
     if (N > 0 && width > 0 && !table) return fail(KDA_ERR_INVALID_ARG, "%s: a page table is required", name);
     if (N > 1 && stride < width) return fail(KDA_ERR_INVALID_ARG, "%s: table rows overlap (stride below the width)", name);
     if (!aligned_to(table, 4)) return fail(KDA_ERR_MISALIGNED, "%s: the page table must be 4-byte aligned", name);
-    if (N * ((int64_t)width / 256 + 2) > kMaxGrid) return fail(KDA_ERR_INVALID_ARG, "%s: the page table is too large", name);
     return KDA_OK;
 }
 
@@ -86,6 +85,13 @@ int check_pages(const char* name, const Pool& k, const Pool& v, int32_t page_siz
 
 // strides and sizes small enough that no byte offset leaves 63 bits
 bool sane_stride(int64_t elements) { return elements >= 0 && elements < ((int64_t)1 << 40); }
+
+// A launch of the call would not fit a grid.
+int check_groups(const char* name, int64_t groups) {
+    if (groups <= kda::max_groups(256)) return KDA_OK;
+    return fail(KDA_ERR_INVALID_ARG, "%s: the call is too large (%lld workgroups of 256 threads; a launch holds fewer "
+                "than 2^32 threads)", name, (long long)groups);
+}
 
 int check_workspace(const char* name, void* ws, size_t bytes, size_t need) {
     if (!aligned_to(ws, 256)) return fail(KDA_ERR_MISALIGNED, "%s: workspace must be 256-byte aligned", name);
@@ -189,7 +195,8 @@ int kda_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_s
     const Pool kp = pool_of(k_pages, k_page_stride * es, page, n_pages);
     const Pool vp = pool_of(v_pages, v_page_stride * es, page, n_pages);
     if (int rc = check_pages(name, kp, vp, page_size, H_kv, d, dtype, true)) return rc;
-    if (T_total < 0 || T_total > kMaxGrid) return fail(KDA_ERR_INVALID_ARG, "%s: T_total must be in [0, 2^31)", name);
+    if (T_total < 0 || T_total > kMaxCount) return fail(KDA_ERR_INVALID_ARG, "%s: T_total must be in [0, 2^31)", name);
+    if (int rc = check_groups(name, kda::cache_append_groups(T_total, H_kv, d, (int)es))) return rc;
     if (!cu_seqlens && T_total != N)
         return fail(KDA_ERR_INVALID_ARG, "%s: without cu_seqlens T_total must be N", name);
     if (T_total > 0 && (N < 1 || !k || !v || !start))
@@ -231,7 +238,10 @@ size_t kda_paged_decode_workspace(int32_t N, int32_t H_q, int32_t H_kv, int32_t 
     if (N < 0 || H_kv <= 0 || H_kv > 1024 || H_q <= 0 || H_q % H_kv || H_q > 16384 || !valid_dtype(dtype) ||
         !kda::paged_decode_supported(d) || max_length < 0 || window < 0 || sinks < 0)
         return (size_t)-1;
-    return kda::paged_decode_workspace(N, H_q, H_kv, d, dtype == KDA_BF16, max_length, window, sinks);
+    size_t need;
+    const int64_t groups =
+        kda::paged_decode_groups(N, H_q, H_kv, d, dtype == KDA_BF16, max_length, window, sinks, &need);
+    return groups > kda::max_groups(256) ? (size_t)-1 : need;
 }
 
 int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int64_t k_page_stride,
@@ -255,19 +265,19 @@ int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const
     if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
         return fail(KDA_ERR_INVALID_ARG, "%s: window and sinks must be >= 0, and sinks 0 without a window", name);
     if (max_length < 0) return fail(KDA_ERR_INVALID_ARG, "%s: max_length must be >= 0", name);
-    if ((int64_t)N * H_q * ((int64_t)table_pages * page_size / 1024 + 2) > kMaxGrid)
-        return fail(KDA_ERR_INVALID_ARG, "%s: N * H_q times the table's tokens is too large", name);
     const int64_t room = (int64_t)table_pages * page_size;
     const int64_t most = max_length > 0 && max_length < room ? max_length : room;
     if (room > 0x7FFFFFFF - 4096)
         return fail(KDA_ERR_INVALID_ARG, "%s: table_pages * page_size must be below 2^31 - 4096", name);
+    size_t need;
+    if (int rc = check_groups(name, kda::paged_decode_groups(N, H_q, H_kv, d, dtype == KDA_BF16, most, window, sinks, &need)))
+        return rc;
     if (N > 0 && (!q || !lengths || !out)) return fail(KDA_ERR_INVALID_ARG, "%s: q, lengths and out are required", name);
     if (N > 1 && q_stride * es < row) return fail(KDA_ERR_INVALID_ARG, "%s: queries overlap (stride below H_q * d)", name);
     if (!aligned16(q) || (N > 1 && q_stride * es % 16))
         return fail(KDA_ERR_MISALIGNED, "%s: the rows of q must be 16-byte aligned", name);
     if (!aligned16(out) || !aligned_to(lse, 4) || !aligned_to(lengths, 4))
         return fail(KDA_ERR_MISALIGNED, "%s: out must be 16-byte, lse and lengths 4-byte aligned", name);
-    const size_t need = kda::paged_decode_workspace(N, H_q, H_kv, d, dtype == KDA_BF16, most, window, sinks);
     if (int rc = check_workspace(name, workspace, workspace_bytes, need)) return rc;
     const Span ins[] = {{q, extent(N, q_stride * es, row)}, kp.span(), vp.span(),
                         table_span(page_table, table_stride, N, table_pages), {lengths, (size_t)N * 4}};
@@ -298,6 +308,7 @@ int kda_cache_fork(const int32_t* page_table, int64_t table_stride, const int32_
         return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
     if (!refcount || (N > 0 && !lengths) || (N_out > 0 && (!parents || !lengths_out)))
         return fail(KDA_ERR_INVALID_ARG, "%s: refcount, lengths, parents and lengths_out are required", name);
+    if (int rc = check_groups(name, kda::cache_rows_groups(N > N_out ? N : N_out, table_pages))) return rc;
     const void* words[] = {lengths, refcount, parents, lengths_out};
     for (const void* p : words)
         if (!aligned_to(p, 4)) return fail(KDA_ERR_MISALIGNED, "%s: int32 buffers must be 4-byte aligned", name);
@@ -320,8 +331,8 @@ int kda_cache_free(int32_t* page_table, int64_t table_stride, int32_t* lengths, 
     static const char* name = "kda_cache_free";
     if (int rc = check_table(name, page_table, table_stride, N, table_pages, n_pages)) return rc;
     if (!sane_stride(table_stride)) return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
-    if (n_rows < 0 || (int64_t)n_rows * ((int64_t)table_pages / 256 + 2) > kMaxGrid)
-        return fail(KDA_ERR_INVALID_ARG, "%s: bad number of rows", name);
+    if (n_rows < 0) return fail(KDA_ERR_INVALID_ARG, "%s: the number of rows must be >= 0", name);
+    if (int rc = check_groups(name, kda::cache_rows_groups(n_rows, table_pages))) return rc;
     if (!refcount || (N > 0 && !lengths) || (n_rows > 0 && !rows))
         return fail(KDA_ERR_INVALID_ARG, "%s: refcount, lengths and rows are required", name);
     if (!aligned_to(lengths, 4) || !aligned_to(refcount, 4) || !aligned_to(rows, 4))
@@ -382,6 +393,7 @@ int kda_cache_compact(const int32_t* page_table, int64_t table_stride, int32_t N
         return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
     if (!refcount || !refcount_out || (n_pages > 1 && !moves))
         return fail(KDA_ERR_INVALID_ARG, "%s: refcount, refcount_out and moves are required", name);
+    if (int rc = check_groups(name, kda::cache_compact_groups(N, table_pages, n_pages))) return rc;
     const void* words[] = {refcount, refcount_out, moves};
     for (const void* p : words)
         if (!aligned_to(p, 4)) return fail(KDA_ERR_MISALIGNED, "%s: int32 buffers must be 4-byte aligned", name);
@@ -412,7 +424,7 @@ int kda_cache_compact(const int32_t* page_table, int64_t table_stride, int32_t N
 int kda_pages_copy(void* const* pools, const int64_t* page_strides, const int64_t* page_bytes, int32_t n_pools,
                    int32_t n_pages, const int32_t* pairs, int64_t n_pairs, void* hip_stream) {
     static const char* name = "kda_pages_copy";
-    if (n_pages < 0 || n_pairs < 0 || n_pairs > kMaxGrid)
+    if (n_pages < 0 || n_pairs < 0 || n_pairs > kMaxCount)
         return fail(KDA_ERR_INVALID_ARG, "%s: n_pages and n_pairs must be in [0, 2^31)", name);
     if (n_pools > 0 && !page_strides) return fail(KDA_ERR_INVALID_ARG, "%s: page_strides is required", name);
     if (int rc = read_pools(name, pools, page_strides, page_bytes, n_pools, n_pages)) return rc;
@@ -453,8 +465,7 @@ int kda_beam_select(const void* logits, int64_t row_stride, const float* scores,
     const int64_t rows = (int64_t)B * K, es = dtype == KDA_BF16 ? 2 : 4;
     if (!sane_stride(row_stride) || (rows > 1 && row_stride < V))
         return fail(KDA_ERR_INVALID_ARG, "%s: row_stride must be in [V, 2^40)", name);
-    if (rows * (((int64_t)V + 7) / 4096 + 1) > kMaxGrid)
-        return fail(KDA_ERR_INVALID_ARG, "%s: B * K * V is too large", name);
+    if (int rc = check_groups(name, kda::beam_select_groups(B, K, V))) return rc;
     if (!aligned_to(logits, es)) return fail(KDA_ERR_MISALIGNED, "%s: logits must be aligned to their element", name);
     const void* words[] = {scores, scores_out, parents, tokens};
     for (const void* p : words)
@@ -487,8 +498,6 @@ int kda_beam_reorder(void* const* states, const int64_t* row_bytes, int32_t n_st
     for (int32_t i = 0; i < n_states; ++i) {
         if (overlap(Span{states[i], (size_t)(rows * row_bytes[i])}, Span{parents, (size_t)rows * 4}))
             return fail(KDA_ERR_ALIAS, "%s: state %d overlaps parents", name, i);
-        if ((row_bytes[i] / 4096 + 1) * B * kda::kMaxPools > kMaxGrid)
-            return fail(KDA_ERR_INVALID_ARG, "%s: B times the row size is too large", name);
     }
     if (injected_launch_failure()) return injected(name);
     hipStream_t s = static_cast<hipStream_t>(hip_stream);

@@ -344,6 +344,9 @@ int kda_validate_gates(const float* g, int64_t n_g, const float* beta, int64_t n
  * left out and never makes a kernel read or write outside the caller's buffers.
  * All calls are deterministic: integer results do not depend on the order in
  * which workgroups run, and free pages are taken lowest first.
+ * A call that needs 2^32 or more threads in one launch is refused
+ * (KDA_ERR_INVALID_ARG; some 2^24 sequences, table rows or query heads, or 2^28
+ * short tokens); kda_pages_copy and kda_beam_reorder go on in further launches.
  */
 
 /*

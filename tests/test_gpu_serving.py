@@ -623,6 +623,25 @@ def test_pages_copy_of_strided_pools_and_states():
     assert torch.equal(states.cpu(), want)
 
 
+def test_pages_copy_of_lists_longer_than_a_launch():
+    """More than 2^26 workgroups of 64 threads, which is more than a grid holds: two slices of the list.  Pages of
+    2 MiB are 512 pieces, so 2^20 + 9 pairs an eighth apart make 2^26 + 1024 workgroups."""
+    pool = torch.randn(24, 1 << 19, generator=gen(3)).to(DEV)
+    n = (1 << 20) + 9
+    pairs = torch.full((n, 2), -1, dtype=torch.int32)
+    apart = -(-n // 8)
+    want = pool.clone()
+    # the list's ends, and both sides of the slices' border in every eighth of it
+    at = [0, n - 1] + [i * apart + x for i in range(8) for x in (((1 << 26) - 1) // 512 - 1, ((1 << 26) - 1) // 512)]
+    at = sorted({x for x in at if x < n})
+    assert len(at) == 16 and apart * 512 > (1 << 26) - 1
+    for to, x in enumerate(at, start=6):
+        pairs[x] = torch.tensor([to % 6, to], dtype=torch.int32)
+        want[to] = want[to % 6]
+    kda.pages_copy(pool, pairs.to(DEV))
+    assert torch.equal(pool, want)
+
+
 # ------------------------------------------------------------------------------------------------
 # beam search
 # ------------------------------------------------------------------------------------------------
@@ -828,6 +847,19 @@ def test_beam_reorder(B, K, row):
     assert torch.equal(a.cpu(), want_a) and torch.equal(b.cpu(), want_b)
     kda.beam_reorder(a, torch.arange(K, dtype=torch.int32, device=DEV).expand(B, K).contiguous())
     assert torch.equal(a.cpu(), want_a)
+
+
+def test_beam_reorder_of_more_groups_than_a_launch():
+    """2^24 + 5 groups of two short rows: more workgroups of 256 threads than a grid holds."""
+    B = (1 << 24) + 5
+    a = torch.arange(4 * 2 * B, dtype=torch.int32, device=DEV).view(B, 2, 4)
+    parents = torch.randint(-1, 3, (B, 2), generator=gen(4), dtype=torch.int32).to(DEV)
+    keep = torch.arange(2, device=DEV)
+    at = torch.where((parents >= 0) & (parents < 2), parents, keep).long()
+    want = torch.gather(a, 1, at[:, :, None].expand(B, 2, 4))
+    states = a.view(2 * B, 4).clone()
+    kda.beam_reorder(states, parents)
+    assert torch.equal(states.view(B, 2, 4), want)
 
 
 # ------------------------------------------------------------------------------------------------

@@ -126,6 +126,52 @@ def test_the_unchanged_calls_pass_validation(monkeypatch, name, defaults):
     assert _call(L, name, defaults) == _l.KDA_ERR_HIP and b"injected" in L.kda_last_error()
 
 
+FAR = [1 << 45, 1 << 46, 1 << 47]  # fake buffers far enough apart for the largest calls
+
+
+@pytest.mark.parametrize("name,defaults,at_most,one_more", [
+    ("kda_cache_append", dict(APPEND, cu=P[6], k=FAR[0], v=FAR[1], H=1, d=64, k_stride=64, v_stride=64, kp_stride=1024,
+                              vp_stride=1024), dict(T=(1 << 28) - 16), dict(T=1 << 28)),
+    ("kda_paged_decode", dict(DECODE, Hq=1, Hkv=1, d=64, q_stride=64, kp_stride=1024, vp_stride=1024),
+     dict(N=(1 << 24) - 1), dict(N=1 << 24)),
+    # 4096 tokens are two parts, and the launch that joins them has a workgroup for every query head
+    ("kda_paged_decode", dict(DECODE, Hq=128, Hkv=8, d=64, q_stride=128 * 64, kp_stride=8 << 18, vp_stride=8 << 18,
+                              n_pages=2, page=4096, width=1, ws=FAR[0], ws_bytes=1 << 40),
+     dict(N=(1 << 17) - 1), dict(N=1 << 17)),
+    ("kda_cache_fork", dict(FORK, width=1 << 26, stride=1 << 26, out_stride=1 << 26, N=0, table=None, out=FAR[0]),
+     dict(N_out=63), dict(N_out=64)),
+    ("kda_cache_free", FREE, dict(n_rows=(1 << 24) - 1), dict(n_rows=1 << 24)),
+    ("kda_cache_compact", dict(COMPACT, ws_bytes=1 << 30), dict(N=(1 << 24) - 2), dict(N=(1 << 24) - 1)),
+    ("kda_beam_select", dict(SELECT, K=1, V=4, row=4, n_out=1), dict(B=(1 << 24) - 1), dict(B=1 << 24)),
+])
+def test_calls_whose_launch_has_2_to_32_threads_are_refused(monkeypatch, name, defaults, at_most, one_more):
+    """A grid holds fewer than 2^32 threads, 2^24 - 1 workgroups of 256."""
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    assert _call(L, name, defaults, **at_most) == _l.KDA_ERR_HIP and b"injected" in L.kda_last_error()
+    assert _call(L, name, defaults, **one_more) == _l.KDA_ERR_INVALID_ARG and b"2^32" in L.kda_last_error()
+
+
+def test_sizes_whose_products_leave_64_bits_are_refused(monkeypatch):
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    most = 2 ** 31 - 1
+    assert _call(L, "kda_paged_decode", DECODE, N=most, Hq=16384, q_stride=16384 * 128, page=4096,
+                 kp_stride=4 * 4096 * 128, vp_stride=4 * 4096 * 128, width=most, stride=most) == _l.KDA_ERR_INVALID_ARG
+    assert L.kda_paged_decode_workspace(most, 16384, 1, 128, 1, most, 0, 0) == 2 ** 64 - 1
+    assert L.kda_paged_decode_workspace(1 << 24, 1, 1, 128, 1, 64, 0, 0) == 2 ** 64 - 1
+
+
+def test_calls_with_wide_tables_and_few_tokens_are_taken(monkeypatch):
+    """16384 sequences of 128 heads with room for 2^20 tokens each, of which no more than 4096 are used."""
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    need = L.kda_paged_decode_workspace(16384, 128, 8, 128, 1, 4096, 0, 0)
+    kw = dict(N=16384, Hq=128, Hkv=8, q_stride=128 * 128, kp_stride=8 * 128 * 128, vp_stride=8 * 128 * 128, page=128,
+              width=8192, stride=8192, max_length=4096, q=FAR[0], out=FAR[1], ws=FAR[2], ws_bytes=need)
+    assert _call(L, "kda_paged_decode", DECODE, **kw) == _l.KDA_ERR_HIP and b"injected" in L.kda_last_error()
+
+
 def test_pages_of_keys_and_values_may_interleave(monkeypatch):
     """Keys and values in one pool [n_pages, 2, H, page_size, d]: the extents overlap, the pages do not."""
     _l, L = _lib()
