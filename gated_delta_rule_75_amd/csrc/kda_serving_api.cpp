@@ -53,18 +53,22 @@ bool overlap(const Pool& a, const Pool& b) {
     return fwd < a.page || a.stride - fwd < b.page;
 }
 
+// strides and sizes small enough that no byte offset leaves 63 bits
+bool sane_stride(int64_t elements) { return elements >= 0 && elements < ((int64_t)1 << 40); }
+
 int check_table(const char* name, const int32_t* table, int64_t stride, int64_t N, int32_t width, int32_t n_pages) {
     if (N < 0 || width < 0) return fail(KDA_ERR_INVALID_ARG, "%s: sizes must be >= 0", name);
     if (n_pages < 1 || n_pages >= kMaxPages)
         return fail(KDA_ERR_INVALID_ARG, "%s: n_pages must be in [1, 2^24)", name);
     if (N > 0 && width > 0 && !table) return fail(KDA_ERR_INVALID_ARG, "%s: a page table is required", name);
     if (N > 1 && stride < width) return fail(KDA_ERR_INVALID_ARG, "%s: table rows overlap (stride below the width)", name);
+    if (N > 1 && !sane_stride(stride)) return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
     if (!aligned_to(table, 4)) return fail(KDA_ERR_MISALIGNED, "%s: the page table must be 4-byte aligned", name);
     return KDA_OK;
 }
 
 Span table_span(const int32_t* t, int64_t stride, int64_t N, int32_t width) {
-    return Span{t, width > 0 ? extent(N, stride * 4, (int64_t)width * 4) : 0};
+    return Span{t, width > 0 ? extent(N, N > 1 ? stride * 4 : 0, (int64_t)width * 4) : 0};
 }
 
 int check_pages(const char* name, const Pool& k, const Pool& v, int32_t page_size, int32_t H, int32_t d,
@@ -82,9 +86,6 @@ int check_pages(const char* name, const Pool& k, const Pool& v, int32_t page_siz
     if (written && overlap(k, v)) return fail(KDA_ERR_ALIAS, "%s: k_pages and v_pages overlap", name);
     return KDA_OK;
 }
-
-// strides and sizes small enough that no byte offset leaves 63 bits
-bool sane_stride(int64_t elements) { return elements >= 0 && elements < ((int64_t)1 << 40); }
 
 // A launch of the call would not fit a grid.
 int check_groups(const char* name, int64_t groups) {

@@ -335,6 +335,7 @@ int kda_validate_gates(const float* g, int64_t n_g, const float* beta, int64_t n
  *                     outside [0, n_pages) means that there is no page (write
  *                     -1): attention leaves its tokens out, writes to it are
  *                     dropped.
+ *                     Strides of all calls are below 2^40 elements.
  *   lengths           int32 [N], tokens of each sequence
  *   refcount          int32 [n_pages]: how many table entries (of all tables of
  *                     the pool) name the page; 0 means that it is free.  There

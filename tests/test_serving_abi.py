@@ -152,6 +152,21 @@ def test_calls_whose_launch_has_2_to_32_threads_are_refused(monkeypatch, name, d
     assert _call(L, name, defaults, **one_more) == _l.KDA_ERR_INVALID_ARG and b"2^32" in L.kda_last_error()
 
 
+@pytest.mark.parametrize("name,defaults", [("kda_cache_append", APPEND), ("kda_paged_decode", DECODE),
+                                           ("kda_cache_fork", FORK), ("kda_cache_free", FREE),
+                                           ("kda_cache_reserve", RESERVE), ("kda_cache_compact", COMPACT)])
+@pytest.mark.parametrize("stride", [1 << 40, 1 << 61, 1 << 62, 2 ** 63 - 1])
+def test_table_strides_beyond_2_to_40_are_refused(monkeypatch, name, defaults, stride):
+    """In bytes such a stride can wrap to a small one, past the check for overlaps."""
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    assert _call(L, name, defaults, stride=stride) == _l.KDA_ERR_INVALID_ARG and b"stride" in L.kda_last_error()
+    # a single row has no stride
+    if name in ("kda_cache_append", "kda_paged_decode"):
+        one = dict(N=1, T=1) if name == "kda_cache_append" else dict(N=1)
+        assert _call(L, name, defaults, stride=stride, **one) == _l.KDA_ERR_HIP, L.kda_last_error()
+
+
 def test_sizes_whose_products_leave_64_bits_are_refused(monkeypatch):
     _l, L = _lib()
     monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
