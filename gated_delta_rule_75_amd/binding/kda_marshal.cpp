@@ -480,4 +480,17 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_marshal", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kda_marshal(void) { return PyModule_Create(&module); }
+#define KDA_TEXT_(x) #x
+#define KDA_TEXT(x) KDA_TEXT_(x)
+
+// The versions that the module was built for: serving.py uses it with these only.
+PyMODINIT_FUNC PyInit__kda_marshal(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && (PyModule_AddStringConstant(m, "torch_version", KDA_TORCH_VERSION) < 0 ||
+              PyModule_AddStringConstant(m, "python_version",
+                                         KDA_TEXT(PY_MAJOR_VERSION) "." KDA_TEXT(PY_MINOR_VERSION)) < 0)) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -63,19 +63,34 @@ def build_library(verbose: bool = False, jobs: int = 8) -> str:
     return LIB
 
 
-def build_marshal(verbose: bool = False) -> str:
-    """Compile binding/kda_marshal.cpp (host code against torch's headers) to ``_kda_marshal.so``."""
+def build_marshal(verbose: bool = False):
+    """Compile binding/kda_marshal.cpp (host code against torch's headers) to ``_kda_marshal.so``.
+
+    Returns its path, or None where there is no g++ or a header is missing: the binding then marshals in
+    Python, with the same results."""
     import sysconfig
 
     import torch
 
     base = os.path.dirname(torch.__file__)
+    python = sysconfig.get_paths()["include"]
+    missing = [] if shutil.which("g++") else ["g++"]
+    missing += [h for h in (os.path.join(python, "Python.h"),
+                            os.path.join(base, "include", "torch", "csrc", "autograd", "python_variable.h"))
+                if not os.path.exists(h)]
+    if missing:
+        if os.path.exists(MARSHAL):  # it may not fit the library that has just been built
+            os.remove(MARSHAL)
+        print(f"{os.path.basename(MARSHAL)} not built (no {', '.join(missing)}); the calls are marshalled in Python",
+              flush=True)
+        return None
     tmp = MARSHAL + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], os.path.join(PKG, "binding", "kda_marshal.cpp"), "-o", tmp,
+           f'-DKDA_TORCH_VERSION="{torch.__version__}"',
+           "-isystem", python, os.path.join(PKG, "binding", "kda_marshal.cpp"), "-o", tmp,
            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)

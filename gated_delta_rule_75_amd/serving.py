@@ -12,6 +12,8 @@ the library's HIP kernels on the current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import sys
+import warnings
 
 import torch
 
@@ -34,6 +36,14 @@ def _lib_():
         try:
             from . import _kda_marshal
         except ImportError:
+            return _LIB
+        # it reads torch's and CPython's structures, so it serves the versions that it was built for only
+        here = (torch.__version__, "%d.%d" % tuple(sys.version_info[:2]))
+        built = (getattr(_kda_marshal, "torch_version", "?"), getattr(_kda_marshal, "python_version", "?"))
+        if here != built:
+            warnings.warn("_kda_marshal.so was built for torch %s, python %s, and this is torch %s, python %s: the "
+                          "serving calls are marshalled in Python until it is built again" % (*built, *here),
+                          RuntimeWarning)
             return _LIB
         _kda_marshal.setup(_RAW_STREAM or _stream_of, _lib.check,
                            {n: ctypes.cast(getattr(_LIB, n), ctypes.c_void_p).value for n in _lib.EXPORTS})

@@ -295,3 +295,47 @@ def test_binding_refuses_host_and_misshapen_tensors():
         _rows(torch.zeros(4, 64, 4).transpose(1, 2), "x", torch.Size((4, 4, 64)))
     with pytest.raises(ValueError, match="shape"):
         _rows(x, "x", torch.Size((2, 4, 32)))
+
+
+@pytest.mark.parametrize("what", ["torch", "python"])
+def test_a_marshalling_module_built_for_another_torch_or_python_is_not_used(monkeypatch, what):
+    """The module reads torch's and CPython's structures: one that was built for others is left aside with a
+    warning, and the calls are marshalled in Python."""
+    import sys
+
+    _lib()
+    from gated_delta_rule_75_amd import build, serving
+
+    if not os.path.exists(build.MARSHAL):
+        pytest.skip("marshalling module not built")
+    monkeypatch.setattr(serving, "_LIB", None)
+    monkeypatch.setattr(serving, "_M", None)
+    serving._lib_()
+    assert serving._M is not None
+    monkeypatch.setattr(serving, "_LIB", None)
+    monkeypatch.setattr(serving, "_M", None)
+    if what == "torch":
+        monkeypatch.setattr(torch, "__version__", "1.2.3")
+    else:
+        monkeypatch.setattr(sys, "version_info", (2, 7, 0))
+    with pytest.warns(RuntimeWarning, match=what):
+        assert serving._lib_() is not None
+    assert serving._M is None
+
+
+@pytest.mark.parametrize("missing", ["compiler", "headers"])
+def test_the_build_goes_on_without_the_marshalling_module(monkeypatch, tmp_path, capsys, missing):
+    """Without g++ or the headers the library is complete; a module of an earlier build is taken away."""
+    import sysconfig
+
+    from gated_delta_rule_75_amd import build
+
+    old = tmp_path / "_kda_marshal.so"
+    old.write_bytes(b"old")
+    monkeypatch.setattr(build, "MARSHAL", str(old))
+    if missing == "compiler":
+        monkeypatch.setattr(build.shutil, "which", lambda name: None)
+    else:
+        monkeypatch.setattr(sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    assert build.build_marshal() is None
+    assert not old.exists() and "not built" in capsys.readouterr().out
