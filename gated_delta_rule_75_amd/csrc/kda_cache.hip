@@ -169,19 +169,23 @@ __global__ __launch_bounds__(kTableThreads) void free_kernel(CacheFreeArgs a, ui
 // Workspace of reserve and compact.  `bits`: one bit per page (free pages for reserve, used ones
 // for compact); `shared`: one bit per page with more than one reference when the call began (reserve);
 // `before`: set bits of the word's block before the word; `block`: set bits of the block; `aux`: per
-// sequence the number of pages needed (reserve), or the counts of the moved pages (compact).
+// sequence the number of pages needed (reserve), or the counts of the moved pages (compact); `sums`: the
+// pages needed before each group of sequences (reserve, many sequences).
 struct CacheWs {
     uint64_t* bits;
     uint64_t* shared;
     uint32_t* before;
     int32_t* block;
     int32_t* aux;
+    int32_t* sums;
     int words, blocks;
 };
 
 __host__ __device__ inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-__host__ __device__ inline CacheWs cache_ws(void* ws, int64_t n_pages) {
+__host__ __device__ inline int64_t aux_entries(int64_t N, int64_t n_pages) { return N > n_pages / 2 ? N : n_pages / 2; }
+
+__host__ __device__ inline CacheWs cache_ws(void* ws, int64_t N, int64_t n_pages) {
     CacheWs w;
     const int64_t blocks = up(n_pages, kBlockPages) / kBlockPages, words = blocks * kBlockWords;
     char* p = static_cast<char*>(ws);
@@ -189,7 +193,10 @@ __host__ __device__ inline CacheWs cache_ws(void* ws, int64_t n_pages) {
     w.shared = reinterpret_cast<uint64_t*>(p + words * 8);
     w.before = reinterpret_cast<uint32_t*>(p + words * 16);
     w.block = reinterpret_cast<int32_t*>(p + words * 20);
-    w.aux = reinterpret_cast<int32_t*>(p + words * 20 + up(blocks * 4, 16));
+    // (no rounding up in between: the compiler took it apart into an address that is no multiple of 4 and an
+    // offset of 15, whose low bits a scalar load drops, each for itself)
+    w.aux = w.block + blocks;
+    w.sums = w.aux + aux_entries(N, n_pages);
     w.words = (int)words;
     w.blocks = (int)blocks;
     return w;
@@ -315,7 +322,7 @@ template <bool FREE>
 __device__ __forceinline__ CacheWs small_scan(const int32_t* refs, int n_pages, SmallScan& s) {
     constexpr int kWords = kSmallBlocks * kBlockWords, kPer = kWords / (kSmallThreads / 64);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    CacheWs w{s.bits, s.shared, s.before, s.block, s.aux, kWords, kSmallBlocks};
+    CacheWs w{s.bits, s.shared, s.before, s.block, s.aux, nullptr, kWords, kSmallBlocks};
     int32_t r[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -359,9 +366,14 @@ __device__ __forceinline__ CacheWs small_scan(const int32_t* refs, int n_pages, 
 // ------------------------------------------------------------------------------------------
 // First launch: the blocks' scans, and one wave per sequence that counts the pages it needs.  The scan
 // also keeps a bit for every shared page, which carries the verdict on the counts as they were when
-// the call began over to the second launch, which changes them.  Nothing of a table is written before it
+// the call began over to the last launch, which changes them.  Nothing of a table is written before it
 // is known whether its sequence is served, so one that is not keeps every entry, whatever it holds.
 constexpr int kRowsPerGroup = kScanThreads / 64;
+// Sequences up to which every group of the second launch adds up the needs before it, which grows with
+// their square; for more a launch between the two does it once (reserve_sums_kernel).  Kernel time of the
+// call without and with that launch: 21.6 and 24.0 us for 8192 sequences, 29.1 and 29.4 for 12 288, 36.2 and 34.0
+// for 16 384, 2.07 and 0.35 ms for 262 144.
+constexpr int64_t kDirectRows = 12288;
 
 // columns that hold the new tokens' positions; none where nothing is to be reserved, bad where the
 // row is too narrow
@@ -427,7 +439,7 @@ __device__ __forceinline__ int2 take_pages(const CacheReserveArgs& a, const Cach
 }
 
 __global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserveArgs a) {
-    const CacheWs w = cache_ws(a.ws, a.n_pages);
+    const CacheWs w = cache_ws(a.ws, a.N, a.n_pages);
     if ((int)blockIdx.x < w.blocks) {
         scan_block<true>(a.refs, a.n_pages, w, blockIdx.x);
         return;
@@ -439,19 +451,62 @@ __global__ __launch_bounds__(kScanThreads) void reserve_scan_kernel(CacheReserve
     if ((threadIdx.x & 63) == 0) w.aux[n] = s.bad ? -1 : need;
 }
 
+// Pages needed before each group of sequences, by one workgroup that keeps the running sum.  A sum stops at
+// kNoPages, more than a pool has, so that it fits 32 bits however much is asked for.
+constexpr int kSumThreads = 1024;
+constexpr int32_t kNoPages = 1 << 30;
+
+__global__ __launch_bounds__(kSumThreads) void reserve_sums_kernel(CacheReserveArgs a) {
+    __shared__ int64_t s_wave[2][kSumThreads / 64];
+    const CacheWs w = cache_ws(a.ws, a.N, a.n_pages);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t groups = (a.N + kRowsPerGroup - 1) / kRowsPerGroup;
+    int64_t carry = 0;
+    for (int64_t g0 = 0, turn = 0; g0 < groups; g0 += kSumThreads, turn ^= 1) {
+        const int64_t g = g0 + threadIdx.x;
+        int64_t own = 0;
+#pragma unroll
+        for (int i = 0; i < kRowsPerGroup; ++i) {
+            const int64_t n = g * kRowsPerGroup + i;
+            const int32_t need = w.aux[n < a.N ? n : a.N - 1];
+            own += n < a.N && need > 0 ? need : 0;
+        }
+        int64_t x = own;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int64_t y = __shfl_up(x, off, 64);
+            if (lane >= off) x += y;
+        }
+        if (lane == 63) s_wave[turn][wave] = x;
+        __syncthreads();  // (the other half of s_wave is written next, so one barrier a turn is enough)
+        int64_t before = carry, all = carry;
+        for (int i = 0; i < kSumThreads / 64; ++i) {
+            before += i < wave ? s_wave[turn][i] : 0;
+            all += s_wave[turn][i];
+        }
+        before += x - own;
+        if (g < groups) w.sums[g] = before < kNoPages ? (int32_t)before : kNoPages;
+        carry = all < kNoPages ? all : kNoPages;
+    }
+}
+
 // Second launch: one wave per sequence.  Its first page is the free one whose rank is the sum of the
 // needs before it.
 __global__ __launch_bounds__(kScanThreads) void reserve_kernel(CacheReserveArgs a) {
     __shared__ int32_t s_prefix[kMaxBlocks + 1];
     __shared__ int64_t s_sum[kRowsPerGroup];
-    const CacheWs w = cache_ws(a.ws, a.n_pages);
+    const CacheWs w = cache_ws(a.ws, a.N, a.n_pages);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n0 = (int64_t)blockIdx.x * kRowsPerGroup, n = n0 + wave;
     // pages needed by the sequences before this group
     int64_t sum = 0;
-    for (int64_t i = threadIdx.x; i < n0; i += kScanThreads) sum += w.aux[i] > 0 ? w.aux[i] : 0;
+    if (a.N <= kDirectRows) {
+        for (int64_t i = threadIdx.x; i < n0; i += kScanThreads) sum += w.aux[i] > 0 ? w.aux[i] : 0;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    } else if (wave == 0) {
+        sum = w.sums[blockIdx.x];
+    }
     if (lane == 0) s_sum[wave] = sum;
     block_prefix(w, s_prefix);  // ends with a barrier
     if (n >= a.N) return;
@@ -554,7 +609,7 @@ __global__ __launch_bounds__(kSmallThreads) void reserve_small_kernel(CacheReser
 // behind it; there are as many of one as of the other, and sources and targets are disjoint, so the
 // copies can run in any order.
 __global__ __launch_bounds__(kScanThreads) void compact_scan_kernel(CacheCompactArgs a) {
-    scan_block<false>(a.refs, a.pt.n_pages, cache_ws(a.ws, a.pt.n_pages), blockIdx.x);
+    scan_block<false>(a.refs, a.pt.n_pages, cache_ws(a.ws, a.N, a.pt.n_pages), blockIdx.x);
 }
 
 // page p's part in the moves (pages before p, and before the number L of used pages: `front`)
@@ -592,7 +647,7 @@ __device__ __forceinline__ void remap_entry(const CacheCompactArgs& a, const Cac
 
 __global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(CacheCompactArgs a) {
     __shared__ int32_t s_prefix[kMaxBlocks + 1];
-    const CacheWs w = cache_ws(a.ws, a.pt.n_pages);
+    const CacheWs w = cache_ws(a.ws, a.N, a.pt.n_pages);
     block_prefix(w, s_prefix);
     const int32_t L = s_prefix[w.blocks], front = bits_before(w, s_prefix, L);
     const int p = blockIdx.x * kScanThreads + threadIdx.x;
@@ -602,7 +657,7 @@ __global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(CacheCompact
 __global__ __launch_bounds__(kScanThreads) void compact_remap_kernel(CacheCompactArgs a, int count_groups,
                                                                      int col_groups) {
     __shared__ int32_t s_prefix[kMaxBlocks + 1];
-    const CacheWs w = cache_ws(a.ws, a.pt.n_pages);
+    const CacheWs w = cache_ws(a.ws, a.N, a.pt.n_pages);
     block_prefix(w, s_prefix);
     const int32_t L = s_prefix[w.blocks];
     if ((int)blockIdx.x < count_groups) {
@@ -747,8 +802,8 @@ hipError_t launch_cache_free(const CacheFreeArgs& a, hipStream_t s) {
 }
 
 size_t cache_workspace(int64_t N, int64_t n_pages) {
-    const int64_t blocks = div_up(n_pages, kBlockPages), aux = N > n_pages / 2 ? N : n_pages / 2;
-    return (size_t)up(blocks * kBlockWords * 20 + up(blocks * 4, 16) + aux * 4, 256);
+    const int64_t blocks = div_up(n_pages, kBlockPages), sums = div_up(N, kRowsPerGroup);
+    return (size_t)up(blocks * kBlockWords * 20 + (blocks + aux_entries(N, n_pages) + sums) * 4, 256);
 }
 
 hipError_t launch_cache_reserve(const CacheReserveArgs& a, hipStream_t s) {
@@ -761,6 +816,10 @@ hipError_t launch_cache_reserve(const CacheReserveArgs& a, hipStream_t s) {
     hipError_t e = timed_launch(kKernelCacheScan, s, [&] {
         hipLaunchKernelGGL(reserve_scan_kernel, dim3((unsigned)(blocks + groups)), dim3(kScanThreads), 0, s, a);
     });
+    if (e == hipSuccess && a.N > kDirectRows)
+        e = timed_launch(kKernelCacheScan, s, [&] {
+            hipLaunchKernelGGL(reserve_sums_kernel, dim3(1), dim3(kSumThreads), 0, s, a);
+        });
     if (e != hipSuccess) return e;
     return timed_launch(kKernelCacheReserve, s, [&] {
         hipLaunchKernelGGL(reserve_kernel, dim3((unsigned)groups), dim3(kScanThreads), 0, s, a);

@@ -537,6 +537,34 @@ def test_reserve_leaves_a_sequence_that_is_not_served_as_it_was(n, width, n_page
     assert T.tolist() == want_table and R.tolist() == want_refs
 
 
+@pytest.mark.parametrize("n,free", [(4099, 10 ** 6), (70001, 60000), (70001, 10 ** 6), ((1 << 22) + 3, 5 * 10 ** 6)])
+def test_reserve_for_many_sequences(n, free):
+    """Up to millions of sequences of two columns, of which some ask for nothing and some for more than their
+    row holds; pages for all, or for the first ones.  (The sums over the sequences before each one have to
+    grow with the sequences, not with their square.)"""
+    g = gen(n)
+    n_pages = 9 * 10 ** 6
+    refs = torch.ones(n_pages, dtype=torch.int32)
+    refs[torch.randperm(n_pages, generator=g)[:free]] = 0
+    new = torch.randint(-5, 40, (n,), generator=g, dtype=torch.int32)
+    refs, new = refs.to(DEV), new.to(DEV)
+    ids = torch.nonzero(refs == 0).flatten()
+    need = torch.where((new > 0) & (new <= 32), (new + 15) // 16, 0).long()
+    base = torch.cumsum(need, 0) - need
+    served = (need > 0) & (base + need <= free)
+    want = torch.full((n, 2), -1, dtype=torch.int32, device=DEV)
+    for j in (0, 1):
+        has = served & (need > j)
+        want[has, j] = ids[(base + j)[has]].to(torch.int32)
+    want_refs = refs.clone()
+    want_refs[want[want >= 0].long()] = 1
+    table = torch.full((n, 2), -1, dtype=torch.int32, device=DEV)
+    lengths = torch.zeros(n, dtype=torch.int32, device=DEV)
+    copies, granted = kda.cache_reserve(table, lengths, refs, new, 16)
+    assert torch.equal(table, want) and torch.equal(refs, want_refs) and bool((copies == -1).all())
+    assert torch.equal(granted, torch.where(served, new, 0)) and torch.equal(lengths, granted)
+
+
 def test_cache_calls_leave_the_rest_of_wider_buffers_alone():
     wide = torch.full((4, 20), 77, dtype=torch.int32, device=DEV)
     T = wide[:, 4:9]
