@@ -11,9 +11,14 @@
 //    takes one part of one key-value head for 16 or 32 of its query heads, each wave every fourth
 //    step of it.  With few sequences the parts get short, so that the chip is filled; their partial
 //    results (m, l, unnormalised out) are joined by a second launch.
-//  * A wave reads the page numbers of all its tiles with one load at the start, then keeps the tiles
-//    of the next step in flight in registers while it works on this one.  Nothing goes through
-//    LDS before the end.
+//  * A wave reads the page numbers of all its tiles with one load at the start; its tiles go straight to
+//    registers, and nothing goes through LDS before the end.  bf16 with D <= 128 has the next step's tiles
+//    in flight while it works on this one.  fp32 does not: the compiler moves their loads behind the
+//    score products and the softmax, so that only the second product covers them.  With long sequences the
+//    other waves of the SIMD make up for it (64 sequences of 8192 tokens, 8 key heads: bf16 5.8 TB/s, fp32 6.0 at
+//    D = 128 and 5.8 at 64), with short parts they do not (48 sequences with a window of 1024, 4 key heads,
+//    D = 64, fp32: 4.1).  D = 256 loads a step and then works on it: bf16 with all 24 loads out first (6.1
+//    TB/s), fp32 with two or three between the products at a time (5.5).
 //  * Scores are K Q^T on the matrix cores, tokens as rows and query heads as columns.  The result
 //    leaves four consecutive tokens of one head in each lane, which is how the next product wants
 //    them: out^T = V^T P^T sums over tokens in any order, so a lane's own tokens serve as its
@@ -22,9 +27,10 @@
 //    (D / 16) lane + c, which the write of the result undoes.  Maxima, sums and rescaling are per
 //    head, which is per lane.
 //  * bf16: the weights go into the second product as the sum of three bf16 (each what the ones before
-//    left), which is the fp32 weight to 2^-26.  One would show in the fp32 result (2^-9), and two still
-//    doubled its error (2^-18 a weight: 7 to 9e-7 against 4 to 5e-7 relative for the output; the time
-//    is the same, the matrix cores wait for memory).
+//    left).  The first leaves 2^-8 of a weight at most, the second 2^-17, the third nothing: its 8 bits
+//    hold what is left of 24 (from 2^-103 up, where the last bit is still a normal number).  One would show
+//    in the fp32 result, and two still doubled its error (7 to 9e-7 against 4 to 5e-7 relative for the
+//    output; the time is the same, the matrix cores wait for memory).
 //  * Loads are bounded by descriptors that end with the tile's last visible token (none for a tile
 //    without a page), and rows before the first visible one are replaced by it, so no slot that is
 //    not visible is ever used, whatever it holds.
@@ -131,7 +137,7 @@ __global__ __launch_bounds__(kThreads, HT == 2 && D == 128 ? 1 : 2) void paged_d
     using S = Step<T, D>;
     constexpr bool kBf16 = std::is_same<T, uint16_t>::value;
     constexpr int NT = S::NT, KS = S::KS, VEC = S::VEC, ES = sizeof(T);
-    constexpr bool kAhead = D <= 128;  // D = 256: a step already is 32 KB a wave, and has no registers to spare
+    constexpr bool kAhead = D <= 128;  // D = 256: a step is 32 KB a wave, twice that has no registers (229 of 256 used)
     constexpr int kRow = D + 4;        // LDS row of a head, shifted by one 16-byte bank group per head
     __shared__ __attribute__((aligned(16))) float s_o[2][16][kRow];
     __shared__ float s_m[kWaves][16 * HT], s_l[kWaves][16 * HT];
@@ -526,6 +532,12 @@ PartPlan part_plan(int64_t N, int Hq, int Hkv, int d, int bf16, int64_t max_leng
         // three steps and the join as four.  Against the rule below, whole calls: 13.4 and 21.3 us for 100
         // sequences with a window of 512, 14.1 and 17.7 for a lone one of 9000 tokens, 20.6 and 33.9 for one
         // of 30000 in fp32; at worst 25.9 and 24.4, for 48 with a window of 1024 in fp32.
+        // Two sequences may differ, but half of the launch at least follows the longer one, and the rule below
+        // aims at workgroups for many: 11.9 and 12.3 us for two of 3000 tokens (fp32 16.0 and 23.9), 16.3 and
+        // 16.9 for 9000 and 300 (fp32 23.5 and 27.8), 26.8 and 29.4 for 30 000 and 1000 (fp32 48.1 and 52.2),
+        // 40.7 and 41.4 for two of 30 000; equal from there on.
+        // Resident workgroups: 256 CUs times the waves of a SIMD, which are what 512 registers hold of 134 (D = 64),
+        // 371 (D = 128 with 32 heads) or 196 to 236 (the others) each.
         const int64_t slots = 256 * (d == 64 && p.heads == 16 ? 3 : d == 128 && p.heads == 32 ? 1 : 2);
         int64_t best = 0;
         for (int64_t steps = 1; steps * step_tiles <= kMaxPartTiles; ++steps) {

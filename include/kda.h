@@ -389,7 +389,7 @@ int kda_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_s
  * gives out = 0 and lse = -inf.  Tokens that are not visible are never used,
  * whatever bits their slots hold.  Products are exact in bf16 with fp32 sums;
  * with KDA_BF16 the softmax weights enter their product as the sum of three bf16
- * values (within 2^-24 of the fp32 weight).  A visible key or value that is not
+ * values, which is the fp32 weight itself (from 2^-103 up).  A visible key or value that is not
  * finite makes what it enters NaN, but for a score of -inf, which has weight 0.
  * workspace: kda_paged_decode_workspace bytes for the same arguments, 256-byte
  * aligned, overlapping no argument; holds the partial results where a sequence
