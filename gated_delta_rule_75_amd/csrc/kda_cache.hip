@@ -783,6 +783,10 @@ hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t s) {
 
 int64_t cache_rows_groups(int64_t rows, int width) { return rows * (width ? div_up(width, kTableThreads) : 1); }
 
+int64_t cache_reserve_groups(int64_t N, int64_t n_pages) {
+    return div_up(n_pages, kBlockPages) + div_up(N, kRowsPerGroup);
+}
+
 int64_t cache_compact_groups(int64_t N, int width, int64_t n_pages) {
     return div_up(n_pages, kScanThreads) + N * div_up(width, kScanThreads);
 }

@@ -221,6 +221,7 @@ struct CacheReserveArgs {
     int32_t* granted;
     void* ws;
 };
+int64_t cache_reserve_groups(int64_t N, int64_t n_pages);
 hipError_t launch_cache_reserve(const CacheReserveArgs& a, hipStream_t s);
 
 struct CacheCompactArgs {

@@ -271,8 +271,9 @@ int kda_paged_decode(const void* q, int64_t q_stride, const void* k_pages, const
     if (room > 0x7FFFFFFF - 4096)
         return fail(KDA_ERR_INVALID_ARG, "%s: table_pages * page_size must be below 2^31 - 4096", name);
     size_t need;
-    if (int rc = check_groups(name, kda::paged_decode_groups(N, H_q, H_kv, d, dtype == KDA_BF16, most, window, sinks, &need)))
-        return rc;
+    const int64_t groups =
+        kda::paged_decode_groups(N, H_q, H_kv, d, dtype == KDA_BF16, most, window, sinks, &need);
+    if (int rc = check_groups(name, groups)) return rc;
     if (N > 0 && (!q || !lengths || !out)) return fail(KDA_ERR_INVALID_ARG, "%s: q, lengths and out are required", name);
     if (N > 1 && q_stride * es < row) return fail(KDA_ERR_INVALID_ARG, "%s: queries overlap (stride below H_q * d)", name);
     if (!aligned16(q) || (N > 1 && q_stride * es % 16))
@@ -362,6 +363,7 @@ int kda_cache_reserve(int32_t* page_table, int64_t table_stride, int32_t* length
     if (int rc = check_table(name, page_table, table_stride, N, table_pages, n_pages)) return rc;
     if (!sane_stride(table_stride)) return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
     if (page_size < 1) return fail(KDA_ERR_INVALID_ARG, "%s: page_size must be positive", name);
+    if (int rc = check_groups(name, kda::cache_reserve_groups(N, n_pages))) return rc;
     if (!refcount || (N > 0 && (!lengths || !new_tokens || !copies || !granted)))
         return fail(KDA_ERR_INVALID_ARG, "%s: refcount, lengths, new_tokens, copies and granted are required", name);
     const void* words[] = {lengths, refcount, new_tokens, copies, granted};

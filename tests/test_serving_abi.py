@@ -141,6 +141,8 @@ FAR = [1 << 45, 1 << 46, 1 << 47]  # fake buffers far enough apart for the large
     ("kda_cache_fork", dict(FORK, width=1 << 26, stride=1 << 26, out_stride=1 << 26, N=0, table=None, out=FAR[0]),
      dict(N_out=63), dict(N_out=64)),
     ("kda_cache_free", FREE, dict(n_rows=(1 << 24) - 1), dict(n_rows=1 << 24)),
+    ("kda_cache_reserve", dict(RESERVE, ws_bytes=1 << 33, table=FAR[0]), dict(N=4 * ((1 << 24) - 2)),
+     dict(N=4 * ((1 << 24) - 2) + 1)),  # one workgroup for the ten pages, one for every four sequences
     ("kda_cache_compact", dict(COMPACT, ws_bytes=1 << 30), dict(N=(1 << 24) - 2), dict(N=(1 << 24) - 1)),
     ("kda_beam_select", dict(SELECT, K=1, V=4, row=4, n_out=1), dict(B=(1 << 24) - 1), dict(B=1 << 24)),
 ])
