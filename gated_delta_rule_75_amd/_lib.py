@@ -18,6 +18,7 @@ KDA_ERR_ALIAS, KDA_ERR_WORKSPACE, KDA_ERR_HIP = -4, -5, -6
 KDA_F32, KDA_BF16 = 0, 1
 KDA_OP_PREFILL, KDA_OP_APPEND, KDA_OP_DECODE, KDA_OP_BACKWARD = 0, 1, 2, 3
 KDA_GATE_CHANNEL, KDA_GATE_HEAD = 0, 1
+KDA_ROTARY_HALVES, KDA_ROTARY_INTERLEAVED = 0, 1
 KDA_NOALLOC_SCRATCH_BYTES = 128 << 20  # the fixed device scratch of kda_append_prefill_noalloc
 
 # every symbol include/kda.h declares
@@ -27,13 +28,14 @@ EXPORTS = ("kda_prefill_chunked", "kda_append_prefill", "kda_decode_step", "kda_
            "kda_status_string", "kda_last_error", "kda_version", "kda_timing_begin", "kda_timing_end",
            "kda_cache_append", "kda_paged_decode", "kda_paged_decode_workspace", "kda_cache_fork", "kda_cache_free",
            "kda_cache_reserve", "kda_cache_compact", "kda_cache_workspace_size", "kda_pages_copy", "kda_beam_select",
-           "kda_beam_select_workspace", "kda_beam_reorder", "kda_validate_page_table")
+           "kda_beam_select_workspace", "kda_beam_reorder", "kda_validate_page_table",
+           "kda_rotary", "kda_rotary_append")
 KERNEL_NAMES = {1: "kda_prep", 2: "kda_state", 3: "kda_chunk_f32", 4: "kda_decode", 5: "kda_bwd_factors",
                 6: "kda_bwd_fwd_chain", 7: "kda_bwd_rev_chain", 8: "kda_bwd_grad_state", 9: "kda_bwd_grad_chunk",
                 10: "kda_cache_append", 11: "kda_paged_decode", 12: "kda_paged_join", 13: "kda_cache_fork",
                 14: "kda_cache_free", 15: "kda_cache_scan", 16: "kda_cache_reserve", 17: "kda_cache_plan",
                 18: "kda_cache_remap", 19: "kda_pages_copy", 20: "kda_beam_scan", 21: "kda_beam_join",
-                22: "kda_beam_reorder"}
+                22: "kda_beam_reorder", 23: "kda_rotary"}
 
 _LIB = None
 
@@ -111,6 +113,9 @@ def load():
         "kda_beam_select": [vp, i64, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp],
         "kda_beam_reorder": [vp, vp, i32, vp, i32, i32, vp],
         "kda_validate_page_table": [vp, i64, vp, i32, i32, i32, i32, i64],
+        "kda_rotary": [vp, i64, vp, i64, vp, vp, i64, i32, i32, i32, i32, i32, f32, i32, i32, vp, i64, vp, i64, vp],
+        "kda_rotary_append": [vp, i64, vp, i64, vp, i64, vp, vp, i32, i64, vp, i32, i32, f32, vp, i64, vp, vp, i64, i64,
+                              i32, i32, vp, i64, i32, i32, i32, i32, i32, vp],
     }.items():
         getattr(L, name).restype = ctypes.c_int
         getattr(L, name).argtypes = args

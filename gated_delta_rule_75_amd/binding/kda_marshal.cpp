@@ -1,9 +1,9 @@
-// Marshalling of the serving calls (serving.py) for the usual case, in C: every tensor a plain,
+// Marshalling of the serving calls (serving.py, prompt.py) for the usual case, in C: every tensor a plain,
 // contiguous one of the expected type and shape on the current device.  A small call is bound by the
 // host, and Python's checks and ctypes' argument conversion are most of its 7 to 14 us.
 //
 // Each function takes the Python call's arguments in order and returns its result, or False where
-// anything is not as usual; serving.py then goes its own way, which handles strides and other devices
+// anything is not as usual; the Python call then goes its own way, which handles strides and other devices
 // and raises what is to be raised.  The library's functions are given by address, so this module links
 // only torch and nothing of it computes.
 #include <Python.h>
@@ -35,6 +35,8 @@ decltype(&kda_pages_copy) f_copy;
 decltype(&kda_beam_select) f_select;
 decltype(&kda_beam_select_workspace) f_select_ws;
 decltype(&kda_beam_reorder) f_reorder;
+decltype(&kda_rotary) f_rotary;
+decltype(&kda_rotary_append) f_place;
 
 using at::Tensor;
 constexpr auto kI32 = at::kInt;
@@ -442,6 +444,92 @@ PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
+// "half" or "interleaved"
+bool layout_of(PyObject* o, int32_t& x) {
+    if (!PyUnicode_CheckExact(o)) return false;
+    if (PyUnicode_CompareWithASCIIString(o, "half") == 0) x = KDA_ROTARY_HALVES;
+    else if (PyUnicode_CompareWithASCIIString(o, "interleaved") == 0) x = KDA_ROTARY_INTERLEAVED;
+    else return false;
+    return true;
+}
+
+// q, k, positions, freqs, layout, amplitude, inverse, q_out, k_out
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    KDA_USUAL(n_args == 9);
+    const int dev = device_of(a[0]);
+    KDA_USUAL(dev >= 0);
+    const int code = code_of(a[0]);
+    KDA_USUAL(code >= 0);
+    const auto type = THPVariable_Unpack(a[0]).scalar_type();
+    const Tensor *q = plain(a[0], type, 3, dev), *positions = plain(a[2], kI32, 1, dev),
+                 *freqs = plain(a[3], at::kDouble, 1, dev);
+    int32_t layout;
+    KDA_USUAL(q && positions && freqs && layout_of(a[4], layout) && PyFloat_CheckExact(a[5]) && PyBool_Check(a[6]));
+    const int64_t T = q->size(0), d = q->size(2);
+    KDA_USUAL(positions->size(0) == T && freqs->size(0) > 0 && 2 * freqs->size(0) <= d && small(T) &&
+              small(q->size(1)) && small(d));
+    const Tensor* k = nullptr;
+    if (a[1] != Py_None) {
+        k = plain(a[1], type, 3, dev);
+        KDA_USUAL(k && k->size(0) == T && k->size(2) == d && small(k->size(1)));
+    } else {
+        KDA_USUAL(a[8] == Py_None);
+    }
+    Tensor qo, ko;
+    KDA_USUAL(output_of(a[7], q->sizes(), type, dev, *q, qo) && (!k || output_of(a[8], k->sizes(), type, dev, *k, ko)));
+    KDA_CALL(f_rotary(q->data_ptr(), q->stride(0), k ? k->data_ptr() : nullptr, k ? k->stride(0) : 0,
+                      static_cast<const int32_t*>(positions->data_ptr()), static_cast<const double*>(freqs->data_ptr()),
+                      T, (int32_t)q->size(1), k ? (int32_t)k->size(1) : 0, (int32_t)d, (int32_t)(2 * freqs->size(0)),
+                      layout, (float)PyFloat_AS_DOUBLE(a[5]), a[6] == Py_True, code, qo.data_ptr(), qo.stride(0),
+                      k ? ko.data_ptr() : nullptr, k ? ko.stride(0) : 0, stream));
+    if (k) return pair(std::move(qo), std::move(ko));
+    PyObject* x = THPVariable_Wrap(std::move(qo));
+    PyObject* r = x ? PyTuple_Pack(2, x, Py_None) : nullptr;
+    Py_XDECREF(x);
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, k_pages, v_pages, page_table, start, freqs, cu_seqlens, layout, amplitude, q_out
+PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    KDA_USUAL(n_args == 12);
+    const int dev = device_of(a[0]);
+    KDA_USUAL(dev >= 0);
+    const int code = code_of(a[0]);
+    KDA_USUAL(code >= 0);
+    const auto type = THPVariable_Unpack(a[0]).scalar_type();
+    const Tensor *q = plain(a[0], type, 3, dev), *k = plain(a[1], type, 3, dev), *v = plain(a[2], type, 3, dev),
+                 *kp = plain(a[3], type, 4, dev), *vp = plain(a[4], type, 4, dev), *table = plain(a[5], kI32, 2, dev),
+                 *start = plain(a[6], kI32, 1, dev), *freqs = plain(a[7], at::kDouble, 1, dev);
+    int32_t layout;
+    KDA_USUAL(q && k && v && kp && vp && table && start && freqs && layout_of(a[9], layout) && PyFloat_CheckExact(a[10]));
+    const int64_t T = q->size(0), d = q->size(2), N = table->size(0);
+    KDA_USUAL(k->sizes() == v->sizes() && k->size(0) == T && k->size(2) == d && kp->sizes() == vp->sizes() &&
+              kp->size(1) == k->size(1) && kp->size(3) == d && start->size(0) == N && freqs->size(0) > 0 &&
+              2 * freqs->size(0) <= d);
+    KDA_USUAL(small(T) && small(q->size(1)) && small(k->size(1)) && small(d) && small(kp->size(0)) &&
+              small(kp->size(2)) && small(N) && small(table->size(1)));
+    const Tensor* cu = nullptr;
+    if (a[8] != Py_None) {
+        cu = plain(a[8], kI32, 1, dev);
+        KDA_USUAL(cu && cu->size(0) == N + 1);
+    }
+    Tensor qo;
+    KDA_USUAL(output_of(a[11], q->sizes(), type, dev, *q, qo));
+    KDA_CALL(f_place(q->data_ptr(), q->stride(0), k->data_ptr(), k->stride(0), v->data_ptr(), v->stride(0),
+                     cu ? static_cast<const int32_t*>(cu->data_ptr()) : nullptr,
+                     static_cast<const int32_t*>(start->data_ptr()), (int32_t)N, T,
+                     static_cast<const double*>(freqs->data_ptr()), (int32_t)(2 * freqs->size(0)), layout,
+                     (float)PyFloat_AS_DOUBLE(a[10]), qo.data_ptr(), qo.stride(0), kp->data_ptr(), vp->data_ptr(),
+                     kp->stride(0), vp->stride(0), (int32_t)kp->size(0), (int32_t)kp->size(2),
+                     static_cast<const int32_t*>(table->data_ptr()), table->stride(0), (int32_t)table->size(1),
+                     (int32_t)q->size(1), (int32_t)k->size(1), (int32_t)d, code, stream));
+    return THPVariable_Wrap(std::move(qo));
+    END_HANDLE_TH_ERRORS
+}
+
 // setup(raw_stream, check, {name: address})
 template <typename F>
 bool address(PyObject* d, const char* name, F& f) {
@@ -463,7 +551,8 @@ PyObject* setup(PyObject*, PyObject* args) {
         !address(d, "kda_cache_free", f_free) || !address(d, "kda_cache_reserve", f_reserve) ||
         !address(d, "kda_cache_compact", f_compact) || !address(d, "kda_cache_workspace_size", f_cache_ws) ||
         !address(d, "kda_pages_copy", f_copy) || !address(d, "kda_beam_select", f_select) ||
-        !address(d, "kda_beam_select_workspace", f_select_ws) || !address(d, "kda_beam_reorder", f_reorder))
+        !address(d, "kda_beam_select_workspace", f_select_ws) || !address(d, "kda_beam_reorder", f_reorder) ||
+        !address(d, "kda_rotary", f_rotary) || !address(d, "kda_rotary_append", f_place))
         return nullptr;
     Py_INCREF(raw);
     Py_INCREF(check);
@@ -475,7 +564,8 @@ PyObject* setup(PyObject*, PyObject* args) {
 #define KDA_FN(name) {#name, (PyCFunction)(void*)name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {KDA_FN(cache_append),  KDA_FN(paged_decode),  KDA_FN(cache_fork), KDA_FN(cache_free),
                          KDA_FN(cache_reserve), KDA_FN(cache_compact), KDA_FN(pages_copy), KDA_FN(beam_select),
-                         KDA_FN(beam_reorder),  {"setup", setup, METH_VARARGS, nullptr},  {nullptr, nullptr, 0, nullptr}};
+                         KDA_FN(beam_reorder),  KDA_FN(rotary),        KDA_FN(rotary_append),
+                         {"setup", setup, METH_VARARGS, nullptr},      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -483,7 +573,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_marshal", nullptr, -1, method
 #define KDA_TEXT_(x) #x
 #define KDA_TEXT(x) KDA_TEXT_(x)
 
-// The versions that the module was built for: serving.py uses it with these only.
+// The versions that the module was built for: it is used with these only.
 PyMODINIT_FUNC PyInit__kda_marshal(void) {
     PyObject* m = PyModule_Create(&module);
     if (m && (PyModule_AddStringConstant(m, "torch_version", KDA_TORCH_VERSION) < 0 ||

@@ -65,4 +65,20 @@ __device__ __forceinline__ float gate_from_raw(float a, float scale) {
     return -scale * (fmaxf(a, 0.f) + __builtin_amdgcn_logf(t) * 0.6931471805599453f);
 }
 
+// The segment that holds packed token t: the last n of 0 .. N-1 with cu[n] <= t, 0 if there is none (N >= 1;
+// cu non-decreasing).  A wave probes 64 ends at a time, so two loads in a chain serve 4096 segments.  t and the
+// result are wave-uniform; whatever cu holds, no other element than cu[1] .. cu[N - 1] is read.
+__device__ __forceinline__ int64_t segment_of(const int32_t* cu, int64_t N, int64_t t) {
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, left = N - 1;
+    while (left > 0) {
+        const int64_t step = (left + 63) / 64, at = (lane + 1) * step;
+        const int hits = __popcll(__ballot(at <= left && cu[lo + (at <= left ? at : left)] <= t));
+        lo += hits * step;
+        left -= hits * step;
+        left = left < step - 1 ? left : step - 1;
+    }
+    return lo;
+}
+
 }  // namespace kda

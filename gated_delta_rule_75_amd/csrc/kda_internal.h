@@ -31,7 +31,8 @@ enum KernelId {
     kKernelPagesCopy = 19,
     kKernelBeamScan = 20,
     kKernelBeamJoin = 21,
-    kKernelBeamReorder = 22
+    kKernelBeamReorder = 22,
+    kKernelRotary = 23
 };
 bool timing_on();
 void timed_begin(int kernel_id, hipStream_t s);
@@ -264,5 +265,34 @@ struct BeamSelectArgs {
 int64_t beam_select_groups(int64_t B, int K, int V);
 size_t beam_select_workspace(int64_t B, int K, int V, int n_out);
 hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------------------
+// prompt chunks
+// ---------------------------------------------------------------------------------------
+// Rotation of queries and keys.  With kp the keys and the values go into pages (kda_rotary_append), and the
+// positions are start[n] + i; otherwise both go to tensors and positions has one for each token.
+struct RotaryArgs {
+    const void* q;
+    const void* k;  // or nullptr (H_k = 0)
+    const void* v;  // pages only
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    void* q_out;
+    void* k_out;
+    int64_t q_out_stride, k_out_stride;
+    const int32_t* positions;
+    const int32_t* cu;     // [N + 1] or nullptr (one token per sequence)
+    const int32_t* start;  // [N]
+    int64_t N, T;
+    const double* freqs;   // [r / 2]
+    int Hq, Hk, d, r, interleaved, inverse, bf16;
+    float amplitude;
+    void* kp;
+    void* vp;
+    int64_t kp_stride, vp_stride;
+    PageTable pt;
+    int page_size;
+};
+int64_t rotary_groups(const RotaryArgs& a);
+hipError_t launch_rotary(const RotaryArgs& a, hipStream_t s);
 
 }  // namespace kda

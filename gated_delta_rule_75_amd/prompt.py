@@ -1,0 +1,161 @@
+"""Prompt chunks through the attention layers of a hybrid stack: rotary positions.
+
+New tokens are packed ``[T, H, d]`` with ``cu_seqlens`` int32 ``[N + 1]``; pages and tables are those of
+``serving.py``.  Contracts: ``include/kda.h``.
+
+As in the package's other calls, this module checks and marshals torch tensors; the work is done by
+the library's HIP kernels on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import _lib, serving
+from .serving import _EMPTY, _I32, _lead, _lib_, _row, _run, _vector
+
+_F64 = torch.float64
+_LAYOUTS = {"half": _lib.KDA_ROTARY_HALVES, "interleaved": _lib.KDA_ROTARY_INTERLEAVED}
+
+
+def rotary_frequencies(rotary_dim, *, base=10000.0, scaling=None, factor=1.0, original_length=None, slow=1.0,
+                       fast=32.0, device="cuda"):
+    """Frequencies (radians per token) of rotary positions, float64 [rotary_dim / 2]: base^(-2 i / rotary_dim).
+
+    scaling for contexts `factor` times longer than `original_length`, with t_i the turns of pair i over
+    original_length tokens:
+      "linear"  f / factor
+      "ntk"     base * factor^(rotary_dim / (rotary_dim - 2)): the slowest pair turns 1 / factor as fast
+      "smooth"  f / factor where t <= slow, f where t >= fast, linear in t between
+      "ramp"    the same ends, linear in i between the pairs that make `fast` and `slow` turns (these rounded
+                down and up)
+    Any other frequencies may be used as well.  The factor of the rotated channels that such scalings come with
+    is the calls' `amplitude`, for instance 0.1 log(factor) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and positive, got {rotary_dim}")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    if scaling == "ntk":
+        if rotary_dim < 4:
+            raise ValueError("scaling 'ntk' needs a rotary_dim of 4 or more")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    i = torch.arange(rotary_dim // 2, dtype=_F64)
+    f = base ** (-2.0 * i / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("smooth", "ramp"):
+        if original_length is None or not original_length > 0 or not fast > slow > 0:
+            raise ValueError(f"scaling {scaling!r} needs original_length > 0 and fast > slow > 0")
+        if scaling == "smooth":
+            keep = (original_length * f / (2 * math.pi) - slow) / (fast - slow)
+        else:
+            if not base > 1:
+                raise ValueError("scaling 'ramp' needs a base above 1")
+            # the (fractional) pair that makes `turns` turns
+            lo, hi = (rotary_dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+                      for turns in (fast, slow))
+            lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rotary_dim - 1)
+            keep = 1.0 - (i - lo) / max(hi - lo, 1e-3)
+        keep = keep.clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device)
+
+
+def _turn(freqs, layout, di, d):
+    """Layout code and rotary_dim."""
+    code = _LAYOUTS.get(layout)
+    if code is None:
+        raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+    _vector(freqs, "freqs", _F64, None, di)
+    if freqs.shape[0] < 1 or 2 * freqs.shape[0] > d:
+        raise ValueError(f"freqs must have 1 .. {d // 2} values, got {freqs.shape[0]}")
+    return code, 2 * freqs.shape[0]
+
+
+def _turned(out, name, x, di):
+    """The given output for x, or a new contiguous one, and its row stride."""
+    if out is None:
+        out = _EMPTY(x.shape, dtype=x.dtype, device=x.device)
+        return out, out.stride(0)
+    stride = _row(out, name, x.dtype, 3, di)
+    if out.shape != x.shape:
+        raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    return out, stride
+
+
+def rotary(q, k, positions, freqs, *, layout="half", amplitude=1.0, inverse=False, q_out=None, k_out=None):
+    """Rotary positions of queries and keys.
+
+    q [T,H_q,d], k [T,H_k,d] or None (float32 or bfloat16; rows of any stride), positions int32 [T], freqs
+    float64 [rotary_dim / 2] (``rotary_frequencies``); channels from rotary_dim on are copied.  layout "half":
+    pairs (i, i + rotary_dim / 2); "interleaved": pairs (2 i, 2 i + 1).  The rotated channels are multiplied by
+    amplitude.  inverse=True rotates back by the same angles: given the gradients of the outputs, the call
+    returns those of q and k.  q_out, k_out: outputs, which may be q and k themselves.
+
+    Returns (q_out, k_out), k_out None without k."""
+    if serving._M is not None:
+        done = serving._M.rotary(q, k, positions, freqs, layout, amplitude, inverse, q_out, k_out)
+        if done is not False:
+            return done
+    code, di = _lead(q, "q")
+    qs = _row(q, "q", q.dtype, 3, di)
+    T, Hq, d = q.shape
+    Hk = ks = kos = 0
+    pk = pko = None
+    if k is not None:
+        ks = _row(k, "k", q.dtype, 3, di)
+        if k.shape[0] != T or k.shape[2] != d:
+            raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not go together")
+        Hk = k.shape[1]
+    elif k_out is not None:
+        raise ValueError("k_out given without k")
+    _vector(positions, "positions", _I32, (T,), di)
+    lay, r = _turn(freqs, layout, di, d)
+    q_out, qos = _turned(q_out, "q_out", q, di)
+    if k is not None:
+        k_out, kos = _turned(k_out, "k_out", k, di)
+        pk, pko = k.data_ptr(), k_out.data_ptr()
+    _run(_lib_().kda_rotary, di, q.data_ptr(), qs, pk, ks, positions.data_ptr(), freqs.data_ptr(), T, Hq, Hk, d, r, lay,
+         amplitude, int(bool(inverse)), code, q_out.data_ptr(), qos, pko, kos)
+    return q_out, k_out
+
+
+def rotary_append(q, k, v, k_pages, v_pages, page_table, start, freqs, *, cu_seqlens=None, layout="half",
+                  amplitude=1.0, q_out=None):
+    """``rotary`` and ``cache_append`` in one launch: the rotated keys and the values go into their pages.
+
+    q [T,H_q,d], k, v [T,H_kv,d]; k_pages, v_pages, page_table, start and cu_seqlens as in cache_append: token i
+    of sequence n is at position start[n] + i.  freqs, layout, amplitude as in rotary.
+    Returns q_out [T,H_q,d] (which may be given as q itself).  Rows of q_out that belong to no sequence are not
+    written."""
+    if serving._M is not None:
+        done = serving._M.rotary_append(q, k, v, k_pages, v_pages, page_table, start, freqs, cu_seqlens, layout,
+                                        amplitude, q_out)
+        if done is not False:
+            return done
+    code, di = _lead(q, "q")
+    dt = q.dtype
+    qs, ks, vs = _row(q, "q", dt, 3, di), _row(k, "k", dt, 3, di), _row(v, "v", dt, 3, di)
+    kps, vps = _row(k_pages, "k_pages", dt, 4, di), _row(v_pages, "v_pages", dt, 4, di)
+    T, Hq, d = q.shape
+    pages = k_pages.shape
+    n_pages, H, page_size, dp = pages
+    if k.shape != v.shape or k.shape != (T, H, d) or v_pages.shape != pages or dp != d:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, k_pages {tuple(pages)} and "
+                         f"v_pages {tuple(v_pages.shape)} do not go together")
+    ts = _row(page_table, "page_table", _I32, 2, di)
+    N, P = page_table.shape
+    _vector(start, "start", _I32, (N,), di)
+    cu = None
+    if cu_seqlens is not None:
+        _vector(cu_seqlens, "cu_seqlens", _I32, (N + 1,), di)
+        cu = cu_seqlens.data_ptr()
+    lay, r = _turn(freqs, layout, di, d)
+    q_out, qos = _turned(q_out, "q_out", q, di)
+    _run(_lib_().kda_rotary_append, di, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu, start.data_ptr(), N,
+         T, freqs.data_ptr(), r, lay, amplitude, q_out.data_ptr(), qos, k_pages.data_ptr(), v_pages.data_ptr(), kps,
+         vps, n_pages, page_size, page_table.data_ptr(), ts, P, Hq, H, d, code)
+    return q_out

@@ -535,6 +535,62 @@ size_t kda_beam_select_workspace(int32_t B, int32_t K, int32_t V, int32_t n_out)
 int kda_beam_reorder(void* const* states, const int64_t* row_bytes, int32_t n_states, const int32_t* parents,
                      int32_t B, int32_t K, void* hip_stream);
 
+/*
+ * Prompt chunks: rotary positions
+ * ==========================================================================
+ *
+ * A chunk of new tokens (a prompt's segment, a chat turn, drafted tokens) goes
+ * through an attention layer as rotated queries and keys.  Pair i < rotary_dim / 2
+ * of a token at position p is turned by the angle a = p * freqs[i]:
+ *     (x, y) -> amplitude * (x cos a - y sin a, x sin a + y cos a)
+ *   layout KDA_ROTARY_HALVES       x, y are channels i and i + rotary_dim / 2
+ *          KDA_ROTARY_INTERLEAVED  x, y are channels 2 i and 2 i + 1
+ * Channels from rotary_dim on are copied as they are.
+ *   freqs      DEVICE double [rotary_dim / 2], radians per token, 8-byte aligned: any
+ *              base and any scaling for long contexts is a choice of them (and of
+ *              amplitude)
+ * The angle is an fp64 product reduced by multiples of 2 pi in fp64, its cosine and
+ * sine and the rotation are fp32, and the result is rounded once to dtype.
+ */
+typedef enum { KDA_ROTARY_HALVES = 0, KDA_ROTARY_INTERLEAVED = 1 } kda_rotary_layout;
+
+/*
+ * kda_rotary — rotates queries and keys.
+ *   q, k        token t at t * q_stride (k_stride) elements: [H_q, d], [H_k, d]
+ *               dtype, contiguous; 16-byte aligned, strides too.  k and k_out are
+ *               NULL with H_k = 0.
+ *   positions   int32 [T], any value
+ *   inverse     1: turn by -a, which (amplitude included) is the transpose of the
+ *               rotation: applied to the gradients of q_out and k_out it gives those
+ *               of q and k
+ *   q_out, k_out  laid out as q and k; each is its input itself (same address and
+ *               stride, in place) or does not overlap it.  No other overlap.
+ * d: a multiple of 8 up to 512; rotary_dim even, 2 .. d; H_q <= 16384, H_k <= 1024.
+ */
+int kda_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const int32_t* positions,
+               const double* freqs, int64_t T, int32_t H_q, int32_t H_k, int32_t d, int32_t rotary_dim,
+               int32_t layout, float amplitude, int32_t inverse, int32_t dtype, void* q_out, int64_t q_out_stride,
+               void* k_out, int64_t k_out_stride, void* hip_stream);
+
+/*
+ * kda_rotary_append — kda_rotary and kda_cache_append in one launch, with the same
+ * results: token i of sequence n is at position start[n] + i; its rotated queries go
+ * to q_out, its rotated keys and its values into the pages.
+ *   q, k, v     token t at t * stride elements: [H_q, d], [H_kv, d], [H_kv, d]
+ *   cu_seqlens, start, pages, table: as in kda_cache_append.  A position without a
+ *               page is dropped (q_out is written); rows of q_out that belong to no
+ *               sequence are left as they were.
+ *   q_out       as in kda_rotary (may be q itself); overlaps neither pages nor k, v
+ * d in {64, 128, 256}; the rest as in kda_rotary.
+ */
+int kda_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, const int32_t* cu_seqlens, const int32_t* start, int32_t N, int64_t T_total,
+                      const double* freqs, int32_t rotary_dim, int32_t layout, float amplitude, void* q_out,
+                      int64_t q_out_stride, void* k_pages, void* v_pages, int64_t k_page_stride,
+                      int64_t v_page_stride, int32_t n_pages, int32_t page_size, const int32_t* page_table,
+                      int64_t table_stride, int32_t table_pages, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype,
+                      void* hip_stream);
+
 /* Host-side validator (as those above) of a page table and lengths, HOST arrays:
  * 0 <= lengths[n] <= min(max_length, table_pages * page_size) and entries that
  * are -1 or in [0, n_pages). */
@@ -593,7 +649,8 @@ typedef enum {
     KDA_KERNEL_PAGES_COPY = 19,    /* pages copied */
     KDA_KERNEL_BEAM_SCAN = 20,     /* beam search: best logits and log-sum of a part of a row */
     KDA_KERNEL_BEAM_JOIN = 21,     /* beam search: choice over the beams */
-    KDA_KERNEL_BEAM_REORDER = 22   /* states reordered */
+    KDA_KERNEL_BEAM_REORDER = 22,  /* states reordered */
+    KDA_KERNEL_ROTARY = 23         /* queries and keys rotated (and put into pages) */
 } kda_kernel;
 
 int kda_timing_begin(void);

@@ -1,0 +1,194 @@
+"""Refusals of the prompt chunks' calls: host-side validation of the C ABI and of the binding, and the
+frequencies of rotary positions (no GPU needed: every call here is refused before anything is launched)."""
+import math
+import os
+
+import pytest
+import torch
+
+BASE = 1 << 40
+P = [BASE + i * (1 << 34) for i in range(20)]  # aligned, non-overlapping fake buffers, never read
+
+
+def _lib():
+    from gated_delta_rule_75_amd import _lib
+
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.skip("HIP library not built")
+    return _lib, _lib.load()
+
+
+def _call(L, name, defaults, **kw):
+    unknown = set(kw) - set(defaults)
+    assert not unknown, unknown
+    args = dict(defaults, **kw)
+    return getattr(L, name)(*args.values())
+
+
+ROTARY = dict(q=P[0], q_stride=1024, k=P[1], k_stride=256, positions=P[2], freqs=P[3], T=100, Hq=8, Hk=2, d=128, r=128,
+              layout=0, amplitude=1.0, inverse=0, dtype=1, q_out=P[4], qo_stride=1024, k_out=P[5], ko_stride=256,
+              stream=None)
+PLACE = dict(q=P[0], q_stride=1024, k=P[1], k_stride=256, v=P[2], v_stride=256, cu=P[3], start=P[4], N=4, T=100,
+             freqs=P[5], r=128, layout=0, amplitude=1.0, q_out=P[6], qo_stride=1024, kp=P[7], vp=P[8], kp_stride=4096,
+             vp_stride=4096, n_pages=10, page=16, table=P[9], stride=8, width=8, Hq=8, Hkv=2, d=128, dtype=1,
+             stream=None)
+
+
+@pytest.mark.parametrize("name,defaults,change,status,says", [
+    ("kda_rotary", ROTARY, dict(dtype=2), -1, b"dtype"),
+    ("kda_rotary", ROTARY, dict(T=-1), -1, b"T must"),
+    ("kda_rotary", ROTARY, dict(T=1 << 31), -1, b"T must"),
+    ("kda_rotary", ROTARY, dict(d=100), -2, b"d=100"),
+    ("kda_rotary", ROTARY, dict(d=520), -2, b"d=520"),
+    ("kda_rotary", ROTARY, dict(d=0), -2, b"d=0"),
+    ("kda_rotary", ROTARY, dict(r=130), -1, b"rotary_dim"),
+    ("kda_rotary", ROTARY, dict(r=63), -1, b"rotary_dim"),
+    ("kda_rotary", ROTARY, dict(r=0), -1, b"rotary_dim"),
+    ("kda_rotary", ROTARY, dict(Hq=0), -1, b"H_q"),
+    ("kda_rotary", ROTARY, dict(Hq=16385), -1, b"H_q"),
+    ("kda_rotary", ROTARY, dict(Hk=1025), -1, b"H_k"),
+    ("kda_rotary", ROTARY, dict(Hk=0), -1, b"go together"),
+    ("kda_rotary", ROTARY, dict(k=None), -1, b"k is required"),
+    ("kda_rotary", ROTARY, dict(k=None, Hk=0), -1, b"go together"),
+    ("kda_rotary", ROTARY, dict(layout=2), -1, b"layout"),
+    ("kda_rotary", ROTARY, dict(amplitude=float("nan")), -1, b"amplitude"),
+    ("kda_rotary", ROTARY, dict(freqs=None), -1, b"freqs"),
+    ("kda_rotary", ROTARY, dict(freqs=P[3] + 4), -3, b"8-byte"),
+    ("kda_rotary", ROTARY, dict(positions=None), -1, b"positions"),
+    ("kda_rotary", ROTARY, dict(positions=P[2] + 2), -3, b"4-byte"),
+    ("kda_rotary", ROTARY, dict(q=None), -1, b"q is required"),
+    ("kda_rotary", ROTARY, dict(q_out=None), -1, b"q_out is required"),
+    ("kda_rotary", ROTARY, dict(q_stride=1016), -1, b"overlap"),
+    ("kda_rotary", ROTARY, dict(q_stride=1 << 40), -1, b"strides"),
+    ("kda_rotary", ROTARY, dict(ko_stride=260), -3, b"k_out"),
+    ("kda_rotary", ROTARY, dict(q=P[0] + 8), -3, b"16-byte"),
+    ("kda_rotary", ROTARY, dict(q_out=P[0] + 2048), -4, b"overlaps"),
+    ("kda_rotary", ROTARY, dict(q_out=P[0], qo_stride=2048), -4, b"overlaps"),
+    ("kda_rotary", ROTARY, dict(q_out=P[1]), -4, b"overlaps"),
+    ("kda_rotary", ROTARY, dict(k_out=P[0]), -4, b"overlaps"),
+    ("kda_rotary", ROTARY, dict(k_out=P[4]), -4, b"overlap"),
+    ("kda_rotary", ROTARY, dict(q_out=P[2] - 1024), -4, b"positions or freqs"),
+    ("kda_rotary", ROTARY, dict(freqs=P[5] + 64), -4, b"positions or freqs"),
+    ("kda_rotary_append", PLACE, dict(d=96), -2, b"d=96"),
+    ("kda_rotary_append", PLACE, dict(page=24), -2, b"page_size=24"),
+    ("kda_rotary_append", PLACE, dict(dtype=7), -1, b"dtype"),
+    ("kda_rotary_append", PLACE, dict(Hkv=0), -1, b"H_kv"),
+    ("kda_rotary_append", PLACE, dict(Hq=0), -1, b"H_q"),
+    ("kda_rotary_append", PLACE, dict(r=129), -1, b"rotary_dim"),
+    ("kda_rotary_append", PLACE, dict(layout=-1), -1, b"layout"),
+    ("kda_rotary_append", PLACE, dict(amplitude=float("inf")), -1, b"amplitude"),
+    ("kda_rotary_append", PLACE, dict(cu=None), -1, b"T_total must be N"),
+    ("kda_rotary_append", PLACE, dict(N=0), -1, b"at least one"),
+    ("kda_rotary_append", PLACE, dict(T=-3), -1, b"T_total"),
+    ("kda_rotary_append", PLACE, dict(start=None), -1, b"start"),
+    ("kda_rotary_append", PLACE, dict(v=None), -1, b"v is required"),
+    ("kda_rotary_append", PLACE, dict(v_stride=252), -1, b"tokens of v overlap"),
+    ("kda_rotary_append", PLACE, dict(kp_stride=4088), -1, b"pages overlap"),
+    ("kda_rotary_append", PLACE, dict(vp=P[7] + 16), -4, b"overlap"),
+    ("kda_rotary_append", PLACE, dict(q=P[7]), -4, b"pages overlap"),
+    ("kda_rotary_append", PLACE, dict(q_out=P[8]), -4, b"pages overlap"),
+    ("kda_rotary_append", PLACE, dict(freqs=P[7] + 64), -4, b"pages overlap"),
+    ("kda_rotary_append", PLACE, dict(q_out=P[1]), -4, b"q_out overlaps"),
+    ("kda_rotary_append", PLACE, dict(q_out=P[0] + 1024), -4, b"q_out overlaps"),
+    ("kda_rotary_append", PLACE, dict(q_out=P[9]), -4, b"q_out overlaps"),
+    ("kda_rotary_append", PLACE, dict(stride=7), -1, b"table rows overlap"),
+    ("kda_rotary_append", PLACE, dict(stride=1 << 40), -1, b"strides"),
+    ("kda_rotary_append", PLACE, dict(n_pages=0), -1, b"n_pages"),
+])
+def test_calls_are_refused_before_any_launch(name, defaults, change, status, says):
+    _l, L = _lib()
+    assert _call(L, name, defaults, **change) == status, L.kda_last_error()
+    assert says in L.kda_last_error(), L.kda_last_error()
+
+
+@pytest.mark.parametrize("name,defaults", [
+    ("kda_rotary", ROTARY), ("kda_rotary", dict(ROTARY, q_out=P[0], k_out=P[1])),
+    ("kda_rotary", dict(ROTARY, k=None, k_out=None, Hk=0)), ("kda_rotary", dict(ROTARY, T=0, q=None, q_out=None)),
+    ("kda_rotary_append", PLACE), ("kda_rotary_append", dict(PLACE, q_out=P[0])),
+    ("kda_rotary_append", dict(PLACE, cu=None, N=100, stride=8))])
+def test_the_unchanged_calls_pass_validation(monkeypatch, name, defaults):
+    """The refusals above are due to their one change: without it only the injected failure is left."""
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    assert _call(L, name, defaults) == _l.KDA_ERR_HIP and b"injected" in L.kda_last_error()
+
+
+def test_queries_and_keys_may_be_slices_of_one_projection(monkeypatch):
+    """Rows of equal stride that lie between one another do not overlap, in place or not."""
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    kw = dict(q=P[0], k=P[0] + 2 * 1024, q_stride=1536, k_stride=1536)
+    assert _call(L, "kda_rotary", ROTARY, **kw) == _l.KDA_ERR_HIP, L.kda_last_error()
+    inside = dict(kw, q_out=P[0], k_out=P[0] + 2 * 1024, qo_stride=1536, ko_stride=1536)
+    assert _call(L, "kda_rotary", ROTARY, **inside) == _l.KDA_ERR_HIP, L.kda_last_error()
+    assert _call(L, "kda_rotary", ROTARY, **dict(inside, k_out=P[0] + 2 * 1024 - 16)) == _l.KDA_ERR_ALIAS
+    kw = dict(kw, v=P[0] + 2 * 1280, v_stride=1536, q_out=P[0], qo_stride=1536)
+    assert _call(L, "kda_rotary_append", PLACE, **kw) == _l.KDA_ERR_HIP, L.kda_last_error()
+
+
+@pytest.mark.parametrize("name,defaults,at_most,one_more", [
+    ("kda_rotary", dict(ROTARY, k=None, k_out=None, Hk=0, Hq=1, d=512, r=512, q_stride=512, qo_stride=512, q=1 << 45,
+                        q_out=1 << 46), dict(T=8 * ((1 << 24) - 1)), dict(T=8 * ((1 << 24) - 1) + 1)),
+    ("kda_rotary_append", dict(PLACE, Hq=16384, q_stride=16384 * 64, qo_stride=16384 * 64, d=64, r=64, q=1 << 50,
+                               q_out=1 << 52, k=1 << 53, v=1 << 54), dict(T=8 * ((1 << 24) - 1)), dict(T=8 * ((1 << 24) - 1) + 1)),
+])
+def test_calls_whose_launch_has_2_to_32_threads_are_refused(monkeypatch, name, defaults, at_most, one_more):
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    assert _call(L, name, defaults, **at_most) == _l.KDA_ERR_HIP and b"injected" in L.kda_last_error()
+    assert _call(L, name, defaults, **one_more) == _l.KDA_ERR_INVALID_ARG and b"2^32" in L.kda_last_error()
+
+
+def test_binding_refuses_host_and_misshapen_tensors():
+    import gated_delta_rule_75_amd as kda
+
+    x, t = torch.zeros(2, 4, 64), torch.zeros(2, dtype=torch.int32)
+    f = torch.zeros(32, dtype=torch.float64)
+    pages = torch.zeros(3, 4, 16, 64)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        kda.rotary(x, x, t, f)
+    with pytest.raises(ValueError, match="unsupported dtype"):
+        kda.rotary(x.half(), None, t, f)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        kda.rotary([1], None, t, f)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        kda.rotary_append(x, x, x, pages, pages, t[:, None], t, f)
+
+
+# ------------------------------------------------------------------------------------------------
+# frequencies
+# ------------------------------------------------------------------------------------------------
+def test_rotary_frequencies():
+    from gated_delta_rule_75_amd import rotary_frequencies as freq
+
+    f = freq(128, device="cpu")
+    assert f.dtype == torch.float64 and f.shape == (64,)
+    for i in (0, 1, 17, 63):
+        assert abs(float(f[i]) - 10000.0 ** (-2 * i / 128)) <= 1e-15 * float(f[i]) * 8
+    assert torch.equal(freq(128, scaling="linear", factor=4.0, device="cpu"), f / 4.0)
+    ntk = freq(128, scaling="ntk", factor=8.0, device="cpu")
+    assert float(ntk[0]) == 1.0 and abs(float(ntk[63] / f[63]) * 8.0 - 1) <= 1e-12
+    turns = 8192 * f / (2 * math.pi)
+    for kind in ("smooth", "ramp"):
+        g = freq(128, scaling=kind, factor=16.0, original_length=8192, slow=1.0, fast=4.0, device="cpu")
+        ratio = g / f
+        assert bool((ratio[turns > 10] == 1.0).all()) and bool(((ratio[turns < 0.5] * 16 - 1).abs() < 1e-12).all())
+        assert bool((ratio[1:] <= ratio[:-1] + 1e-12).all())
+    smooth = freq(128, scaling="smooth", factor=16.0, original_length=8192, slow=1.0, fast=4.0, device="cpu")
+    mid = ((turns > 1) & (turns < 4)).nonzero().flatten().tolist()
+    assert mid
+    for i in mid:
+        keep = (float(turns[i]) - 1.0) / 3.0
+        assert abs(float(smooth[i] / f[i]) - (keep + (1 - keep) / 16.0)) <= 1e-12
+
+
+@pytest.mark.parametrize("kw", [dict(rotary_dim=7), dict(rotary_dim=0), dict(rotary_dim=8, base=0.0),
+                                dict(rotary_dim=8, scaling="linear", factor=0.0), dict(rotary_dim=8, scaling="x"),
+                                dict(rotary_dim=2, scaling="ntk"), dict(rotary_dim=8, scaling="smooth"),
+                                dict(rotary_dim=8, scaling="ramp", original_length=100, slow=4.0, fast=4.0),
+                                dict(rotary_dim=8, base=0.5, scaling="ramp", original_length=100)])
+def test_rotary_frequencies_refusals(kw):
+    from gated_delta_rule_75_amd import rotary_frequencies
+
+    with pytest.raises(ValueError):
+        rotary_frequencies(device="cpu", **kw)
