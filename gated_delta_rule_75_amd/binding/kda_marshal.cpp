@@ -37,6 +37,9 @@ decltype(&kda_beam_select_workspace) f_select_ws;
 decltype(&kda_beam_reorder) f_reorder;
 decltype(&kda_rotary) f_rotary;
 decltype(&kda_rotary_append) f_place;
+decltype(&kda_token_logprobs) f_logprobs;
+decltype(&kda_token_logprobs_workspace) f_logprobs_ws;
+decltype(&kda_token_logprobs_grad) f_logprobs_grad;
 
 using at::Tensor;
 constexpr auto kI32 = at::kInt;
@@ -530,6 +533,91 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
+// An optional plain contiguous [rows] argument; false for any other.
+bool optional_of(PyObject* o, at::ScalarType type, int64_t rows, int dev, const void*& p) {
+    p = nullptr;
+    if (o == Py_None) return true;
+    const Tensor* t = plain(o, type, 1, dev);
+    if (!t || t->size(0) != rows) return false;
+    p = t->data_ptr();
+    return true;
+}
+
+// logits, tokens, top, entropy, workspace
+PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    KDA_USUAL(n_args == 5);
+    const int dev = device_of(a[0]);
+    KDA_USUAL(dev >= 0);
+    const int code = code_of(a[0]);
+    KDA_USUAL(code >= 0);
+    const Tensor* x = plain(a[0], THPVariable_Unpack(a[0]).scalar_type(), 2, dev);
+    int32_t top;
+    KDA_USUAL(x && int_of(a[2], top) && top >= 0 && PyBool_Check(a[3]) && small(x->size(1)) && top <= x->size(1));
+    const int64_t R = x->size(0), V = x->size(1);
+    const bool want = a[3] == Py_True;
+    const void* tokens;
+    KDA_USUAL(optional_of(a[1], kI32, R, dev, tokens));
+    Tensor keep;
+    void* ws;
+    size_t ws_bytes;
+    KDA_USUAL(workspace_of(a[4], f_logprobs_ws(R, (int32_t)V, top), dev, *x, keep, ws, ws_bytes));
+    const bool given = a[1] != Py_None;
+    Tensor lp, lse = fresh({R}, at::kFloat, *x), ent, best, which;
+    if (given) lp = fresh({R}, at::kFloat, *x);
+    if (want) ent = fresh({R}, at::kFloat, *x);
+    if (top) {
+        best = fresh({R, top}, at::kFloat, *x);
+        which = fresh({R, top}, kI32, *x);
+    }
+    auto floats = [](Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; };
+    KDA_CALL(f_logprobs(x->data_ptr(), x->stride(0), static_cast<const int32_t*>(tokens), R, (int32_t)V, top, code,
+                        floats(lp), floats(lse), floats(ent), floats(best), top ? ints(which) : nullptr, ws, ws_bytes,
+                        stream));
+    PyObject* r = PyTuple_New(5);
+    if (!r) return nullptr;
+    Tensor* out[5] = {&lp, &lse, &ent, &best, &which};
+    for (int i = 0; i < 5; ++i) {
+        PyObject* o = Py_None;
+        if (out[i]->defined()) o = THPVariable_Wrap(std::move(*out[i]));
+        else Py_INCREF(o);
+        if (!o) {
+            Py_DECREF(r);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(r, i, o);
+    }
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// logits, tokens, lse, d_logprobs, d_lse, entropy, d_entropy, out
+PyObject* token_logprobs_grad(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    KDA_USUAL(n_args == 8);
+    const int dev = device_of(a[0]);
+    KDA_USUAL(dev >= 0);
+    const int code = code_of(a[0]);
+    KDA_USUAL(code >= 0);
+    const auto type = THPVariable_Unpack(a[0]).scalar_type();
+    const Tensor* x = plain(a[0], type, 2, dev);
+    KDA_USUAL(x && small(x->size(1)) && a[2] != Py_None);
+    const int64_t R = x->size(0);
+    KDA_USUAL((a[3] == Py_None || a[1] != Py_None) && (a[6] == Py_None || a[5] != Py_None));
+    const void *tokens, *lse, *d_lp, *d_lse, *ent, *d_ent;
+    KDA_USUAL(optional_of(a[1], kI32, R, dev, tokens) && optional_of(a[2], at::kFloat, R, dev, lse) &&
+              optional_of(a[3], at::kFloat, R, dev, d_lp) && optional_of(a[4], at::kFloat, R, dev, d_lse) &&
+              optional_of(a[5], at::kFloat, R, dev, ent) && optional_of(a[6], at::kFloat, R, dev, d_ent));
+    Tensor out;
+    KDA_USUAL(output_of(a[7], x->sizes(), type, dev, *x, out));
+    auto floats = [](const void* p) { return static_cast<const float*>(p); };
+    KDA_CALL(f_logprobs_grad(x->data_ptr(), x->stride(0), static_cast<const int32_t*>(tokens), floats(lse), floats(ent),
+                             floats(d_lp), floats(d_lse), floats(d_ent), R, (int32_t)x->size(1), code, out.data_ptr(),
+                             out.stride(0), stream));
+    return THPVariable_Wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
 // setup(raw_stream, check, {name: address})
 template <typename F>
 bool address(PyObject* d, const char* name, F& f) {
@@ -552,7 +640,10 @@ PyObject* setup(PyObject*, PyObject* args) {
         !address(d, "kda_cache_compact", f_compact) || !address(d, "kda_cache_workspace_size", f_cache_ws) ||
         !address(d, "kda_pages_copy", f_copy) || !address(d, "kda_beam_select", f_select) ||
         !address(d, "kda_beam_select_workspace", f_select_ws) || !address(d, "kda_beam_reorder", f_reorder) ||
-        !address(d, "kda_rotary", f_rotary) || !address(d, "kda_rotary_append", f_place))
+        !address(d, "kda_rotary", f_rotary) || !address(d, "kda_rotary_append", f_place) ||
+        !address(d, "kda_token_logprobs", f_logprobs) ||
+        !address(d, "kda_token_logprobs_workspace", f_logprobs_ws) ||
+        !address(d, "kda_token_logprobs_grad", f_logprobs_grad))
         return nullptr;
     Py_INCREF(raw);
     Py_INCREF(check);
@@ -565,6 +656,7 @@ PyObject* setup(PyObject*, PyObject* args) {
 PyMethodDef methods[] = {KDA_FN(cache_append),  KDA_FN(paged_decode),  KDA_FN(cache_fork), KDA_FN(cache_free),
                          KDA_FN(cache_reserve), KDA_FN(cache_compact), KDA_FN(pages_copy), KDA_FN(beam_select),
                          KDA_FN(beam_reorder),  KDA_FN(rotary),        KDA_FN(rotary_append),
+                         KDA_FN(token_logprobs), KDA_FN(token_logprobs_grad),
                          {"setup", setup, METH_VARARGS, nullptr},      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -32,7 +32,10 @@ enum KernelId {
     kKernelBeamScan = 20,
     kKernelBeamJoin = 21,
     kKernelBeamReorder = 22,
-    kKernelRotary = 23
+    kKernelRotary = 23,
+    kKernelLogprobScan = 24,
+    kKernelLogprobJoin = 25,
+    kKernelLogprobGrad = 26
 };
 bool timing_on();
 void timed_begin(int kernel_id, hipStream_t s);
@@ -294,5 +297,39 @@ struct RotaryArgs {
 };
 int64_t rotary_groups(const RotaryArgs& a);
 hipError_t launch_rotary(const RotaryArgs& a, hipStream_t s);
+
+struct LogprobArgs {
+    const void* logits;
+    int64_t row_stride;
+    const int32_t* tokens;  // with logprobs
+    int64_t R;
+    int V, top, bf16;
+    float* logprobs;  // or nullptr, like the others
+    float* lse;
+    float* entropy;
+    float* top_logprobs;
+    int32_t* top_tokens;
+    void* ws;
+};
+int64_t logprob_groups(int64_t R, int V);
+size_t logprob_workspace(int64_t R, int V, int top);
+hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s);
+
+struct LogprobGradArgs {
+    const void* logits;
+    int64_t row_stride;
+    const int32_t* tokens;    // with d_logprobs
+    const float* lse;
+    const float* entropy;     // with d_entropy
+    const float* d_logprobs;  // or nullptr, like the others
+    const float* d_lse;
+    const float* d_entropy;
+    int64_t R;
+    int V, bf16;
+    void* d_logits;
+    int64_t out_stride;
+};
+int64_t logprob_grad_groups(int64_t R, int V);
+hipError_t launch_logprob_grad(const LogprobGradArgs& a, hipStream_t s);
 
 }  // namespace kda

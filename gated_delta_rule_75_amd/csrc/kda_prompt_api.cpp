@@ -38,6 +38,22 @@ int check_turn(const char* name, const double* freqs, int32_t H_q, int32_t d, in
     return KDA_OK;
 }
 
+int check_logits(const char* name, const void* x, int64_t stride, int64_t R, int32_t V, int32_t dtype) {
+    if (!valid_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, "%s: dtype must be KDA_F32 or KDA_BF16", name);
+    if (R < 0 || R > kMaxCount) return fail(KDA_ERR_INVALID_ARG, "%s: R must be in [0, 2^31)", name);
+    if (V < 1 || V >= (1 << 24)) return fail(KDA_ERR_INVALID_ARG, "%s: V=%d, expected 1 .. 2^24 - 1", name, V);
+    if (!sane_stride(stride)) return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
+    if (R > 1 && stride < V) return fail(KDA_ERR_INVALID_ARG, "%s: rows overlap (stride below V)", name);
+    if (R > 0 && !x) return fail(KDA_ERR_INVALID_ARG, "%s: logits and d_logits are required", name);
+    if (!aligned_to(x, dtype == KDA_BF16 ? 2 : 4))
+        return fail(KDA_ERR_MISALIGNED, "%s: logits must be aligned to their type", name);
+    return KDA_OK;
+}
+
+Span logit_span(const void* x, int64_t stride, int64_t R, int32_t V, int64_t es) {
+    return Span{x, extent(R, R > 1 ? stride * es : 0, V * es)};
+}
+
 }  // namespace
 
 extern "C" {
@@ -145,6 +161,75 @@ int kda_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_
     }
     if (injected_launch_failure()) return injected(name);
     return check_hip(kda::launch_rotary(a, s), s, name);
+}
+
+size_t kda_token_logprobs_workspace(int64_t R, int32_t V, int32_t top) {
+    if (R < 0 || R > kMaxCount || V < 1 || V >= (1 << 24) || top < 0 || top > 64 || top > V ||
+        kda::logprob_groups(R, V) > kda::max_groups(256))
+        return (size_t)-1;
+    return kda::logprob_workspace(R, V, top);
+}
+
+int kda_token_logprobs(const void* logits, int64_t row_stride, const int32_t* tokens, int64_t R, int32_t V,
+                       int32_t top, int32_t dtype, float* logprobs, float* lse, float* entropy, float* top_logprobs,
+                       int32_t* top_tokens, void* workspace, size_t workspace_bytes, void* hip_stream) {
+    static const char* name = "kda_token_logprobs";
+    if (int rc = check_logits(name, logits, row_stride, R, V, dtype)) return rc;
+    if (top < 0 || top > 64 || top > V) return fail(KDA_ERR_INVALID_ARG, "%s: top=%d, expected 0 .. 64 and at most V", name, top);
+    if (int rc = check_groups(name, kda::logprob_groups(R, V))) return rc;
+    if (R > 0 && (!logprobs != !tokens)) return fail(KDA_ERR_INVALID_ARG, "%s: tokens and logprobs go together", name);
+    if (R > 0 && ((top == 0) != !top_logprobs || (top == 0) != !top_tokens))
+        return fail(KDA_ERR_INVALID_ARG, "%s: top, top_logprobs and top_tokens go together", name);
+    if (!aligned_to(tokens, 4) || !aligned_to(logprobs, 4) || !aligned_to(lse, 4) || !aligned_to(entropy, 4) ||
+        !aligned_to(top_logprobs, 4) || !aligned_to(top_tokens, 4))
+        return fail(KDA_ERR_MISALIGNED, "%s: tokens and outputs must be 4-byte aligned", name);
+    const size_t need = kda::logprob_workspace(R, V, top);
+    if (int rc = check_workspace(name, workspace, workspace_bytes, need)) return rc;
+    const int64_t es = dtype == KDA_BF16 ? 2 : 4;
+    const size_t n = (size_t)R * 4;
+    const Span ins[] = {logit_span(logits, row_stride, R, V, es), {tokens, n}};
+    const Span outs[] = {{logprobs, n}, {lse, n}, {entropy, n}, {top_logprobs, n * top}, {top_tokens, n * top},
+                         {workspace, need}};
+    if (int rc = check_alias(name, outs, ins)) return rc;
+    if (injected_launch_failure()) return injected(name);
+    kda::LogprobArgs a{};
+    a.logits = logits; a.row_stride = row_stride; a.tokens = tokens; a.R = R; a.V = V; a.top = top;
+    a.bf16 = dtype == KDA_BF16;
+    a.logprobs = logprobs; a.lse = lse; a.entropy = entropy; a.top_logprobs = top_logprobs; a.top_tokens = top_tokens;
+    a.ws = workspace;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    return check_hip(kda::launch_logprobs(a, s), s, name);
+}
+
+int kda_token_logprobs_grad(const void* logits, int64_t row_stride, const int32_t* tokens, const float* lse,
+                            const float* entropy, const float* d_logprobs, const float* d_lse, const float* d_entropy,
+                            int64_t R, int32_t V, int32_t dtype, void* d_logits, int64_t out_stride,
+                            void* hip_stream) {
+    static const char* name = "kda_token_logprobs_grad";
+    if (int rc = check_logits(name, logits, row_stride, R, V, dtype)) return rc;
+    if (int rc = check_logits(name, d_logits, out_stride, R, V, dtype)) return rc;
+    if (int rc = check_groups(name, kda::logprob_grad_groups(R, V))) return rc;
+    if (R > 0 && !lse) return fail(KDA_ERR_INVALID_ARG, "%s: lse is required", name);
+    if (R > 0 && d_logprobs && !tokens) return fail(KDA_ERR_INVALID_ARG, "%s: d_logprobs needs tokens", name);
+    if (R > 0 && d_entropy && !entropy) return fail(KDA_ERR_INVALID_ARG, "%s: d_entropy needs entropy", name);
+    if (!aligned_to(tokens, 4) || !aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(d_logprobs, 4) ||
+        !aligned_to(d_lse, 4) || !aligned_to(d_entropy, 4))
+        return fail(KDA_ERR_MISALIGNED, "%s: the rows' values must be 4-byte aligned", name);
+    const int64_t es = dtype == KDA_BF16 ? 2 : 4;
+    const Pool x = rows_of(logits, row_stride * es, V * es, R), y = rows_of(d_logits, out_stride * es, V * es, R);
+    const size_t n = (size_t)R * 4;
+    const Span ins[] = {{tokens, n}, {lse, n}, {entropy, n}, {d_logprobs, n}, {d_lse, n}, {d_entropy, n}};
+    if (!same(x, y) && overlap(x, y))
+        return fail(KDA_ERR_ALIAS, "%s: d_logits overlaps logits and is not the same", name);
+    for (const Span& in : ins)
+        if (overlap(y.span(), in)) return fail(KDA_ERR_ALIAS, "%s: d_logits overlaps an input", name);
+    if (injected_launch_failure()) return injected(name);
+    kda::LogprobGradArgs a{};
+    a.logits = logits; a.row_stride = row_stride; a.tokens = tokens; a.lse = lse; a.entropy = entropy;
+    a.d_logprobs = d_logprobs; a.d_lse = d_lse; a.d_entropy = d_entropy; a.R = R; a.V = V;
+    a.bf16 = dtype == KDA_BF16; a.d_logits = d_logits; a.out_stride = out_stride;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    return check_hip(kda::launch_logprob_grad(a, s), s, name);
 }
 
 }  // extern "C"

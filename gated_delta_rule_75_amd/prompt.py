@@ -1,4 +1,5 @@
-"""Prompt chunks through the attention layers of a hybrid stack: rotary positions.
+"""Prompt chunks through the attention layers of a hybrid stack: rotary positions, and log-probabilities of the
+tokens that follow.
 
 New tokens are packed ``[T, H, d]`` with ``cu_seqlens`` int32 ``[N + 1]``; pages and tables are those of
 ``serving.py``.  Contracts: ``include/kda.h``.
@@ -13,7 +14,7 @@ import math
 import torch
 
 from . import _lib, serving
-from .serving import _EMPTY, _I32, _lead, _lib_, _row, _run, _vector
+from .serving import _EMPTY, _F32, _I32, _int32, _lead, _lib_, _row, _run, _run_scratch, _vector
 
 _F64 = torch.float64
 _LAYOUTS = {"half": _lib.KDA_ROTARY_HALVES, "interleaved": _lib.KDA_ROTARY_INTERLEAVED}
@@ -159,3 +160,75 @@ def rotary_append(q, k, v, k_pages, v_pages, page_table, start, freqs, *, cu_seq
          T, freqs.data_ptr(), r, lay, amplitude, q_out.data_ptr(), qos, k_pages.data_ptr(), v_pages.data_ptr(), kps,
          vps, n_pages, page_size, page_table.data_ptr(), ts, P, Hq, H, d, code)
     return q_out
+
+
+def _optional(t, name, dtype, shape, di):
+    """Address of an optional contiguous tensor."""
+    if t is None:
+        return None
+    _vector(t, name, dtype, shape, di)
+    return t.data_ptr()
+
+
+def token_logprobs(logits, tokens, *, top=0, entropy=False, workspace=None):
+    """Log-probabilities of given tokens, the rows' log-sums, and on request their entropy and best alternatives.
+
+    logits [R,V] (float32 or bfloat16; rows of any stride), tokens int32 [R], or None; a token outside [0, V) is
+    ignored (0).  NaN logits count as -inf.
+    Returns (logprobs [R], lse [R], entropy [R], top_logprobs [R,top], top_tokens int32 [R,top]), float32 but for
+    the last; None for what was not asked for.  The alternatives are in descending order, ties to the lower
+    token; top <= 64."""
+    if serving._M is not None:
+        done = serving._M.token_logprobs(logits, tokens, top, entropy, workspace)
+        if done is not False:
+            return done
+    _int32(top=top)
+    code, di = _lead(logits, "logits")
+    stride = _row(logits, "logits", logits.dtype, 2, di)
+    R, V = logits.shape
+    if top < 0 or top > V:
+        raise ValueError(f"top must be in 0 .. V, got {top}")
+    dev = logits.device
+    pt = _optional(tokens, "tokens", _I32, (R,), di)
+    lp = None if tokens is None else _EMPTY(R, dtype=_F32, device=dev)
+    lse = _EMPTY(R, dtype=_F32, device=dev)
+    ent = _EMPTY(R, dtype=_F32, device=dev) if entropy else None
+    best = _EMPTY((R, top), dtype=_F32, device=dev) if top else None
+    which = _EMPTY((R, top), dtype=_I32, device=dev) if top else None
+    L = _lib_()
+    _run_scratch(L.kda_token_logprobs, di, workspace, (L.kda_token_logprobs_workspace, R, V, top), logits.data_ptr(),
+                 stride, pt, R, V, top, code, *(None if x is None else x.data_ptr() for x in (lp, lse, ent, best, which)))
+    return lp, lse, ent, best, which
+
+
+def token_logprobs_grad(logits, tokens, lse, d_logprobs=None, *, d_lse=None, entropy=None, d_entropy=None, out=None):
+    """Gradient of ``token_logprobs`` with respect to the logits, in their dtype:
+    p (d_lse - d_logprob - d_entropy (log p + entropy)) + d_logprob at the token.
+
+    logits, tokens as given to token_logprobs, lse and entropy float32 [R] as it returned them; d_logprobs, d_lse,
+    d_entropy float32 [R] or None (zero).  out: a tensor [R,V], which may be logits itself."""
+    if serving._M is not None:
+        done = serving._M.token_logprobs_grad(logits, tokens, lse, d_logprobs, d_lse, entropy, d_entropy, out)
+        if done is not False:
+            return done
+    code, di = _lead(logits, "logits")
+    stride = _row(logits, "logits", logits.dtype, 2, di)
+    R, V = logits.shape
+    _vector(lse, "lse", _F32, (R,), di)
+    if d_logprobs is not None and tokens is None:
+        raise ValueError("d_logprobs needs tokens")
+    if d_entropy is not None and entropy is None:
+        raise ValueError("d_entropy needs entropy")
+    pt = _optional(tokens, "tokens", _I32, (R,), di)
+    rows = [_optional(t, name, _F32, (R,), di) for t, name in (
+        (entropy, "entropy"), (d_logprobs, "d_logprobs"), (d_lse, "d_lse"), (d_entropy, "d_entropy"))]
+    if out is None:
+        out = _EMPTY((R, V), dtype=logits.dtype, device=logits.device)
+        os = V
+    else:
+        os = _row(out, "out", logits.dtype, 2, di)
+        if out.shape != (R, V):
+            raise ValueError(f"out must have shape {(R, V)}, got {tuple(out.shape)}")
+    _run(_lib_().kda_token_logprobs_grad, di, logits.data_ptr(), stride, pt, lse.data_ptr(), *rows, R, V, code,
+         out.data_ptr(), os)
+    return out

@@ -591,6 +591,47 @@ int kda_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_
                       int64_t table_stride, int32_t table_pages, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype,
                       void* hip_stream);
 
+/*
+ * Prompt chunks: log-probabilities of given tokens
+ * ==========================================================================
+ *
+ * kda_token_logprobs — for every row x of logits (a prompt's tokens, drafted tokens, a training batch):
+ *     lse = log sum_u exp(x_u),   logprob = x_token - lse,
+ *     entropy = -sum_u p_u log p_u with p_u = exp(x_u - lse),
+ *     and the `top` largest x - lse with their tokens, in descending order, ties to the lower token.
+ *   logits     row r at r * row_stride elements: [V] dtype.  NaN counts as -inf.
+ *   tokens     int32 [R], with logprobs (NULL without).  A token outside [0, V) is
+ *              ignored: its logprob is 0.
+ *   logprobs, lse, entropy   float [R], each may be NULL
+ *   top_logprobs, top_tokens float, int32 [R, top]; NULL with top = 0
+ * A row whose log-sum is not finite (all -inf, or a logit of +inf) has entropy 0, and a log-probability that is NaN
+ * there counts as -inf.
+ * V < 2^24, 0 <= top <= 64, top <= V.
+ * workspace: kda_token_logprobs_workspace bytes, 256-byte aligned, overlapping no argument; needs no
+ * initialisation.
+ */
+int kda_token_logprobs(const void* logits, int64_t row_stride, const int32_t* tokens, int64_t R, int32_t V,
+                       int32_t top, int32_t dtype, float* logprobs, float* lse, float* entropy, float* top_logprobs,
+                       int32_t* top_tokens, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* Workspace bytes of kda_token_logprobs; (size_t)-1 for an invalid combination. */
+size_t kda_token_logprobs_workspace(int64_t R, int32_t V, int32_t top);
+
+/*
+ * kda_token_logprobs_grad — the gradient of kda_token_logprobs with respect to the logits:
+ *     d_logits_v = p_v (d_lse - d_logprob - d_entropy (log p_v + entropy)) + d_logprob [v = token]
+ *   logits, tokens   as given to kda_token_logprobs; lse, entropy float [R]: its results
+ *   d_logprobs (with tokens), d_lse, d_entropy (with entropy)   float [R], each may be NULL (zero)
+ *   d_logits   row r at r * out_stride elements: [V] dtype; may be logits itself (same address and stride),
+ *              no other overlap
+ * An ignored token's d_logprob counts as 0.  Where p_v is 0 (logits of -inf or NaN) it contributes nothing; rows whose
+ * lse is not finite have gradient 0.  Computed in fp32, rounded once to dtype.
+ */
+int kda_token_logprobs_grad(const void* logits, int64_t row_stride, const int32_t* tokens, const float* lse,
+                            const float* entropy, const float* d_logprobs, const float* d_lse, const float* d_entropy,
+                            int64_t R, int32_t V, int32_t dtype, void* d_logits, int64_t out_stride,
+                            void* hip_stream);
+
 /* Host-side validator (as those above) of a page table and lengths, HOST arrays:
  * 0 <= lengths[n] <= min(max_length, table_pages * page_size) and entries that
  * are -1 or in [0, n_pages). */
@@ -650,7 +691,10 @@ typedef enum {
     KDA_KERNEL_BEAM_SCAN = 20,     /* beam search: best logits and log-sum of a part of a row */
     KDA_KERNEL_BEAM_JOIN = 21,     /* beam search: choice over the beams */
     KDA_KERNEL_BEAM_REORDER = 22,  /* states reordered */
-    KDA_KERNEL_ROTARY = 23         /* queries and keys rotated (and put into pages) */
+    KDA_KERNEL_ROTARY = 23,        /* queries and keys rotated (and put into pages) */
+    KDA_KERNEL_LOGPROB_SCAN = 24,  /* token log-probabilities: a row or a part of one */
+    KDA_KERNEL_LOGPROB_JOIN = 25,  /* token log-probabilities: join of the split rows */
+    KDA_KERNEL_LOGPROB_GRAD = 26   /* gradient of token log-probabilities */
 } kda_kernel;
 
 int kda_timing_begin(void);

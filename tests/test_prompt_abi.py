@@ -32,6 +32,10 @@ PLACE = dict(q=P[0], q_stride=1024, k=P[1], k_stride=256, v=P[2], v_stride=256, 
              freqs=P[5], r=128, layout=0, amplitude=1.0, q_out=P[6], qo_stride=1024, kp=P[7], vp=P[8], kp_stride=4096,
              vp_stride=4096, n_pages=10, page=16, table=P[9], stride=8, width=8, Hq=8, Hkv=2, d=128, dtype=1,
              stream=None)
+SCORE = dict(logits=P[0], row=1000, tokens=P[1], R=50, V=1000, top=4, dtype=1, logprobs=P[2], lse=P[3], entropy=P[4],
+             best=P[5], which=P[6], ws=P[7], ws_bytes=1 << 20, stream=None)
+GRAD = dict(logits=P[0], row=1000, tokens=P[1], lse=P[2], entropy=P[3], d_logprobs=P[4], d_lse=P[5], d_entropy=P[6], R=50,
+            V=1000, dtype=1, out=P[7], out_row=1000, stream=None)
 
 
 @pytest.mark.parametrize("name,defaults,change,status,says", [
@@ -94,6 +98,39 @@ PLACE = dict(q=P[0], q_stride=1024, k=P[1], k_stride=256, v=P[2], v_stride=256, 
     ("kda_rotary_append", PLACE, dict(stride=7), -1, b"table rows overlap"),
     ("kda_rotary_append", PLACE, dict(stride=1 << 40), -1, b"strides"),
     ("kda_rotary_append", PLACE, dict(n_pages=0), -1, b"n_pages"),
+    ("kda_token_logprobs", SCORE, dict(dtype=3), -1, b"dtype"),
+    ("kda_token_logprobs", SCORE, dict(R=-1), -1, b"R must"),
+    ("kda_token_logprobs", SCORE, dict(R=1 << 31), -1, b"R must"),
+    ("kda_token_logprobs", SCORE, dict(V=0), -1, b"V=0"),
+    ("kda_token_logprobs", SCORE, dict(V=1 << 24, row=1 << 24), -1, b"V=16777216"),
+    ("kda_token_logprobs", SCORE, dict(row=999), -1, b"rows overlap"),
+    ("kda_token_logprobs", SCORE, dict(row=1 << 40), -1, b"strides"),
+    ("kda_token_logprobs", SCORE, dict(logits=None), -1, b"required"),
+    ("kda_token_logprobs", SCORE, dict(logits=P[0] + 1), -3, b"aligned"),
+    ("kda_token_logprobs", SCORE, dict(top=65), -1, b"top=65"),
+    ("kda_token_logprobs", SCORE, dict(top=-1), -1, b"top=-1"),
+    ("kda_token_logprobs", SCORE, dict(V=3), -1, b"top=4"),
+    ("kda_token_logprobs", SCORE, dict(top=0), -1, b"go together"),
+    ("kda_token_logprobs", SCORE, dict(which=None), -1, b"go together"),
+    ("kda_token_logprobs", SCORE, dict(tokens=None), -1, b"go together"),
+    ("kda_token_logprobs", SCORE, dict(logprobs=None), -1, b"go together"),
+    ("kda_token_logprobs", SCORE, dict(lse=P[3] + 2), -3, b"4-byte"),
+    ("kda_token_logprobs", SCORE, dict(lse=P[2] + 64), -4, b"overlap"),
+    ("kda_token_logprobs", SCORE, dict(entropy=P[0]), -4, b"overlaps an input"),
+    ("kda_token_logprobs", SCORE, dict(R=2, V=100000, row=100000, ws_bytes=8), -5, b"needed"),
+    ("kda_token_logprobs", SCORE, dict(R=2, V=100000, row=100000, ws=None), -5, b"needed"),
+    ("kda_token_logprobs", SCORE, dict(R=2, V=100000, row=100000, ws=P[7] + 8), -3, b"256-byte"),
+    ("kda_token_logprobs_grad", GRAD, dict(dtype=3), -1, b"dtype"),
+    ("kda_token_logprobs_grad", GRAD, dict(V=0), -1, b"V=0"),
+    ("kda_token_logprobs_grad", GRAD, dict(out=None), -1, b"required"),
+    ("kda_token_logprobs_grad", GRAD, dict(out_row=999), -1, b"rows overlap"),
+    ("kda_token_logprobs_grad", GRAD, dict(lse=None), -1, b"lse"),
+    ("kda_token_logprobs_grad", GRAD, dict(tokens=None), -1, b"needs tokens"),
+    ("kda_token_logprobs_grad", GRAD, dict(entropy=None), -1, b"needs entropy"),
+    ("kda_token_logprobs_grad", GRAD, dict(d_lse=P[5] + 1), -3, b"4-byte"),
+    ("kda_token_logprobs_grad", GRAD, dict(out=P[0] + 2000), -4, b"not the same"),
+    ("kda_token_logprobs_grad", GRAD, dict(out=P[0], out_row=1008), -4, b"not the same"),
+    ("kda_token_logprobs_grad", GRAD, dict(out=P[3] - 64), -4, b"overlaps an input"),
 ])
 def test_calls_are_refused_before_any_launch(name, defaults, change, status, says):
     _l, L = _lib()
@@ -105,7 +142,11 @@ def test_calls_are_refused_before_any_launch(name, defaults, change, status, say
     ("kda_rotary", ROTARY), ("kda_rotary", dict(ROTARY, q_out=P[0], k_out=P[1])),
     ("kda_rotary", dict(ROTARY, k=None, k_out=None, Hk=0)), ("kda_rotary", dict(ROTARY, T=0, q=None, q_out=None)),
     ("kda_rotary_append", PLACE), ("kda_rotary_append", dict(PLACE, q_out=P[0])),
-    ("kda_rotary_append", dict(PLACE, cu=None, N=100, stride=8))])
+    ("kda_rotary_append", dict(PLACE, cu=None, N=100, stride=8)),
+    ("kda_token_logprobs", SCORE), ("kda_token_logprobs", dict(SCORE, tokens=None, logprobs=None, entropy=None)),
+    ("kda_token_logprobs", dict(SCORE, top=0, best=None, which=None, lse=None)),
+    ("kda_token_logprobs_grad", GRAD), ("kda_token_logprobs_grad", dict(GRAD, out=P[0])),
+    ("kda_token_logprobs_grad", dict(GRAD, d_lse=None, d_entropy=None, entropy=None))])
 def test_the_unchanged_calls_pass_validation(monkeypatch, name, defaults):
     """The refusals above are due to their one change: without it only the injected failure is left."""
     _l, L = _lib()
@@ -131,6 +172,8 @@ def test_queries_and_keys_may_be_slices_of_one_projection(monkeypatch):
                         q_out=1 << 46), dict(T=8 * ((1 << 24) - 1)), dict(T=8 * ((1 << 24) - 1) + 1)),
     ("kda_rotary_append", dict(PLACE, Hq=16384, q_stride=16384 * 64, qo_stride=16384 * 64, d=64, r=64, q=1 << 50,
                                q_out=1 << 52, k=1 << 53, v=1 << 54), dict(T=8 * ((1 << 24) - 1)), dict(T=8 * ((1 << 24) - 1) + 1)),
+    ("kda_token_logprobs", dict(SCORE, V=4, row=4), dict(R=(1 << 24) - 1), dict(R=1 << 24)),
+    ("kda_token_logprobs_grad", dict(GRAD, V=4, row=4, out_row=4), dict(R=4 * ((1 << 24) - 1)), dict(R=(1 << 26) - 3)),
 ])
 def test_calls_whose_launch_has_2_to_32_threads_are_refused(monkeypatch, name, defaults, at_most, one_more):
     _l, L = _lib()
@@ -153,6 +196,28 @@ def test_binding_refuses_host_and_misshapen_tensors():
         kda.rotary([1], None, t, f)
     with pytest.raises(ValueError, match="GPU tensor"):
         kda.rotary_append(x, x, x, pages, pages, t[:, None], t, f)
+
+
+def test_workspace_of_token_logprobs():
+    _l, L = _lib()
+    bad = 2 ** 64 - 1
+    assert L.kda_token_logprobs_workspace(2, 100000, 5) > 0
+    assert L.kda_token_logprobs_workspace(5000, 100000, 5) == 0 and L.kda_token_logprobs_workspace(0, 100000, 5) == 0
+    for args in ((-1, 10, 1), (5, 0, 0), (5, 1 << 24, 1), (5, 10, 11), (5, 100, 65), (5, 100, -1), (1 << 31, 100, 1)):
+        assert L.kda_token_logprobs_workspace(*args) == bad, args
+
+
+def test_binding_refuses_misplaced_logits():
+    import gated_delta_rule_75_amd as kda
+
+    x, t, f = torch.zeros(2, 40), torch.zeros(2, dtype=torch.int32), torch.zeros(2)
+    for call in (lambda: kda.token_logprobs(x, t), lambda: kda.token_logprobs_grad(x, t, f, f)):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call()
+    with pytest.raises(ValueError, match="unsupported dtype"):
+        kda.token_logprobs(x.half(), t)
+    with pytest.raises(ValueError, match="top"):
+        kda.token_logprobs(x, t, top=2 ** 32)
 
 
 # ------------------------------------------------------------------------------------------------
