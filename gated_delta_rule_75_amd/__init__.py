@@ -22,7 +22,7 @@ from ._lib import KdaError  # noqa: F401
 __all__ = ["prefill_chunked", "append_prefill", "decode_step", "chunked_backward", "workspace_size", "is_supported",
            "version", "KdaError", "kernel_timing", "cache_append", "paged_decode", "cache_fork", "cache_free",
            "cache_reserve", "cache_compact", "pages_copy", "beam_select", "beam_reorder", "rotary", "rotary_append",
-           "rotary_frequencies", "token_logprobs", "token_logprobs_grad"]
+           "rotary_frequencies", "paged_prefill", "token_logprobs", "token_logprobs_grad"]
 
 _DT = {torch.float32: _lib.KDA_F32, torch.bfloat16: _lib.KDA_BF16}
 
@@ -336,5 +336,5 @@ def decode_step(q, k, v, g, beta, state, *, out=None, state_out=None, prologue_g
 
 from .serving import (beam_reorder, beam_select, cache_append, cache_compact, cache_fork, cache_free,  # noqa: E402
                       cache_reserve, paged_decode, pages_copy)
-from .prompt import (rotary, rotary_append, rotary_frequencies, token_logprobs,  # noqa: E402
+from .prompt import (paged_prefill, rotary, rotary_append, rotary_frequencies, token_logprobs,  # noqa: E402
                      token_logprobs_grad)

@@ -29,15 +29,15 @@ EXPORTS = ("kda_prefill_chunked", "kda_append_prefill", "kda_decode_step", "kda_
            "kda_cache_append", "kda_paged_decode", "kda_paged_decode_workspace", "kda_cache_fork", "kda_cache_free",
            "kda_cache_reserve", "kda_cache_compact", "kda_cache_workspace_size", "kda_pages_copy", "kda_beam_select",
            "kda_beam_select_workspace", "kda_beam_reorder", "kda_validate_page_table",
-           "kda_rotary", "kda_rotary_append", "kda_token_logprobs", "kda_token_logprobs_workspace",
-           "kda_token_logprobs_grad")
+           "kda_rotary", "kda_rotary_append", "kda_paged_prefill", "kda_paged_prefill_workspace", "kda_token_logprobs",
+           "kda_token_logprobs_workspace", "kda_token_logprobs_grad")
 KERNEL_NAMES = {1: "kda_prep", 2: "kda_state", 3: "kda_chunk_f32", 4: "kda_decode", 5: "kda_bwd_factors",
                 6: "kda_bwd_fwd_chain", 7: "kda_bwd_rev_chain", 8: "kda_bwd_grad_state", 9: "kda_bwd_grad_chunk",
                 10: "kda_cache_append", 11: "kda_paged_decode", 12: "kda_paged_join", 13: "kda_cache_fork",
                 14: "kda_cache_free", 15: "kda_cache_scan", 16: "kda_cache_reserve", 17: "kda_cache_plan",
                 18: "kda_cache_remap", 19: "kda_pages_copy", 20: "kda_beam_scan", 21: "kda_beam_join",
                 22: "kda_beam_reorder", 23: "kda_rotary", 24: "kda_logprob_scan", 25: "kda_logprob_join",
-                26: "kda_logprob_grad"}
+                26: "kda_logprob_grad", 27: "kda_paged_prefill", 28: "kda_prefill_join"}
 
 _LIB = None
 
@@ -118,6 +118,8 @@ def load():
         "kda_rotary": [vp, i64, vp, i64, vp, vp, i64, i32, i32, i32, i32, i32, f32, i32, i32, vp, i64, vp, i64, vp],
         "kda_rotary_append": [vp, i64, vp, i64, vp, i64, vp, vp, i32, i64, vp, i32, i32, f32, vp, i64, vp, vp, i64, i64,
                               i32, i32, vp, i64, i32, i32, i32, i32, i32, vp],
+        "kda_paged_prefill": [vp, i64, vp, vp, i64, i64, i32, i32, vp, i64, i32, vp, vp, i32, i64, i32, i32, i32, i32, f32,
+                              i32, i32, i64, vp, vp, vp, sz, vp],
         "kda_token_logprobs": [vp, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp],
         "kda_token_logprobs_grad": [vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, i32, vp, i64, vp],
     }.items():
@@ -129,6 +131,8 @@ def load():
     L.kda_cache_workspace_size.argtypes = [i32, i32]
     L.kda_beam_select_workspace.restype = sz
     L.kda_beam_select_workspace.argtypes = [i32, i32, i32, i32]
+    L.kda_paged_prefill_workspace.restype = sz
+    L.kda_paged_prefill_workspace.argtypes = [i32, i64, i32, i32, i32, i32, i64, i32, i32]
     L.kda_token_logprobs_workspace.restype = sz
     L.kda_token_logprobs_workspace.argtypes = [i64, i32, i32]
     _LIB = L

@@ -37,6 +37,8 @@ decltype(&kda_beam_select_workspace) f_select_ws;
 decltype(&kda_beam_reorder) f_reorder;
 decltype(&kda_rotary) f_rotary;
 decltype(&kda_rotary_append) f_place;
+decltype(&kda_paged_prefill) f_prefill;
+decltype(&kda_paged_prefill_workspace) f_prefill_ws;
 decltype(&kda_token_logprobs) f_logprobs;
 decltype(&kda_token_logprobs_workspace) f_logprobs_ws;
 decltype(&kda_token_logprobs_grad) f_logprobs_grad;
@@ -533,6 +535,55 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
+// q, k_pages, v_pages, page_table, lengths, cu_seqlens, scale, window, sinks, max_length, out, lse, workspace
+PyObject* paged_prefill(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    KDA_USUAL(n_args == 13);
+    const int dev = device_of(a[0]);
+    KDA_USUAL(dev >= 0);
+    const int code = code_of(a[0]);
+    KDA_USUAL(code >= 0);
+    const auto type = THPVariable_Unpack(a[0]).scalar_type();
+    const Tensor *q = plain(a[0], type, 3, dev), *kp = plain(a[1], type, 4, dev), *vp = plain(a[2], type, 4, dev),
+                 *table = plain(a[3], kI32, 2, dev), *lengths = plain(a[4], kI32, 1, dev), *cu = plain(a[5], kI32, 1, dev);
+    KDA_USUAL(q && kp && vp && table && lengths && cu);
+    const int64_t T = q->size(0), Hq = q->size(1), d = q->size(2), N = table->size(0), P = table->size(1),
+                  page = kp->size(2);
+    KDA_USUAL(kp->sizes() == vp->sizes() && kp->size(3) == d && lengths->size(0) == N && cu->size(0) == N + 1);
+    KDA_USUAL(small(T) && small(N) && small(Hq) && small(d) && small(P) && small(page) && small(kp->size(0)) &&
+              small(kp->size(1)) && small(P * page));
+    int32_t window, sinks, most = (int32_t)(P * page);
+    KDA_USUAL(int_of(a[7], window) && int_of(a[8], sinks));
+    if (a[9] != Py_None) {
+        int32_t bound;
+        KDA_USUAL(int_of(a[9], bound) && bound > 0);
+        most = bound < most ? bound : most;
+    }
+    double scale = 0.;
+    if (a[6] != Py_None) {
+        KDA_USUAL(PyFloat_CheckExact(a[6]));
+        scale = PyFloat_AS_DOUBLE(a[6]);
+    } else {
+        scale = d > 0 ? std::pow((double)d, -0.5) : 0.;
+    }
+    const size_t need =
+        f_prefill_ws((int32_t)N, T, (int32_t)Hq, (int32_t)kp->size(1), (int32_t)d, code, most, window, sinks);
+    Tensor keep, out, lse;
+    void* ws;
+    size_t ws_bytes;
+    KDA_USUAL(workspace_of(a[12], need, dev, *q, keep, ws, ws_bytes));
+    KDA_USUAL(output_of(a[10], q->sizes(), type, dev, *q, out));
+    const bool want = a[11] != Py_None && a[11] != Py_False;
+    if (want) KDA_USUAL(output_of(a[11] == Py_True ? Py_None : a[11], {T, Hq}, at::kFloat, dev, *q, lse));
+    KDA_CALL(f_prefill(q->data_ptr(), q->stride(0), kp->data_ptr(), vp->data_ptr(), kp->stride(0), vp->stride(0),
+                       (int32_t)kp->size(0), (int32_t)page, ints(*table), table->stride(0), (int32_t)P, ints(*lengths),
+                       ints(*cu), (int32_t)N, T, (int32_t)Hq, (int32_t)kp->size(1), (int32_t)d, code, (float)scale,
+                       window, sinks, most, out.data_ptr(), want ? static_cast<float*>(lse.data_ptr()) : nullptr, ws,
+                       ws_bytes, stream));
+    return want ? pair(std::move(out), std::move(lse)) : THPVariable_Wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
 // An optional plain contiguous [rows] argument; false for any other.
 bool optional_of(PyObject* o, at::ScalarType type, int64_t rows, int dev, const void*& p) {
     p = nullptr;
@@ -641,6 +692,8 @@ PyObject* setup(PyObject*, PyObject* args) {
         !address(d, "kda_pages_copy", f_copy) || !address(d, "kda_beam_select", f_select) ||
         !address(d, "kda_beam_select_workspace", f_select_ws) || !address(d, "kda_beam_reorder", f_reorder) ||
         !address(d, "kda_rotary", f_rotary) || !address(d, "kda_rotary_append", f_place) ||
+        !address(d, "kda_paged_prefill", f_prefill) ||
+        !address(d, "kda_paged_prefill_workspace", f_prefill_ws) ||
         !address(d, "kda_token_logprobs", f_logprobs) ||
         !address(d, "kda_token_logprobs_workspace", f_logprobs_ws) ||
         !address(d, "kda_token_logprobs_grad", f_logprobs_grad))
@@ -656,7 +709,7 @@ PyObject* setup(PyObject*, PyObject* args) {
 PyMethodDef methods[] = {KDA_FN(cache_append),  KDA_FN(paged_decode),  KDA_FN(cache_fork), KDA_FN(cache_free),
                          KDA_FN(cache_reserve), KDA_FN(cache_compact), KDA_FN(pages_copy), KDA_FN(beam_select),
                          KDA_FN(beam_reorder),  KDA_FN(rotary),        KDA_FN(rotary_append),
-                         KDA_FN(token_logprobs), KDA_FN(token_logprobs_grad),
+                         KDA_FN(paged_prefill), KDA_FN(token_logprobs), KDA_FN(token_logprobs_grad),
                          {"setup", setup, METH_VARARGS, nullptr},      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

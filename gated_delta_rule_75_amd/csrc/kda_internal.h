@@ -35,7 +35,9 @@ enum KernelId {
     kKernelRotary = 23,
     kKernelLogprobScan = 24,
     kKernelLogprobJoin = 25,
-    kKernelLogprobGrad = 26
+    kKernelLogprobGrad = 26,
+    kKernelPagedPrefill = 27,
+    kKernelPrefillJoin = 28
 };
 bool timing_on();
 void timed_begin(int kernel_id, hipStream_t s);
@@ -297,6 +299,28 @@ struct RotaryArgs {
 };
 int64_t rotary_groups(const RotaryArgs& a);
 hipError_t launch_rotary(const RotaryArgs& a, hipStream_t s);
+
+struct PagedPrefillArgs {
+    const void* q;
+    int64_t q_stride;
+    const void* kp;
+    const void* vp;
+    int64_t kp_stride, vp_stride;
+    PageTable pt;
+    const int32_t* lengths;
+    const int32_t* cu;  // [N + 1]
+    int64_t N, T;
+    int page_size, Hq, Hkv, d, bf16;
+    float scale;
+    int window, sinks;
+    int64_t max_length;  // at most width * page_size
+    void* o;
+    float* lse;  // or nullptr
+    void* ws;
+};
+// workgroups, and in `workspace` (0 where they do not fit a launch) the bytes of the partial results
+int64_t paged_prefill_groups(const PagedPrefillArgs& a, size_t* workspace);
+hipError_t launch_paged_prefill(const PagedPrefillArgs& a, hipStream_t s);
 
 struct LogprobArgs {
     const void* logits;

@@ -163,6 +163,79 @@ int kda_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_
     return check_hip(kda::launch_rotary(a, s), s, name);
 }
 
+size_t kda_paged_prefill_workspace(int32_t N, int64_t T_total, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype,
+                                   int64_t max_length, int32_t window, int32_t sinks) {
+    if (N < 0 || T_total < 0 || T_total > kMaxCount || H_kv <= 0 || H_kv > 1024 || H_q <= 0 || H_q % H_kv ||
+        H_q > 16384 || !valid_dtype(dtype) || !kda::paged_decode_supported(d) || max_length < 0 ||
+        max_length > kMaxCount - 4096 || window < 0 || sinks < 0)
+        return (size_t)-1;
+    kda::PagedPrefillArgs a{};
+    a.N = N; a.T = T_total; a.Hq = H_q; a.Hkv = H_kv; a.d = d; a.bf16 = dtype == KDA_BF16;
+    a.window = window; a.sinks = sinks; a.max_length = max_length;
+    size_t need;
+    return kda::paged_prefill_groups(a, &need) > kda::max_groups(256) ? (size_t)-1 : need;
+}
+
+int kda_paged_prefill(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int64_t k_page_stride,
+                      int64_t v_page_stride, int32_t n_pages, int32_t page_size, const int32_t* page_table,
+                      int64_t table_stride, int32_t table_pages, const int32_t* lengths, const int32_t* cu_seqlens,
+                      int32_t N, int64_t T_total, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype, float scale,
+                      int32_t window, int32_t sinks, int64_t max_length, void* out, float* lse, void* workspace,
+                      size_t workspace_bytes, void* hip_stream) {
+    static const char* name = "kda_paged_prefill";
+    if (int rc = check_table(name, page_table, table_stride, N, table_pages, n_pages)) return rc;
+    const int64_t es = dtype == KDA_BF16 ? 2 : 4;
+    if (!sane_stride(k_page_stride) || !sane_stride(v_page_stride) || !sane_stride(q_stride))
+        return fail(KDA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40)", name);
+    const int64_t page = page_bytes_of(H_kv, page_size, d, es);
+    const Pool kp = pool_of(k_pages, k_page_stride * es, page, n_pages);
+    const Pool vp = pool_of(v_pages, v_page_stride * es, page, n_pages);
+    if (int rc = check_pages(name, kp, vp, page_size, H_kv, d, dtype, false)) return rc;
+    if (T_total < 0 || T_total > kMaxCount) return fail(KDA_ERR_INVALID_ARG, "%s: T_total must be in [0, 2^31)", name);
+    if (H_q <= 0 || H_q % H_kv || H_q > 16384)
+        return fail(KDA_ERR_INVALID_ARG, "%s: H_q must be a multiple of H_kv up to 16384", name);
+    if (!std::isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "%s: scale must be finite", name);
+    if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
+        return fail(KDA_ERR_INVALID_ARG, "%s: window and sinks must be >= 0, and sinks 0 without a window", name);
+    if (max_length < 0) return fail(KDA_ERR_INVALID_ARG, "%s: max_length must be >= 0", name);
+    const int64_t room = (int64_t)table_pages * page_size;
+    const int64_t most = max_length > 0 && max_length < room ? max_length : room;
+    if (room > kMaxCount - 4096)
+        return fail(KDA_ERR_INVALID_ARG, "%s: table_pages * page_size must be below 2^31 - 4096", name);
+    if (T_total > 0 && (N < 1 || !lengths || !cu_seqlens || !out))
+        return fail(KDA_ERR_INVALID_ARG, "%s: lengths, cu_seqlens, out and at least one sequence are required", name);
+    const Pool qi = rows_of(q, q_stride * es, (int64_t)H_q * d * es, T_total);
+    if (int rc = check_rows(name, "q", qi)) return rc;
+    if (!aligned16(out) || !aligned_to(lse, 4) || !aligned_to(lengths, 4) || !aligned_to(cu_seqlens, 4))
+        return fail(KDA_ERR_MISALIGNED, "%s: out must be 16-byte, lse, lengths and cu_seqlens 4-byte aligned", name);
+    kda::PagedPrefillArgs a{};
+    a.q = q; a.q_stride = q_stride; a.kp = k_pages; a.vp = v_pages;
+    a.kp_stride = k_page_stride; a.vp_stride = v_page_stride;
+    a.pt = kda::PageTable{page_table, table_stride, table_pages, n_pages};
+    a.lengths = lengths; a.cu = cu_seqlens; a.N = N; a.T = T_total; a.page_size = page_size;
+    a.Hq = H_q; a.Hkv = H_kv; a.d = d; a.bf16 = dtype == KDA_BF16; a.scale = scale;
+    a.window = window; a.sinks = sinks; a.max_length = most;
+    a.o = out; a.lse = lse; a.ws = workspace;
+    size_t need;
+    if (int rc = check_groups(name, kda::paged_prefill_groups(a, &need))) return rc;
+    if (int rc = check_workspace(name, workspace, workspace_bytes, need)) return rc;
+    const Span ins[] = {qi.span(), kp.span(), vp.span(), table_span(page_table, table_stride, N, table_pages),
+                        {lengths, (size_t)N * 4}, {cu_seqlens, (size_t)(N + 1) * 4}};
+    const Span outs[] = {{out, (size_t)T_total * H_q * d * es}, {lse, lse ? (size_t)T_total * H_q * 4 : 0},
+                         {workspace, need}};
+    if (int rc = check_alias(name, outs, ins)) return rc;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    if (debug_check() && T_total > 0) {
+        std::vector<int32_t> cu;
+        if (int rc = fetch(cu_seqlens, (size_t)N + 1, s, cu, name)) return rc;
+        if (int rc = kda_validate_cu_seqlens(cu.data(), N, T_total)) return rc;
+        if (int rc = debug_check_table(name, page_table, table_stride, lengths, N, table_pages, page_size, n_pages, most, s))
+            return rc;
+    }
+    if (injected_launch_failure()) return injected(name);
+    return check_hip(kda::launch_paged_prefill(a, s), s, name);
+}
+
 size_t kda_token_logprobs_workspace(int64_t R, int32_t V, int32_t top) {
     if (R < 0 || R > kMaxCount || V < 1 || V >= (1 << 24) || top < 0 || top > 64 || top > V ||
         kda::logprob_groups(R, V) > kda::max_groups(256))

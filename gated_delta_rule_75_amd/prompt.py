@@ -1,5 +1,5 @@
-"""Prompt chunks through the attention layers of a hybrid stack: rotary positions, and log-probabilities of the
-tokens that follow.
+"""Prompt chunks through the attention layers of a hybrid stack: rotary positions, attention over the
+cache's pages, and log-probabilities of the tokens that follow.
 
 New tokens are packed ``[T, H, d]`` with ``cu_seqlens`` int32 ``[N + 1]``; pages and tables are those of
 ``serving.py``.  Contracts: ``include/kda.h``.
@@ -160,6 +160,64 @@ def rotary_append(q, k, v, k_pages, v_pages, page_table, start, freqs, *, cu_seq
          T, freqs.data_ptr(), r, lay, amplitude, q_out.data_ptr(), qos, k_pages.data_ptr(), v_pages.data_ptr(), kps,
          vps, n_pages, page_size, page_table.data_ptr(), ts, P, Hq, H, d, code)
     return q_out
+
+
+def paged_prefill(q, k_pages, v_pages, page_table, lengths, cu_seqlens, *, scale=None, window=0, sinks=0,
+                  max_length=None, out=None, lse=None, workspace=None):
+    """Softmax attention of the new tokens of every sequence over its pages (their own keys and values among them).
+
+    q [T,H_q,d] (float32 or bfloat16; rows of any stride), packed segments with cu_seqlens int32 [N+1]; k_pages,
+    v_pages [n_pages,H_kv,page_size,d], page_table int32 [N,P], lengths int32 [N], the new tokens included: the
+    last one of sequence n is at position lengths[n] - 1.  A token sees those before it and itself; window > 0:
+    of these only the last `window` and the first `sinks`.  scale: 1 / sqrt(d) by default.  max_length: an upper
+    bound of lengths that sizes the launch (P * page_size by default).
+    Returns out [T,H_q,d] in q's dtype; with lse=True (or a tensor for it) (out, lse [T,H_q] float32).  A token
+    that sees none gives 0 and -inf; rows that belong to no sequence are not written."""
+    if serving._M is not None:
+        done = serving._M.paged_prefill(q, k_pages, v_pages, page_table, lengths, cu_seqlens, scale, window, sinks,
+                                        max_length, out, lse, workspace)
+        if done is not False:
+            return done
+    _int32(window=window, sinks=sinks)
+    code, di = _lead(q, "q")
+    dt = q.dtype
+    qs = _row(q, "q", dt, 3, di)
+    kps, vps = _row(k_pages, "k_pages", dt, 4, di), _row(v_pages, "v_pages", dt, 4, di)
+    shape, pages = q.shape, k_pages.shape
+    T, Hq, d = shape
+    n_pages, H, page_size, dp = pages
+    ts = _row(page_table, "page_table", _I32, 2, di)
+    N, P = page_table.shape
+    if v_pages.shape != pages or dp != d:
+        raise ValueError(f"q {tuple(shape)}, k_pages {tuple(pages)} and v_pages {tuple(v_pages.shape)} do not go "
+                         "together")
+    _vector(lengths, "lengths", _I32, (N,), di)
+    _vector(cu_seqlens, "cu_seqlens", _I32, (N + 1,), di)
+    dev = q.device
+    if out is None:
+        out = _EMPTY(shape, dtype=dt, device=dev)
+    else:
+        _vector(out, "out", dt, shape, di)
+    if lse is None or lse is False:
+        lse = pl = None
+    else:
+        if lse is True:
+            lse = _EMPTY((T, Hq), dtype=_F32, device=dev)
+        else:
+            _vector(lse, "lse", _F32, (T, Hq), di)
+        pl = lse.data_ptr()
+    most = P * page_size
+    if max_length is not None and max_length < most:
+        if max_length < 0:
+            raise ValueError("max_length must be >= 0")
+        most = max_length if max_length else 1  # 0 would mean no bound
+    L = _lib_()
+    _run_scratch(L.kda_paged_prefill, di, workspace,
+                 (L.kda_paged_prefill_workspace, N, T, Hq, H, d, code, most, window, sinks), q.data_ptr(), qs,
+                 k_pages.data_ptr(), v_pages.data_ptr(), kps, vps, n_pages, page_size, page_table.data_ptr(), ts, P,
+                 lengths.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, H, d, code, d ** -0.5 if scale is None else scale,
+                 window, sinks, most, out.data_ptr(), pl)
+    return out if lse is None else (out, lse)
 
 
 def _optional(t, name, dtype, shape, di):

@@ -592,6 +592,47 @@ int kda_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_
                       void* hip_stream);
 
 /*
+ * Prompt chunks: attention over pages
+ * ==========================================================================
+ *
+ * kda_paged_prefill — softmax attention of the new tokens of every sequence (packed segments, any number of each)
+ * over its pages, in which their own keys and values are already (kda_cache_append, kda_rotary_append):
+ *   s_t = scale * q . k_t,   out = sum_t softmax(s)_t v_t,   lse = log sum_t exp(s_t)
+ * The query of token i of sequence n, which has m = cu[n+1] - cu[n] new tokens, is at position
+ * p = lengths[n] - m + i and sees the tokens t <= p of its sequence (none for p < 0).
+ *   q          token r at r * q_stride elements: [H_q, d] dtype, contiguous; 16-byte
+ *              aligned, stride too.  Heads as in kda_paged_decode.
+ *   cu_seqlens DEVICE int32 [N + 1] as in kda_append_prefill
+ *   lengths    int32 [N], tokens of each sequence, the new ones among them
+ *   window     0, or of those only t > p - window ...
+ *   sinks      ... and t < sinks (0 without a window)
+ *   max_length an upper bound of lengths that sizes the launch; 0: table_pages * page_size (below 2^31 - 4096).
+ *              Tokens behind it are not visible.
+ *   out        [T_total, H_q, d] dtype, contiguous (unlike kda_paged_decode's: a prompt's rows go into a
+ *              projection of their type next); lse [T_total, H_q] float or NULL.  16-byte aligned.  Rows that belong
+ *              to no sequence are left as they were.
+ * A query without a visible token (or whose every visible score is -inf) gives out = 0 and lse = -inf.  Tokens that a
+ * query does not see never change its result, whatever bits their slots hold; a visible key or value that is not finite
+ * makes what it enters not finite, but for a weight of 0.  Products are exact in bf16 with fp32 sums; with KDA_BF16 the
+ * softmax weights are rounded to bf16 for their product with the values (their sum is not), which adds to
+ * the output's own rounding about as much again.
+ * workspace: kda_paged_prefill_workspace bytes for the same arguments, 256-byte aligned, overlapping no argument; holds
+ * the partial results where the keys of few rows are split over several workgroups.  Needs no initialisation.
+ * d in {64, 128, 256}; lengths and cu_seqlens are a caller contract (checked with KDA_DEBUG_CHECK=1).
+ */
+int kda_paged_prefill(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int64_t k_page_stride,
+                      int64_t v_page_stride, int32_t n_pages, int32_t page_size, const int32_t* page_table,
+                      int64_t table_stride, int32_t table_pages, const int32_t* lengths, const int32_t* cu_seqlens,
+                      int32_t N, int64_t T_total, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype, float scale,
+                      int32_t window, int32_t sinks, int64_t max_length, void* out, float* lse, void* workspace,
+                      size_t workspace_bytes, void* hip_stream);
+
+/* Workspace bytes of kda_paged_prefill, max_length being the smaller of the bound given and
+ * table_pages * page_size (not 0 for "no bound" here); (size_t)-1 for an unsupported or invalid combination. */
+size_t kda_paged_prefill_workspace(int32_t N, int64_t T_total, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype,
+                                   int64_t max_length, int32_t window, int32_t sinks);
+
+/*
  * Prompt chunks: log-probabilities of given tokens
  * ==========================================================================
  *
@@ -694,7 +735,9 @@ typedef enum {
     KDA_KERNEL_ROTARY = 23,        /* queries and keys rotated (and put into pages) */
     KDA_KERNEL_LOGPROB_SCAN = 24,  /* token log-probabilities: a row or a part of one */
     KDA_KERNEL_LOGPROB_JOIN = 25,  /* token log-probabilities: join of the split rows */
-    KDA_KERNEL_LOGPROB_GRAD = 26   /* gradient of token log-probabilities */
+    KDA_KERNEL_LOGPROB_GRAD = 26,  /* gradient of token log-probabilities */
+    KDA_KERNEL_PAGED_PREFILL = 27, /* attention of a chunk over pages */
+    KDA_KERNEL_PREFILL_JOIN = 28   /* attention of a chunk over pages: join of the split parts */
 } kda_kernel;
 
 int kda_timing_begin(void);

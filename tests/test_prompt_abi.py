@@ -36,6 +36,9 @@ SCORE = dict(logits=P[0], row=1000, tokens=P[1], R=50, V=1000, top=4, dtype=1, l
              best=P[5], which=P[6], ws=P[7], ws_bytes=1 << 20, stream=None)
 GRAD = dict(logits=P[0], row=1000, tokens=P[1], lse=P[2], entropy=P[3], d_logprobs=P[4], d_lse=P[5], d_entropy=P[6], R=50,
             V=1000, dtype=1, out=P[7], out_row=1000, stream=None)
+PREFILL = dict(q=P[0], q_stride=1024, kp=P[1], vp=P[2], kp_stride=8192, vp_stride=8192, n_pages=10, page=16, table=P[3],
+               stride=8, width=8, lengths=P[4], cu=P[5], N=4, T=100, Hq=8, Hkv=4, d=128, dtype=1, scale=0.1, window=0,
+               sinks=0, max_length=0, out=P[6], lse=P[7], ws=P[8], ws_bytes=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("name,defaults,change,status,says", [
@@ -98,6 +101,37 @@ GRAD = dict(logits=P[0], row=1000, tokens=P[1], lse=P[2], entropy=P[3], d_logpro
     ("kda_rotary_append", PLACE, dict(stride=7), -1, b"table rows overlap"),
     ("kda_rotary_append", PLACE, dict(stride=1 << 40), -1, b"strides"),
     ("kda_rotary_append", PLACE, dict(n_pages=0), -1, b"n_pages"),
+    ("kda_paged_prefill", PREFILL, dict(Hq=6), -1, b"multiple of H_kv"),
+    ("kda_paged_prefill", PREFILL, dict(d=192), -2, b"d=192"),
+    ("kda_paged_prefill", PREFILL, dict(dtype=2), -1, b"dtype"),
+    ("kda_paged_prefill", PREFILL, dict(page=24), -2, b"page_size=24"),
+    ("kda_paged_prefill", PREFILL, dict(scale=float("inf")), -1, b"scale"),
+    ("kda_paged_prefill", PREFILL, dict(window=-1), -1, b"window"),
+    ("kda_paged_prefill", PREFILL, dict(sinks=4), -1, b"sinks"),
+    ("kda_paged_prefill", PREFILL, dict(max_length=-1), -1, b"max_length"),
+    ("kda_paged_prefill", PREFILL, dict(width=1 << 27, stride=1 << 27), -1, b"2^31"),
+    ("kda_paged_prefill", PREFILL, dict(T=-1), -1, b"T_total"),
+    ("kda_paged_prefill", PREFILL, dict(T=1 << 31), -1, b"T_total"),
+    ("kda_paged_prefill", PREFILL, dict(N=0), -1, b"at least one"),
+    ("kda_paged_prefill", PREFILL, dict(lengths=None), -1, b"lengths"),
+    ("kda_paged_prefill", PREFILL, dict(cu=None), -1, b"cu_seqlens"),
+    ("kda_paged_prefill", PREFILL, dict(out=None), -1, b"out"),
+    ("kda_paged_prefill", PREFILL, dict(q=None), -1, b"q is required"),
+    ("kda_paged_prefill", PREFILL, dict(q_stride=1016), -1, b"overlap"),
+    ("kda_paged_prefill", PREFILL, dict(q_stride=1 << 40), -1, b"strides"),
+    ("kda_paged_prefill", PREFILL, dict(q=P[0] + 8), -3, b"16-byte"),
+    ("kda_paged_prefill", PREFILL, dict(out=P[6] + 8), -3, b"16-byte"),
+    ("kda_paged_prefill", PREFILL, dict(cu=P[5] + 2), -3, b"4-byte"),
+    ("kda_paged_prefill", PREFILL, dict(kp_stride=8184), -1, b"pages overlap"),
+    ("kda_paged_prefill", PREFILL, dict(stride=7), -1, b"table rows overlap"),
+    ("kda_paged_prefill", PREFILL, dict(stride=1 << 62), -1, b"strides"),
+    ("kda_paged_prefill", PREFILL, dict(out=P[0]), -4, b"overlaps an input"),
+    ("kda_paged_prefill", PREFILL, dict(out=P[1]), -4, b"overlaps an input"),
+    ("kda_paged_prefill", PREFILL, dict(lse=P[6] + 64), -4, b"overlap"),
+    ("kda_paged_prefill", PREFILL, dict(lse=P[5]), -4, b"overlap"),
+    ("kda_paged_prefill", PREFILL, dict(ws=P[8] + 16), -3, b"256-byte"),
+    ("kda_paged_prefill", PREFILL, dict(T=4, width=1024, stride=1024, ws=None), -5, b"needed"),
+    ("kda_paged_prefill", PREFILL, dict(T=4, width=1024, stride=1024, ws_bytes=64), -5, b"needed"),
     ("kda_token_logprobs", SCORE, dict(dtype=3), -1, b"dtype"),
     ("kda_token_logprobs", SCORE, dict(R=-1), -1, b"R must"),
     ("kda_token_logprobs", SCORE, dict(R=1 << 31), -1, b"R must"),
@@ -143,6 +177,8 @@ def test_calls_are_refused_before_any_launch(name, defaults, change, status, say
     ("kda_rotary", dict(ROTARY, k=None, k_out=None, Hk=0)), ("kda_rotary", dict(ROTARY, T=0, q=None, q_out=None)),
     ("kda_rotary_append", PLACE), ("kda_rotary_append", dict(PLACE, q_out=P[0])),
     ("kda_rotary_append", dict(PLACE, cu=None, N=100, stride=8)),
+    ("kda_paged_prefill", PREFILL), ("kda_paged_prefill", dict(PREFILL, vp=P[1], lse=None, window=5, sinks=2)),
+    ("kda_paged_prefill", dict(PREFILL, T=0, q=None, out=None, N=0)),
     ("kda_token_logprobs", SCORE), ("kda_token_logprobs", dict(SCORE, tokens=None, logprobs=None, entropy=None)),
     ("kda_token_logprobs", dict(SCORE, top=0, best=None, which=None, lse=None)),
     ("kda_token_logprobs_grad", GRAD), ("kda_token_logprobs_grad", dict(GRAD, out=P[0])),
@@ -172,6 +208,8 @@ def test_queries_and_keys_may_be_slices_of_one_projection(monkeypatch):
                         q_out=1 << 46), dict(T=8 * ((1 << 24) - 1)), dict(T=8 * ((1 << 24) - 1) + 1)),
     ("kda_rotary_append", dict(PLACE, Hq=16384, q_stride=16384 * 64, qo_stride=16384 * 64, d=64, r=64, q=1 << 50,
                                q_out=1 << 52, k=1 << 53, v=1 << 54), dict(T=8 * ((1 << 24) - 1)), dict(T=8 * ((1 << 24) - 1) + 1)),
+    ("kda_paged_prefill", dict(PREFILL, Hq=1, Hkv=1, d=64, q_stride=64, kp_stride=1024, vp_stride=1024, q=1 << 45,
+                               out=1 << 46, N=1), dict(T=32 * ((1 << 24) - 2)), dict(T=32 * ((1 << 24) - 1))),
     ("kda_token_logprobs", dict(SCORE, V=4, row=4), dict(R=(1 << 24) - 1), dict(R=1 << 24)),
     ("kda_token_logprobs_grad", dict(GRAD, V=4, row=4, out_row=4), dict(R=4 * ((1 << 24) - 1)), dict(R=(1 << 26) - 3)),
 ])
@@ -198,6 +236,20 @@ def test_binding_refuses_host_and_misshapen_tensors():
         kda.rotary_append(x, x, x, pages, pages, t[:, None], t, f)
 
 
+def test_workspace_of_paged_prefill():
+    _l, L = _lib()
+    bad = 2 ** 64 - 1
+    good = (2, 10, 8, 2, 128, 1, 5000, 0, 0)
+    assert L.kda_paged_prefill_workspace(*good) > 0
+    assert L.kda_paged_prefill_workspace(2, 100000, 8, 2, 128, 1, 5000, 0, 0) == 0
+    assert L.kda_paged_prefill_workspace(0, 0, 8, 2, 128, 1, 5000, 0, 0) == 0
+    for i, x in ((0, -1), (1, -1), (1, 1 << 31), (2, 7), (3, 0), (4, 96), (5, 2), (6, -1), (6, 1 << 31), (7, -1), (8, -1),
+                 (0, (1 << 31) - 1)):
+        args = list(good)
+        args[i] = x
+        assert L.kda_paged_prefill_workspace(*args) == bad, args
+
+
 def test_workspace_of_token_logprobs():
     _l, L = _lib()
     bad = 2 ** 64 - 1
@@ -205,6 +257,19 @@ def test_workspace_of_token_logprobs():
     assert L.kda_token_logprobs_workspace(5000, 100000, 5) == 0 and L.kda_token_logprobs_workspace(0, 100000, 5) == 0
     for args in ((-1, 10, 1), (5, 0, 0), (5, 1 << 24, 1), (5, 10, 11), (5, 100, 65), (5, 100, -1), (1 << 31, 100, 1)):
         assert L.kda_token_logprobs_workspace(*args) == bad, args
+
+
+def test_binding_refuses_misplaced_queries():
+    import gated_delta_rule_75_amd as kda
+
+    x, t, n = torch.zeros(2, 4, 64), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    pages = torch.zeros(3, 4, 16, 64)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        kda.paged_prefill(x, pages, pages, t, n, n)
+    with pytest.raises(ValueError, match="unsupported dtype"):
+        kda.paged_prefill(x.half(), pages, pages, t, n, n)
+    with pytest.raises(ValueError, match="window"):
+        kda.paged_prefill(x, pages, pages, t, n, n, window=2 ** 31)
 
 
 def test_binding_refuses_misplaced_logits():
