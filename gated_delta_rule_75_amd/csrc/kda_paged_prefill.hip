@@ -25,14 +25,12 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 16 bytes per lane from a buffer to LDS: lane i's go to to + 16 i; those behind the descriptor's end become 0.  Written
+// 16 bytes per lane from a buffer to LDS: lane i's go to at + 16 i; those behind the descriptor's end become 0.  Written
 // out, since the compiler would let every read of LDS wait for all such loads, also of those for the next tile.
 // (The clobber keeps the compiler's own uses of m0 whole, each of which sets it right before.)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, int offset, uint32_t more, const char* to) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane(
-        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)to);
+__device__ __forceinline__ void load_lds(u32x4 from, int offset, uint32_t more, uint32_t at) {
     // (a descriptor that vector instructions have written needs five wait states before a load)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
@@ -51,6 +49,11 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 y = {(__bf16)a, (__bf16)b};
     return __builtin_bit_cast(uint32_t, y);
+}
+// the larger of lane and lane ^ 32
+__device__ __forceinline__ float other_half_max(float x) {
+    const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 __device__ __forceinline__ f32x16 zeros() {
     f32x16 z;
@@ -113,7 +116,6 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
     constexpr int LOADS = kPage * ROW / 1024;      // 1 KiB loads of 16 rows
     constexpr int QW = ROW / 32;                   // 16-byte pieces of a lane's query row
     __shared__ __attribute__((aligned(1024))) char s_kv[S::BUFS][2][2 * S::TILE];  // keys and values, twice
-    __shared__ int s_on[2][BN / kPage];
     __shared__ float s_m[WAVES][32], s_l[WAVES][32];
 
     const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, hl = lane >> 5;
@@ -150,22 +152,23 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
     const int tiles = head_tiles + (end + BN - 1) / BN - first;
     const int t0 = part * plan.part_tiles, t1 = t0 + plan.part_tiles < tiles ? t0 + plan.part_tiles : tiles;
 
-    // this lane's row
+    // this lane's row, and its row of q and out (formed again behind the loop, where registers are free)
     const int my = ROWS ? w * 32 + lr : lr;
     const bool mine = my < rows;
-    const int my_i = (g0 + (mine ? my : 0)) / G, my_g = g0 + (mine ? my : 0) - my_i * G;
-    const int64_t token = cu0 + i0 + my_i;
+    auto token_of = [&](int r) { return cu0 + i0 + (g0 + r) / G; };
+    auto head_of = [&](int r) { return h * G + (g0 + r) % G; };
     const int wave_first = ROWS ? w * 32 : 0, wave_rows = rows - wave_first < 32 ? rows - wave_first : 32;
     const int pw_first = position(wave_rows > 0 ? wave_first : 0), pw_last = position(wave_rows > 0 ? wave_first + wave_rows - 1 : 0);
     const int p = mine ? position(my) : pw_last;
     const int p_near = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+    const int p_near_last = a.window > 0 && pw_last >= a.window ? pw_last - a.window + 1 : 0;
     const bool active = wave_rows > 0;
 
     // The scores' sign goes to the queries, so that the factor is positive; a scale of 0 makes them 0.
     const float scale2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
     u32x4 q[QW];
     {
-        const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + (int64_t)(h * G + my_g) * D;
+        const T* qr = static_cast<const T*>(a.q) + token_of(mine ? my : 0) * a.q_stride + (int64_t)head_of(mine ? my : 0) * D;
         const uint32_t flip = a.scale < 0.f ? (kBf16 ? 0x80008000u : 0x80000000u) : 0u;
 #pragma unroll
         for (int s = 0; s < QW; ++s) {
@@ -179,23 +182,33 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
         }
     }
 
-    // loads of tiles: the page numbers of the next 64 of this wave's 16-token pieces are in its lanes
-    constexpr int SUBS = BN / kPage;                          // pieces of a tile
-    constexpr int STEP = ROWS ? 1 : WAVES;                    // tiles between a wave's
-    constexpr int PER = ROWS ? 64 : 64 / SUBS;                // tiles that the lanes cover
-    const int my_sub = ROWS ? w % SUBS : lane % SUBS;
+    // Loads of tiles.  The lanes hold the pages of the wave's next tiles, a lane for each 16-token piece, and those of
+    // the tiles behind these are on their way.
+    constexpr int SUBS = BN / kPage;            // pieces of a tile
+    constexpr int STEP = ROWS ? 1 : WAVES;      // tiles between a wave's
+    constexpr int PER = 64 / SUBS;              // tiles that the lanes cover
     const int w0 = ROWS ? 0 : w;
-    const int32_t* table = a.pt.table + n * a.pt.stride;
-    int lane_page = -1;
-    auto base_of = [&](int t) { return t < head_tiles ? t * BN : (first + t - head_tiles) * BN; };
-    auto look_up = [&](int i) {  // for the wave's tiles i ..
-        const int t = t0 + w0 + STEP * (i + (ROWS ? lane : lane / SUBS));
-        lane_page = -1;
+    const int near_shift = (first - head_tiles) * BN;
+    auto base_of = [&](int t) { return t * BN + (t < head_tiles ? 0 : near_shift); };
+    uint64_t lane_k = 0, lane_v = 0;  // byte offsets of the pieces in the pools
+    uint64_t absent = ~0ull;          // lanes without a page
+    int next_page = -1, next_slot = 0;
+    auto look_up = [&](int i) {  // for the wave's tiles i .. i + PER - 1
+        const int t = t0 + w0 + STEP * (i + lane / SUBS);
+        next_page = -1;
         if (t < t1) {
-            const uint32_t col = (uint32_t)(base_of(t) + my_sub * kPage) / (uint32_t)a.page_size;
-            if (col < (uint32_t)a.pt.width) lane_page = table[col];
-            if (lane_page >= a.pt.n_pages) lane_page = -1;
+            const uint32_t pos = base_of(t) + lane % SUBS * kPage, col = pos / (uint32_t)a.page_size;
+            next_slot = (int)(pos - col * (uint32_t)a.page_size);
+            if (col < (uint32_t)a.pt.width) next_page = a.pt.table[n * a.pt.stride + col];
         }
+    };
+    auto advance = [&](int i) {
+        const bool on = next_page >= 0 && next_page < a.pt.n_pages;
+        const int64_t page = on ? next_page : 0, inner = ((int64_t)h * a.page_size + (on ? next_slot : 0)) * D;
+        lane_k = (uint64_t)(page * a.kp_stride + inner) * ES;
+        lane_v = (uint64_t)(page * a.vp_stride + inner) * ES;
+        absent = __ballot(!on);
+        look_up(i + PER);
     };
     // byte offsets of this lane's 16 bytes inside rows 0 .. 7 and 8 .. 15 of a piece
     int k_at[2], v_at[2];
@@ -205,42 +218,60 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
         k_at[e] = r * ROW + ((lane % 8) ^ swizzle_k(r)) * 16;
         v_at[e] = r * ROW + ((lane % 8) ^ swizzle_v<ES>(r)) * 16;
     }
-    // piece `sub` of tile t: keys or values, from the page to its place in LDS; rows behind the last visible one, or
-    // without a page, become 0
-    auto load_piece = [&](const void* pages, int64_t stride, int page, int t, int sub, const int (&at)[2], char* to) {
-        const int pos = base_of(t) + sub * kPage, limit = t < head_tiles ? head : end;
-        const int left = page >= 0 ? limit - pos : 0, on = left < 0 ? 0 : left > kPage ? kPage : left;
-        const int slot16 = (int)((uint32_t)pos % (uint32_t)a.page_size);
-        const T* from = static_cast<const T*>(pages) + (page >= 0 ? page : 0) * stride +
-                        ((int64_t)h * a.page_size + slot16) * D;
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(from, (uint32_t)(on * ROW));
-#pragma unroll
-        for (int e = 0; e < LOADS; ++e)
-            load_lds(r, at[e & 1], (e >> 1) * 128, to + (e >> 1) * BN * 128 + sub * kPage * 128 + (e & 1) * 1024);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)s_kv[ROWS ? 0 : w]);
+    // A wave's loads of a tile: PIECES pieces (keys or values of 16 tokens) of LOADS loads each, from the page to their
+    // place in LDS.  Rows behind the last visible one, without a page or behind the last tile become 0.
+    constexpr int PIECES = ROWS ? 2 * SUBS / WAVES : 2 * SUBS, ALL_LOADS = PIECES * LOADS;
+    u32x4 from;
+    struct Next {
+        int i, base, limit;  // the wave's tile, its first token, the end of what is visible
     };
-    auto load = [&](int i, char* to, int* on) {  // the wave's tile i
-        const int t = t0 + w0 + STEP * i;
-        if (i % PER == 0) look_up(i);
-        if (t >= t1) return;
-        if constexpr (ROWS) {
-            const int page = __builtin_amdgcn_readlane(lane_page, i & 63), sub = w % SUBS;
-            if (SUBS == WAVES || w < SUBS) load_piece(a.kp, a.kp_stride, page, t, sub, k_at, to);
-            if (SUBS == WAVES || w >= SUBS) load_piece(a.vp, a.vp_stride, page, t, sub, v_at, to + S::TILE);
-            if (lane == 0 && w < SUBS) on[sub] = page >= 0;
-        } else {
+    auto next_of = [&](int i) {
+        const int t = t0 + w0 + STEP * i, sink = t < head_tiles;
+        const int base = t * BN + (sink ? 0 : near_shift), limit = sink ? head : end;
+        return Next{i, base, t < t1 ? limit : 0};
+    };
+    auto load = [&](const Next& x, int n) {  // load n of a tile, into buffer i & 1
+        const int i = x.i, u = n / LOADS, e = n % LOADS;
+        // rows: piece w of the keys, then of the values (or one of these); else keys and values of each in turn
+        const int sub = ROWS ? w % SUBS : u / 2;
+        const bool keys = ROWS ? (PIECES == 2 ? u == 0 : w < SUBS) : u % 2 == 0;
+        if (e == 0) {
+            const int lane_of = i % PER * SUBS + sub;
+            const uint64_t at = keys ? lane_k : lane_v;
+            const uint64_t y = reinterpret_cast<uint64_t>(keys ? a.kp : a.vp) +
+                               ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(at >> 32), lane_of) << 32 |
+                                (uint32_t)__builtin_amdgcn_readlane((uint32_t)at, lane_of));
+            const int left = min(max(x.limit - x.base - sub * kPage, 0), kPage);
+            const int on = (absent >> lane_of) & 1 ? 0 : left;
+            from = u32x4{(uint32_t)y, (uint32_t)(y >> 32) & 0xFFFFu, (uint32_t)(on * ROW), 0x00020000u};
 #pragma unroll
-            for (int sub = 0; sub < SUBS; ++sub) {
-                const int page = __builtin_amdgcn_readlane(lane_page, (i % PER) * SUBS + sub);
-                load_piece(a.kp, a.kp_stride, page, t, sub, k_at, to);
-                load_piece(a.vp, a.vp_stride, page, t, sub, v_at, to + S::TILE);
-            }
+            for (int c = 0; c < 3; ++c) from[c] = __builtin_amdgcn_readfirstlane(from[c]);  // says that it is uniform
         }
+        load_lds(from, (keys ? k_at : v_at)[e & 1], (e >> 1) * 128,
+                 lds + (i & 1) * 2 * S::TILE + (keys ? 0 : S::TILE) + (e >> 1) * BN * 128 + sub * kPage * 128 + (e & 1) * 1024);
     };
+    auto load_all = [&](const Next& x) {
+#pragma unroll
+        for (int n = 0; n < ALL_LOADS; ++n) load(x, n);
+    };
+    auto absent_of = [&](int i) { return (int)(absent >> (i % PER * SUBS)) & ((1 << SUBS) - 1); };
 
     f32x16 o[CT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) o[c] = zeros();
-    float m = -INFINITY, ref = 0.f, l = 0.f;  // running maximum (of the unscaled scores), its product with scale2
+    // The reference of a row's weights is the largest (unscaled) score of the first tile in which it sees a key, and
+    // stays: larger scores later give weights above 1, with the same relative precision, and nothing has to be
+    // rescaled or compared.  Only where sums have left the range of fp32 in the end (a score beyond the reference by
+    // some 80), the largest score of all is looked for in another pass and the row's sums are formed again.
+    float m = -INFINITY, ref = 0.f;  // reference, its product with scale2 (0 while there is none)
+    int pass = 0;
+    bool left = false;  // this row's sums have left the range
+    uint32_t spoiled[CT / 2];  // outputs that a value which is not finite enters, a bit for each
+#pragma unroll
+    for (int c = 0; c < CT / 2; ++c) spoiled[c] = 0;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 
     int k_lane[4], v_lane[2];  // this lane's places in a tile's blocks
 #pragma unroll
@@ -272,14 +303,94 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
     auto value32 = [&](const char* vt, int c, int kg, int i) {  // fp32: two keys
         return *reinterpret_cast<const float*>(vt + c * BN * 128 + (kg * 32 + 8 * (i >> 2) + (i & 3)) * 128 + v_lane[0]);
     };
-    // bits of the bf16 of a word that are not finite
+    // The bits of the bf16 of a word that are not finite: an exponent of ones carries into the sign's place.
     auto odd_bits = [](uint32_t v) {
-        return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+        const uint32_t s = ((v & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+        return (s << 1) - (s >> 15);
     };
 
-    // One tile of the wave's rows.  EDGE: some key of it is not visible to some row.
-    auto work = [&](const char* kt, int base, int lo, int hi, int absent, auto edge) {
-        constexpr bool EDGE = decltype(edge)::value;
+    // One tile that every row of the wave sees whole.  What is read from LDS is a stream of 16-byte pieces per lane:
+    // the keys' in order, then the values'.  Six of them are on their way, each is used by the products of one step
+    // and replaced by the next; the softmax of the first 32 keys goes under the score products of the second, that of the
+    // second under the outputs of the first, and what it takes to ask for the next tile under the scores.  The order is
+    // written out, since the compiler's own asks LDS for each
+    // piece right before its use.
+    constexpr int NK = QW, NV = kBf16 ? 2 * CT : 4 * CT;  // pieces of 32 keys, and of their values
+    constexpr int AHEAD = 6;
+    constexpr int EACH = (ALL_LOADS + KG * NK - 1) / (KG * NK);  // loads of the next tile under each of the first steps
+    auto work = [&](const char* kt, const Next& next) {
+        const char* vt = kt + S::TILE;
+        auto piece = [&](int j) {
+            u32x4 y;
+            if (j < KG * NK) {
+                y = *reinterpret_cast<const u32x4*>(kt + (j % NK / 4) * BN * 128 + (j / NK) * 32 * 128 + k_lane[j % NK & 3]);
+            } else {
+                const int kg = (j - KG * NK) / NV, at = (j - KG * NK) % NV, c = at % CT;
+                if constexpr (kBf16) {
+                    y = value(vt, c, kg, at / CT);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = __float_as_uint(value32(vt, c, kg, at / CT * 4 + i));
+                }
+            }
+            return y;
+        };
+        f32x16 x[KG];
+        float e[KG][16];      // weights
+        u32x4 rounded[KG][2];
+        auto weights = [&](int kg, int from, int to) {
+#pragma unroll
+            for (int i = from; i < to; ++i) {
+                e[kg][i] = exp2_hw(__builtin_fmaf(x[kg][i], scale2, -ref));
+                sum[i & 3] += e[kg][i];
+                if (kBf16 && (i & 1)) rounded[kg][i / 8][i % 8 / 2] = pack_bf16(e[kg][i - 1], e[kg][i]);
+            }
+        };
+        u32x4 ring[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) ring[j] = piece(j);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < KG * (NK + NV); ++j) {
+            const u32x4 y = ring[j % AHEAD];
+            if (j < KG * NK) {
+                const int kg = j / NK, s = j % NK;
+                if (s == 0) x[kg] = zeros();
+                if constexpr (kBf16) {
+                    x[kg] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, y),
+                                                                    __builtin_bit_cast(bf16x8, q[s]), x[kg], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[kg] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(y[i]), __uint_as_float(q[s][i]),
+                                                                     x[kg], 0, 0, 0);
+                }
+                // (not in the first step: the last product of the scores takes a while)
+                if (kg > 0 && s > 0) weights(kg - 1, 16 * (s - 1) / (NK - 1), 16 * s / (NK - 1));
+            } else {
+                const int kg = (j - KG * NK) / NV, at = (j - KG * NK) % NV, c = at % CT, part = at / CT;
+                if (kg == 0 && at == 0 && KG == 1) weights(0, 0, 16);
+                if constexpr (kBf16) {
+                    o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, y), __builtin_bit_cast(bf16x8, rounded[kg][part]), o[c], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[c] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(y[i]), e[kg][4 * part + i], o[c], 0, 0, 0);
+                }
+                if (kg + 1 < KG && at > 0) weights(kg + 1, 16 * (at - 1) / (NV - 1), 16 * at / (NV - 1));
+            }
+            if (j + AHEAD < KG * (NK + NV)) ring[j % AHEAD] = piece(j + AHEAD);
+            if (j < (ALL_LOADS + EACH - 1) / EACH) {
+#pragma unroll
+                for (int n = j * EACH; n < (j + 1) * EACH && n < ALL_LOADS; ++n) load(next, n);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    // One tile of which some key is not visible to some row, or where some row has no reference yet.
+    auto work_edge = [&](const char* kt, int base, int lo, int hi, int gone) {
         const char* vt = kt + S::TILE;
         f32x16 x[KG];
 #pragma unroll
@@ -300,36 +411,32 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        float top = -INFINITY;
+        {
+            // visible: places first .. first + many - 1 of the tile, and the sinks' 0 .. more - 1, for this lane's half
+            const int top = (hi - 1 < p ? hi - 1 : p) - base + 1;  // places below it
+            const int from = (lo > p_near ? lo : p_near) - base, many = top > from ? top - from : 0;
+            const int sink = (a.sinks < base + top ? a.sinks : base + top) - lo, more = sink > 0 ? sink : 0;
+            const int first = 4 * hl - from, less = 4 * hl - (lo - base);
 #pragma unroll
-        for (int kg = 0; kg < KG; ++kg)
+            for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if constexpr (EDGE) {
-                    const int at = kg * 32 + 8 * (i >> 2) + 4 * hl + (i & 3), t = base + at;
-                    const bool on = (t >= lo) & (t < hi) & (t <= p) & ((t >= p_near) | (t < a.sinks)) &
-                                    !((absent >> (at / kPage)) & 1);
-                    x[kg][i] = on ? x[kg][i] : -INFINITY;
+                for (int i = 0; i < 16; ++i) {
+                    const int at = kg * 32 + 8 * (i >> 2) + (i & 3);
+                    const bool on = ((uint32_t)(first + at) < (uint32_t)many) | ((uint32_t)(less + at) < (uint32_t)more);
+                    x[kg][i] = (on & !((gone >> (at / kPage)) & 1)) ? x[kg][i] : -INFINITY;
                 }
-                top = fmaxf(top, x[kg][i]);
-            }
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        // The maximum is followed where it has grown by more than 2^8: weights stay below 2^8 otherwise, which
-        // neither their rounding nor the sums mind
-        const bool up = (top - m) * scale2 > 8.f;
-        if (__any(up)) {
-            const float now = up ? top : m, r = now == -INFINITY ? 0.f : now * scale2;
-            const float keep = exp2_hw(m == -INFINITY ? -INFINITY : ref - r);
-            l *= keep;
+        }
+        if (pass == 1 || __any(m == -INFINITY)) {
+            float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
+            for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[c][i] *= keep;
-            m = now;
-            ref = r;
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, x[kg][i]);
+            top = other_half_max(top);
+            m = pass == 1 && left ? fmaxf(m, top) : m == -INFINITY ? top : m;
+            ref = m == -INFINITY ? 0.f : m * scale2;
         }
         uint32_t pf[KG][8];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
@@ -337,33 +444,30 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
                 x[kg][i] = exp2_hw(__builtin_fmaf(x[kg][i], scale2, -ref));
                 sum[i & 3] += x[kg][i];
             }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        // bf16: the weights are rounded to 8 bits for the product, as the output is; the sum l has them unrounded
+        // bf16: the weights are rounded to 8 bits for the product, as the output is; their sum has them unrounded
         if constexpr (kBf16) {
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) pf[kg][i / 2] = pack_bf16(x[kg][i], x[kg][i + 1]);
         }
-        // In a tile with hidden keys, values that are not finite count as 0: a hidden one's weight of 0 would make
-        // them NaN.  Their sight makes the sums NaN below.
+        // In a tile with hidden keys, values that are not finite count as 0: a hidden one's weight of 0 would make them
+        // NaN.  The outputs that see them are noted below.
         uint32_t odd = 0;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
+        for (int kg = 0; kg < KG; ++kg) {
 #pragma unroll
-            for (int kg = 0; kg < KG; ++kg) {
+            for (int c = 0; c < CT; ++c) {
                 if constexpr (kBf16) {
 #pragma unroll
                     for (int st = 0; st < 2; ++st) {
                         u32x4 v = value(vt, c, kg, st);
-                        if constexpr (EDGE) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t y = odd_bits(v[i]);
-                                odd |= y;
-                                v[i] &= ~y;
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t y = odd_bits(v[i]);
+                            odd |= y;
+                            v[i] &= ~y;
                         }
                         const u32x4 y = {pf[kg][4 * st], pf[kg][4 * st + 1], pf[kg][4 * st + 2], pf[kg][4 * st + 3]};
                         o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
@@ -373,110 +477,131 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float v = value32(vt, c, kg, i);
-                        if constexpr (EDGE) {
-                            const bool y = !(fabsf(v) < INFINITY);
-                            odd |= y;
-                            v = y ? 0.f : v;
-                        }
+                        const bool y = !(fabsf(v) < INFINITY);
+                        odd |= y;
+                        v = y ? 0.f : v;
                         o[c] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, x[kg][i], o[c], 0, 0, 0);
                     }
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (EDGE) {
-            if (__any(odd != 0)) {  // how many such values each sum has a weight for
+        if (__any(odd != 0)) {  // how many such values each sum has a weight for
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    f32x16 count = zeros();
+            for (int c = 0; c < CT; ++c) {
+                f32x16 count = zeros();
 #pragma unroll
-                    for (int kg = 0; kg < KG; ++kg) {
-                        if constexpr (kBf16) {
+                for (int kg = 0; kg < KG; ++kg) {
+                    if constexpr (kBf16) {
 #pragma unroll
-                            for (int st = 0; st < 2; ++st) {
-                                u32x4 v = value(vt, c, kg, st), y;
+                        for (int st = 0; st < 2; ++st) {
+                            u32x4 v = value(vt, c, kg, st), y;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const uint32_t z = pf[kg][4 * st + i];
-                                    v[i] = odd_bits(v[i]) & 0x3F803F80u;
-                                    y[i] = ((z & 0x7FFFu) ? 0x3F80u : 0u) | ((z & 0x7FFF0000u) ? 0x3F800000u : 0u);
-                                }
-                                count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                    __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, y), count, 0, 0, 0);
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t z = pf[kg][4 * st + i];
+                                v[i] = odd_bits(v[i]) & 0x3F803F80u;
+                                // 1 for a weight that is not 0 (no weight is negative, and the least one is 2^-133)
+                                const uint32_t s = ((z & 0x7FFF7FFFu) + 0x7FFF7FFFu) & 0x80008000u;
+                                y[i] = ((s << 1) - (s >> 15)) & 0x3F803F80u;
                             }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                count = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                                    fabsf(value32(vt, c, kg, i)) < INFINITY ? 0.f : 1.f, x[kg][i] != 0.f ? 1.f : 0.f, count,
-                                    0, 0, 0);
+                            count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, y), count, 0, 0, 0);
                         }
-                    }
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[c][i] = count[i] > 0.f ? NAN : o[c][i];
-                    __builtin_amdgcn_sched_barrier(0);
+                        for (int i = 0; i < 16; ++i)
+                            count = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                fabsf(value32(vt, c, kg, i)) < INFINITY ? 0.f : 1.f, x[kg][i] != 0.f ? 1.f : 0.f, count,
+                                0, 0, 0);
+                    }
                 }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) spoiled[c / 2] |= (count[i] > 0.f ? 1u : 0u) << (c % 2 * 16 + i);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
-    auto tile = [&](int t, const char* kt, int absent) {
-        const bool sink = t < head_tiles;
-        const int base = base_of(t), lo = sink ? 0 : near, hi = sink ? head : end;
-        if (!active || base > pw_last) return;
-        const bool whole = absent == 0 && base >= lo && base + BN <= hi && base + BN - 1 <= pw_first &&
-                           (a.window == 0 || base > pw_last - a.window || base + BN <= a.sinks);
-        if (whole) work(kt, base, lo, hi, 0, std::false_type{});
-        else work(kt, base, lo, hi, absent, std::true_type{});
+    // tiles that every row of the wave sees whole: from the last row's window on, up to the first row's position
+    bool ready = false;  // all rows of the wave have a reference
+    const int whole_lo = p_near_last > near ? p_near_last : near, whole_hi = pw_first + 1 < end ? pw_first + 1 : end;
+    const int whole_t0 = head_tiles - first + (whole_lo + BN - 1) / BN, whole_t1 = head_tiles - first + whole_hi / BN;
+    auto whole = [&](int i) {
+        const int t = t0 + w0 + STEP * i;
+        return ready && absent_of(i) == 0 && t >= whole_t0 && t < whole_t1;
+    };
+    auto begin = [&](int i) {  // tile i is there, and the other buffer has been read
+        if ((i + 1) % PER == 0) advance(i + 1);
+        wait_loads();
+        if constexpr (ROWS) __syncthreads();
     };
 
-    if constexpr (ROWS) {
-        const int steps = t1 - t0;
-        auto absent_of = [&](const int* on) {
-            int x = 0;
-#pragma unroll
-            for (int s = 0; s < SUBS; ++s) x |= (on[s] ? 0 : 1) << s;
-            return __builtin_amdgcn_readfirstlane(x);
-        };
-        if (steps > 0) load(0, s_kv[0][0], s_on[0]);
-        for (int i = 0; i < steps; ++i) {
-            wait_loads();
-            __syncthreads();  // tile i is there, and the other buffer has been read
-            load(i + 1, s_kv[0][(i + 1) & 1], s_on[(i + 1) & 1]);
-            tile(t0 + i, s_kv[0][i & 1], absent_of(s_on[i & 1]));
-        }
-    } else {
-        const int steps = t1 - t0 - w > 0 ? (t1 - t0 - w + WAVES - 1) / WAVES : 0;
-        auto absent_of = [&](int i) {
-            int x = 0;
-#pragma unroll
-            for (int s = 0; s < SUBS; ++s) x |= (__builtin_amdgcn_readlane(lane_page, (i % PER) * SUBS + s) < 0 ? 1 : 0) << s;
-            return x;
-        };
-        int on = 0;
-        if (steps > 0) {
-            load(0, s_kv[w][0], nullptr);
-            on = absent_of(0);
-        }
-        for (int i = 0; i < steps; ++i) {
-            int then = 0;
-            wait_loads();
-            if (i + 1 < steps) {
-                load(i + 1, s_kv[w][(i + 1) & 1], nullptr);
-                then = absent_of(i + 1);
+    const int steps = t1 - t0 - w0 > 0 ? (t1 - t0 - w0 + STEP - 1) / STEP : 0;
+    float l;
+    for (;; ++pass) {
+        ready = pass == 2;
+        look_up(0);
+        advance(0);
+        load_all(next_of(0));
+        // (two loops, since the compiler would copy the outputs for every tile where two paths of one loop change them)
+        for (int i = 0; i < steps;) {
+            for (; i < steps && !whole(i); ++i) {
+                const int t = t0 + w0 + STEP * i, base = base_of(t), gone = absent_of(i);
+                begin(i);
+                load_all(next_of(i + 1));
+                if (!active || base > pw_last) continue;
+                work_edge(s_kv[ROWS ? 0 : w][i & 1], base, t < head_tiles ? 0 : near, t < head_tiles ? head : end, gone);
+                ready = pass != 1 && !__any(m == -INFINITY);
             }
-            tile(t0 + w + WAVES * i, s_kv[w][i & 1], on);
-            on = then;
+            for (; i < steps && whole(i); ++i) {
+                begin(i);
+                work(s_kv[ROWS ? 0 : w][i & 1], next_of(i + 1));
+            }
         }
+        wait_loads();
+        l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (pass == 2) break;
+        bool again = pass == 1;
+        if (pass == 0) {
+            float odd = l * 0.f;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) odd = __builtin_fmaf(o[c][i], 0.f, odd);
+            left = odd != odd;
+            left = left | (__shfl_xor((int)left, 32, 64) != 0);
+            again = __any(left);
+        }
+        if (ROWS ? !__syncthreads_or(again) : !again) break;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) o[c] = zeros();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = 0.f;
     }
 
     l += __shfl_xor(l, 32, 64);
-    const int64_t out_row = token * a.Hq + h * G + my_g;
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[c][i] = (spoiled[c / 2] >> (c % 2 * 16 + i)) & 1 ? NAN : o[c][i];
+    // Sums that are joined with others are brought near 1 first, by a power of two.
+    float base = m == -INFINITY ? -INFINITY : ref;
+    if (!ROWS || plan.parts > 1) {
+        const int e = l > 0.f && l < INFINITY ? __builtin_amdgcn_frexp_expf(l) : 0;
+        l = __builtin_amdgcn_ldexpf(l, -e);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[c][i] = __builtin_amdgcn_ldexpf(o[c][i], -e);
+        if (m != -INFINITY) base = ref + (float)e;
+    }
+    int mine_again = mine ? my : 0;
+    asm volatile("" : "+v"(mine_again));
+    const int64_t out_row = token_of(mine_again) * a.Hq + head_of(mine_again);
     auto finish = [&](float M, float L, int64_t row) {  // log-sum of a row
         if (a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
     };
     if constexpr (ROWS) {
         if (!mine) return;
-        const float base = m == -INFINITY ? -INFINITY : ref;
         if (plan.parts > 1) {
             if (hl == 0) part_ml[out_row * plan.parts + part] = make_float2(base, l);
             if (l == 0.f) return;
@@ -505,7 +630,6 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
         // join the waves: their sums go where the tiles were, half of the channels into each buffer
         constexpr int HALF = D / 2, PITCH = HALF + 4;
         static_assert(32 * PITCH * 4 <= 2 * S::TILE, "half of a wave's outputs fits a buffer");
-        const float base = m == -INFINITY ? -INFINITY : ref;
         if (hl == 0) {
             s_m[w][lr] = base;
             s_l[w][lr] = l;
@@ -538,8 +662,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
                 const float* from = reinterpret_cast<const float*>(s_kv[i][c / HALF]) + r * PITCH + c % HALF;
                 y += *reinterpret_cast<const f32x4*>(from);
             }
-            const int ri = (g0 + r) / G;
-            const int64_t row = (cu0 + i0 + ri) * a.Hq + h * G + (g0 + r - ri * G);
+            const int64_t row = token_of(r) * a.Hq + head_of(r);
             if (plan.parts > 1) {
                 if (c == 0) part_ml[row * plan.parts + part] = make_float2(top, L);
                 *reinterpret_cast<f32x4*>(part_o + (row * plan.parts + part) * D + c) = y;
