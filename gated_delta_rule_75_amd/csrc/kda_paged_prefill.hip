@@ -41,6 +41,11 @@ __device__ __forceinline__ void load_lds(u32x4 from, int offset, uint32_t more, 
 // Everything that this wave's loads bring into LDS is there (a barrier alone does not wait for it), and it has read what
 // it asked LDS for, so that the next loads may go there.
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+// The same for all but the last N loads (loads of the compiler's that come between make it wait for more).
+template <int N>
+__device__ __forceinline__ void wait_loads_but() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kPage = 16;  // tokens that surely share a page
@@ -54,6 +59,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float other_half_max(float x) {
     const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+// what the rounding of a and b to y has left of them, rounded
+__device__ __forceinline__ uint32_t rest_of(float a, float b, uint32_t y) {
+    return pack_bf16(a - __uint_as_float(y << 16), b - __uint_as_float(y & 0xFFFF0000u));
 }
 __device__ __forceinline__ f32x16 zeros() {
     f32x16 z;
@@ -69,8 +78,10 @@ __device__ __forceinline__ int swizzle_k(int r) { return ((r >> 1) & 1) << 2 | (
 template <int ES>
 __device__ __forceinline__ int swizzle_v(int r) { return ES == 2 ? ((r >> 1) & 1) << 2 : 0; }
 
-// How a kernel instance splits its work.  ROWS: four waves with 32 rows each share a tile of keys.  Otherwise the
-// waves share 32 rows and each has tiles of its own.
+// How a kernel instance splits its work.
+// ROWS (many rows): four waves with 32 rows each share a tile of keys and values, and load the next into a second buffer.
+// Otherwise (few rows) the waves share 32 rows and each has tiles of its own, in one buffer: the next keys are asked for
+// when the scores are there, the next values behind the outputs, so that twice as many waves' loads are under way.
 template <typename T, int D, bool ROWS>
 struct Shape {
     static constexpr int ES = sizeof(T), ROW = D * ES;
@@ -79,8 +90,8 @@ struct Shape {
     static constexpr int THREADS = 64 * WAVES;
     static constexpr int RT = ROWS ? 128 : 32;               // rows of a workgroup
     static constexpr int TILE = BN * ROW;                    // bytes of a tile's keys
-    static constexpr int BUFS = ROWS ? 1 : WAVES;            // tiles at a time
-    static constexpr int GROUPS = ROWS && ROW <= 512 ? 2 : 1;  // workgroups a CU should hold
+    static constexpr int BUFS = ROWS ? 2 : WAVES;            // tiles in LDS
+    static constexpr int PER_SIMD = ROW <= (ROWS ? 512 : 256) ? 2 : 1;  // waves
 };
 
 // Row tiles of all sequences: tile k of sequence n has slot floor(cu[n] G / RT) + n + k, which leaves every sequence
@@ -108,14 +119,14 @@ struct PrefillPlan {
 };
 
 template <typename T, int D, bool ROWS>
-__global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::GROUPS)) void paged_prefill_kernel(
+__global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::PER_SIMD)) void paged_prefill_kernel(
     PagedPrefillArgs a, PrefillPlan plan, float2* part_ml, float* part_o) {
     using S = Shape<T, D, ROWS>;
     constexpr bool kBf16 = std::is_same<T, uint16_t>::value;
     constexpr int ES = S::ES, ROW = S::ROW, BN = S::BN, WAVES = S::WAVES, RT = S::RT, KG = BN / 32, CT = D / 32;
     constexpr int LOADS = kPage * ROW / 1024;      // 1 KiB loads of 16 rows
     constexpr int QW = ROW / 32;                   // 16-byte pieces of a lane's query row
-    __shared__ __attribute__((aligned(1024))) char s_kv[S::BUFS][2][2 * S::TILE];  // keys and values, twice
+    __shared__ __attribute__((aligned(1024))) char s_kv[S::BUFS][2 * S::TILE];  // keys, values
     __shared__ float s_m[WAVES][32], s_l[WAVES][32];
 
     const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, hl = lane >> 5;
@@ -232,11 +243,11 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
         const int base = t * BN + (sink ? 0 : near_shift), limit = sink ? head : end;
         return Next{i, base, t < t1 ? limit : 0};
     };
-    auto load = [&](const Next& x, int n) {  // load n of a tile, into buffer i & 1
+    auto load = [&](const Next& x, int n) {  // load n of a tile
         const int i = x.i, u = n / LOADS, e = n % LOADS;
-        // rows: piece w of the keys, then of the values (or one of these); else keys and values of each in turn
-        const int sub = ROWS ? w % SUBS : u / 2;
-        const bool keys = ROWS ? (PIECES == 2 ? u == 0 : w < SUBS) : u % 2 == 0;
+        // rows: piece w of the keys, then of the values (or one of these); else all of the keys, then of the values
+        const int sub = ROWS ? w % SUBS : u % SUBS;
+        const bool keys = ROWS ? (PIECES == 2 ? u == 0 : w < SUBS) : u < SUBS;
         if (e == 0) {
             const int lane_of = i % PER * SUBS + sub;
             const uint64_t at = keys ? lane_k : lane_v;
@@ -250,11 +261,11 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
             for (int c = 0; c < 3; ++c) from[c] = __builtin_amdgcn_readfirstlane(from[c]);  // says that it is uniform
         }
         load_lds(from, (keys ? k_at : v_at)[e & 1], (e >> 1) * 128,
-                 lds + (i & 1) * 2 * S::TILE + (keys ? 0 : S::TILE) + (e >> 1) * BN * 128 + sub * kPage * 128 + (e & 1) * 1024);
+                 lds + (ROWS ? (i & 1) * 2 * S::TILE : 0) + (keys ? 0 : S::TILE) + (e >> 1) * BN * 128 + sub * kPage * 128 + (e & 1) * 1024);
     };
-    auto load_all = [&](const Next& x) {
+    auto load_some = [&](const Next& x, int from, int to) {
 #pragma unroll
-        for (int n = 0; n < ALL_LOADS; ++n) load(x, n);
+        for (int n = from; n < to; ++n) load(x, n);
     };
     auto absent_of = [&](int i) { return (int)(absent >> (i % PER * SUBS)) & ((1 << SUBS) - 1); };
 
@@ -390,8 +401,9 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
     };
 
     // One tile of which some key is not visible to some row, or where some row has no reference yet.
-    auto work_edge = [&](const char* kt, int base, int lo, int hi, int gone) {
+    auto work_edge = [&](const char* kt, int base, int lo, int hi, int gone, const Next& next) {
         const char* vt = kt + S::TILE;
+        if constexpr (!ROWS) wait_loads_but<ALL_LOADS / 2>();
         f32x16 x[KG];
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
@@ -411,6 +423,10 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
             }
         }
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!ROWS) {
+            wait_loads_but<ALL_LOADS / 2>();
+            load_some(next, 0, ALL_LOADS / 2);
+        }
         {
             // visible: places first .. first + many - 1 of the tile, and the sinks' 0 .. more - 1, for this lane's half
             const int top = (hi - 1 < p ? hi - 1 : p) - base + 1;  // places below it
@@ -436,7 +452,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
             m = pass == 1 && left ? fmaxf(m, top) : m == -INFINITY ? top : m;
             ref = m == -INFINITY ? 0.f : m * scale2;
         }
-        uint32_t pf[KG][8];
+        uint32_t pf[KG][8], pr[KG][8];
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
@@ -444,17 +460,20 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
                 x[kg][i] = exp2_hw(__builtin_fmaf(x[kg][i], scale2, -ref));
                 sum[i & 3] += x[kg][i];
             }
-        // bf16: the weights are rounded to 8 bits for the product, as the output is; their sum has them unrounded
         if constexpr (kBf16) {
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) pf[kg][i / 2] = pack_bf16(x[kg][i], x[kg][i + 1]);
+                for (int i = 0; i < 16; i += 2) {
+                    pf[kg][i / 2] = pack_bf16(x[kg][i], x[kg][i + 1]);
+                    if (!ROWS) pr[kg][i / 2] = rest_of(x[kg][i], x[kg][i + 1], pf[kg][i / 2]);
+                }
         }
         // In a tile with hidden keys, values that are not finite count as 0: a hidden one's weight of 0 would make them
         // NaN.  The outputs that see them are noted below.
         uint32_t odd = 0;
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!ROWS) wait_loads_but<ALL_LOADS / 2>();
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
 #pragma unroll
@@ -472,6 +491,11 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
                         const u32x4 y = {pf[kg][4 * st], pf[kg][4 * st + 1], pf[kg][4 * st + 2], pf[kg][4 * st + 3]};
                         o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
                                                                        __builtin_bit_cast(bf16x8, y), o[c], 0, 0, 0);
+                        if constexpr (!ROWS) {
+                            const u32x4 z = {pr[kg][4 * st], pr[kg][4 * st + 1], pr[kg][4 * st + 2], pr[kg][4 * st + 3]};
+                            o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
+                                                                           __builtin_bit_cast(bf16x8, z), o[c], 0, 0, 0);
+                        }
                     }
                 } else {
 #pragma unroll
@@ -520,7 +544,85 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+        if constexpr (!ROWS) {
+            wait_loads_but<ALL_LOADS / 2>();
+            load_some(next, ALL_LOADS / 2, ALL_LOADS);
+        }
     };
+    // The same for few rows: keys and values wait for their own loads, and ask for the next ones behind their last use.
+    auto work_keys = [&](const char* kt, const Next& next) {
+        const char* vt = kt + S::TILE;
+        f32x16 x = zeros();
+        u32x4 ring[AHEAD];
+        wait_loads_but<ALL_LOADS / 2>();
+        auto key = [&](int s) {
+            return *reinterpret_cast<const u32x4*>(kt + (s / 4) * BN * 128 + k_lane[s & 3]);
+        };
+#pragma unroll
+        for (int s = 0; s < AHEAD && s < NK; ++s) ring[s] = key(s);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < NK; ++s) {
+            const u32x4 y = ring[s % AHEAD];
+            if constexpr (kBf16) {
+                x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, y),
+                                                            __builtin_bit_cast(bf16x8, q[s]), x, 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(y[i]), __uint_as_float(q[s][i]), x, 0, 0, 0);
+            }
+            if (s + AHEAD < NK) ring[s % AHEAD] = key(s + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        wait_loads_but<ALL_LOADS / 2>();  // (the keys have been read)
+        load_some(next, 0, ALL_LOADS / 2);
+        float e[16];
+        u32x4 high[2], rest[2];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            e[i] = exp2_hw(__builtin_fmaf(x[i], scale2, -ref));
+            sum[i & 3] += e[i];
+            if (kBf16 && (i & 1)) {
+                high[i / 8][i % 8 / 2] = pack_bf16(e[i - 1], e[i]);
+                rest[i / 8][i % 8 / 2] = rest_of(e[i - 1], e[i], high[i / 8][i % 8 / 2]);
+            }
+        }
+        wait_loads_but<ALL_LOADS / 2>();
+        auto val = [&](int j) {
+            u32x4 y;
+            if constexpr (kBf16) {
+                y = value(vt, j % CT, 0, j / CT);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = __float_as_uint(value32(vt, j % CT, 0, j / CT * 4 + i));
+            }
+            return y;
+        };
+#pragma unroll
+        for (int j = 0; j < AHEAD && j < NV; ++j) ring[j] = val(j);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const u32x4 y = ring[j % AHEAD];
+            const int c = j % CT, part = j / CT;
+            if constexpr (kBf16) {
+                o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, y),
+                                                               __builtin_bit_cast(bf16x8, high[part]), o[c], 0, 0, 0);
+                o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, y),
+                                                               __builtin_bit_cast(bf16x8, rest[part]), o[c], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[c] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(y[i]), e[4 * part + i], o[c], 0, 0, 0);
+            }
+            if (j + AHEAD < NV) ring[j % AHEAD] = val(j + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        wait_loads_but<ALL_LOADS / 2>();  // (the values have been read)
+        load_some(next, ALL_LOADS / 2, ALL_LOADS);
+    };
+
     // tiles that every row of the wave sees whole: from the last row's window on, up to the first row's position
     bool ready = false;  // all rows of the wave have a reference
     const int whole_lo = p_near_last > near ? p_near_last : near, whole_hi = pw_first + 1 < end ? pw_first + 1 : end;
@@ -529,10 +631,12 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
         const int t = t0 + w0 + STEP * i;
         return ready && absent_of(i) == 0 && t >= whole_t0 && t < whole_t1;
     };
-    auto begin = [&](int i) {  // tile i is there, and the other buffer has been read
+    auto begin = [&](int i) {
         if ((i + 1) % PER == 0) advance(i + 1);
-        wait_loads();
-        if constexpr (ROWS) __syncthreads();
+        if constexpr (ROWS) {  // tile i is there, and the other buffer has been read
+            wait_loads();
+            __syncthreads();
+        }
     };
 
     const int steps = t1 - t0 - w0 > 0 ? (t1 - t0 - w0 + STEP - 1) / STEP : 0;
@@ -541,20 +645,24 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
         ready = pass == 2;
         look_up(0);
         advance(0);
-        load_all(next_of(0));
+        load_some(next_of(0), 0, ALL_LOADS);
         // (two loops, since the compiler would copy the outputs for every tile where two paths of one loop change them)
         for (int i = 0; i < steps;) {
             for (; i < steps && !whole(i); ++i) {
                 const int t = t0 + w0 + STEP * i, base = base_of(t), gone = absent_of(i);
                 begin(i);
-                load_all(next_of(i + 1));
-                if (!active || base > pw_last) continue;
-                work_edge(s_kv[ROWS ? 0 : w][i & 1], base, t < head_tiles ? 0 : near, t < head_tiles ? head : end, gone);
+                if constexpr (ROWS) {
+                    load_some(next_of(i + 1), 0, ALL_LOADS);
+                    if (!active || base > pw_last) continue;
+                }
+                work_edge(s_kv[ROWS ? i & 1 : w], base, t < head_tiles ? 0 : near, t < head_tiles ? head : end, gone,
+                          next_of(i + 1));
                 ready = pass != 1 && !__any(m == -INFINITY);
             }
             for (; i < steps && whole(i); ++i) {
                 begin(i);
-                work(s_kv[ROWS ? 0 : w][i & 1], next_of(i + 1));
+                if constexpr (ROWS) work(s_kv[i & 1], next_of(i + 1));
+                else work_keys(s_kv[w], next_of(i + 1));
             }
         }
         wait_loads();
@@ -627,9 +735,9 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
                 else *reinterpret_cast<f32x4*>(at) = y;
             }
     } else {
-        // join the waves: their sums go where the tiles were, half of the channels into each buffer
-        constexpr int HALF = D / 2, PITCH = HALF + 4;
-        static_assert(32 * PITCH * 4 <= 2 * S::TILE, "half of a wave's outputs fits a buffer");
+        // join the waves: their sums go where the tiles were, four channels c of row r at place c / 4 ^ r % 8 of its row
+        static_assert(32 * D * 4 <= 2 * S::TILE, "a wave's outputs fit its buffer");
+        auto place = [&](int i, int r, int c) { return reinterpret_cast<f32x4*>(s_kv[i]) + r * (D / 4) + (c / 4 ^ (r & 7)); };
         if (hl == 0) {
             s_m[w][lr] = base;
             s_l[w][lr] = l;
@@ -644,11 +752,10 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
         const float M = joint(lr), keep = base == -INFINITY ? 0.f : exp2_hw(base - M);
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-            float* to = reinterpret_cast<float*>(s_kv[w][c / (CT / 2)]) + lr * PITCH + c % (CT / 2) * 32 + 4 * hl;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<f32x4*>(to + 8 * e) = f32x4{o[c][4 * e] * keep, o[c][4 * e + 1] * keep,
-                                                              o[c][4 * e + 2] * keep, o[c][4 * e + 3] * keep};
+                *place(w, lr, c * 32 + 8 * e + 4 * hl) =
+                    f32x4{o[c][4 * e] * keep, o[c][4 * e + 1] * keep, o[c][4 * e + 2] * keep, o[c][4 * e + 3] * keep};
         }
         __syncthreads();
         for (int x = tid; x < rows * (D / 4); x += S::THREADS) {
@@ -659,8 +766,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::G
 #pragma unroll
             for (int i = 0; i < WAVES; ++i) {
                 L += top == -INFINITY ? 0.f : s_l[i][r] * exp2_hw(s_m[i][r] - top);
-                const float* from = reinterpret_cast<const float*>(s_kv[i][c / HALF]) + r * PITCH + c % HALF;
-                y += *reinterpret_cast<const f32x4*>(from);
+                y += *place(i, r, c);
             }
             const int64_t row = token_of(r) * a.Hq + head_of(r);
             if (plan.parts > 1) {
