@@ -94,8 +94,8 @@ struct Shape {
     static constexpr int PER_SIMD = ROW <= (ROWS ? 512 : 256) ? 2 : 1;  // waves
 };
 
-// Row tiles of all sequences: tile k of sequence n has slot floor(cu[n] G / RT) + n + k, which leaves every sequence
-// enough slots.  The sequence of a slot (wave-uniform), by 64 probes at a time.
+// Row tiles of all sequences, not split: tile k of sequence n has slot floor(cu[n] G / RT) + n + k, which leaves every
+// sequence enough slots.  The sequence of a slot (wave-uniform), by 64 probes at a time.
 __device__ __forceinline__ int64_t slot_begin(const int32_t* cu, int64_t n, int G, int RT) {
     return (int64_t)cu[n] * G / RT + n;
 }
@@ -113,14 +113,175 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t N, int
     return lo;
 }
 
+// The host does not know the lengths, so the work is split on the device: with up to 64 sequences every workgroup looks at
+// all of them and comes to the same shares.  A sequence's row tiles are split into parts of at most P steps, P the total
+// over kGroups workgroups (a little more where that gives no more parts than those), and the parts are numbered.  With
+// more sequences the parts' length goes by the bound of the lengths.  16 sequences with 5 new tokens each, 32 heads over
+// 8, after 1000 to 16379 tokens: 84 us, 135 us with parts by the bound; kGroups of 384 and 1024: 89 and 92 us.  Parts of
+// 8 steps at least: one such sequence after 8000 tokens takes 24 us instead of 21.
+constexpr int kMaxParts = 64;
+constexpr int kGroups = 512, kLeast = 4;  // two workgroups per CU; steps of a part at least
+// The join costs 5 us, so nothing is split if the longest row tile may have fewer steps than this (many rows, 512 tokens:
+// 26 us, split 30; 173 after 3000, 50 steps: 34 us, with longer parts 38), nor if there are more row tiles than this (many
+// rows, 8 sequences of 48 to 2048 new tokens: 129 us, 132 with parts; few rows, lengths differ more).
+constexpr int kSplitSteps[2] = {2 * kLeast, 4 * kLeast};  // few rows, many rows
+constexpr int64_t kSplitTiles[2] = {2048, 256};
 struct PrefillPlan {
-    int64_t slots;
-    int parts, part_tiles;
+    int64_t slots;  // row tiles of a key-value head at most
+    int groups;     // workgroups of a head that the chip holds; 0: nothing is split
+    int parts, steps;  // parts of a row tile and their steps by the bound; 0: by the lengths
 };
+// A workgroup's share.
+struct Item {
+    int64_t n, tile;         // the row tile, of sequence n (-1: none)
+    int part, parts, steps;  // steps of a part
+    int64_t split;           // the row tile's first among the split parts
+};
+
+// What the workspace holds: of every row tile its parts and its first split part; of the split parts of every head
+// (reference, sum) of the rows, then their outputs [RT, D].
+struct Partials {
+    int2* tiles;
+    float2* ml;
+    float* out;
+};
+__host__ __device__ __forceinline__ int64_t places_of(int groups) { return 2 * (int64_t)groups; }
+
+// Steps of a row tile that ends at `length`, at most.
+__host__ __device__ __forceinline__ int steps_to(const PagedPrefillArgs& a, int64_t length, int RT, int BN, int STEP) {
+    const int64_t end = length < 0 ? 0 : length < a.max_length ? length : a.max_length;
+    int64_t tiles = (end + BN - 1) / BN;
+    if (a.window > 0) {
+        const int64_t most = ((int64_t)a.sinks + BN - 1) / BN + ((int64_t)a.window + RT + BN - 1) / BN + 1;
+        tiles = tiles + 1 < most ? tiles + 1 : most;
+    }
+    const int64_t s = (tiles + STEP - 1) / STEP;
+    return (int)(s < 1 ? 1 : s);
+}
+
+template <int RT, int BN, int STEP>
+__device__ __forceinline__ Item item_of(const PagedPrefillArgs& a, const PrefillPlan& plan, int64_t j) {
+    const int G = a.Hq / a.Hkv;
+    Item x{-1, 0, 0, 1, 0x7FFFFFFF, 0};
+    if (plan.groups == 0 || plan.parts > 0) {
+        if (plan.parts > 0) {
+            x.parts = plan.parts;
+            x.steps = plan.steps;
+            x.part = (int)(j / plan.slots);
+            j %= plan.slots;
+            x.split = j * plan.parts;
+        }
+        j = plan.slots - 1 - j;  // late tiles first: they have the most keys
+        x.n = sequence_of(a.cu, a.N, j, G, RT);
+        x.tile = j - slot_begin(a.cu, x.n, G, RT);
+        return x;
+    }
+    // a sequence in each lane
+    const int lane = threadIdx.x & 63;
+    int tiles = 0, steps = 1;
+    float work = 0.f;  // twice the steps of all
+    if (lane < a.N) {
+        const int64_t c0 = a.cu[lane] < 0 ? 0 : a.cu[lane], c1 = a.cu[lane + 1] < a.T ? a.cu[lane + 1] : a.T;
+        const int64_t fresh = c1 > c0 ? c1 - c0 : 0, length = a.lengths[lane];
+        tiles = (int)((fresh * G + RT - 1) / RT);
+        steps = steps_to(a, length, RT, BN, STEP);
+        work = (float)tiles * (float)(steps + steps_to(a, length - fresh + RT, RT, BN, STEP));
+    }
+    float total = work;
+    int all = tiles;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        total += __shfl_xor(total, off, 64);
+        all += __shfl_xor(all, off, 64);
+    }
+    all = __builtin_amdgcn_readfirstlane(all);
+    // The shares to choose from, one in each lane: P, 1.09 P and so on.  Those from 2 P on split into few enough parts,
+    // since a split row tile's parts are at most twice its steps / P.
+    const float share = ceilf(total * 1.0001f / (2 * plan.groups));
+    const float P = ceilf(fmaxf(fminf(share, 1e7f), (float)kLeast) * exp2_hw(0.125f * lane)), per = 1.f / P;
+    auto parts_of = [&](float steps, float P, float per) { return fminf(floorf((steps + P - 1.f) * per), (float)kMaxParts); };
+    float parts = 0.f, split = 0.f;
+    for (int n = 0; n < a.N; ++n) {
+        const float t = (float)__builtin_amdgcn_readlane(tiles, n), s = (float)__builtin_amdgcn_readlane(steps, n);
+        const float y = t * fmaxf(parts_of(s, P, per), 1.f);
+        parts += y;
+        split += y > t ? y : 0.f;
+    }
+    // (few row tiles: no more parts than groups, if a share below 2 P gives that)
+    uint64_t good = __ballot(2 * all > plan.groups || parts <= (float)plan.groups) & 0xFF;
+    const uint64_t fits = __ballot(split <= (float)places_of(plan.groups));
+    if ((good & fits) == 0) good = ~0ull;
+    const int at_lane = __builtin_ctzll(good & fits);
+    const float chosen = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(P), at_lane));
+    const float chosen_per = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(per), at_lane));
+    // the item among the parts of all
+    const int k = (int)fmaxf(parts_of((float)steps, chosen, chosen_per), 1.f), mine = tiles * k, mine_split = k > 1 ? mine : 0;
+    int sum = mine, sum_split = mine_split;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int y = __shfl_up(sum, off, 64), z = __shfl_up(sum_split, off, 64);
+        if (lane >= off) sum += y, sum_split += z;
+    }
+    const int items = __builtin_amdgcn_readlane(sum, 63);
+    if (j >= items) return x;
+    const int at = items - 1 - (int)j;  // late tiles first
+    const int in = __builtin_ctzll(__ballot(sum > at));
+    const int inside = at - __builtin_amdgcn_readlane(sum - mine, in);
+    x.n = in;
+    x.parts = __builtin_amdgcn_readlane(k, in);
+    x.tile = inside / x.parts;
+    x.part = inside - (int)x.tile * x.parts;
+    x.steps = (__builtin_amdgcn_readlane(steps, in) + x.parts - 1) / x.parts;
+    x.split = x.parts > 1 ? __builtin_amdgcn_readlane(sum_split - mine_split, in) + x.tile * x.parts : 0;
+    return x;
+}
+
+// A row tile and what its rows see.
+struct RowTile {
+    int64_t cu0, i0;  // the sequence's first packed token, the tile's first token in it
+    int g0, rows;     // the first row's head in the group, rows
+    int64_t shift;    // position of the sequence's first new token
+    int near, end, head, head_tiles, first, tiles;  // visible: 0 .. head-1 and near .. end-1
+    // (64 bits: a contract that is broken gives any)
+    __device__ __forceinline__ int position(int r, int G) const {
+        const int64_t p = shift + i0 + (g0 + r) / G;
+        return (int)(p < -1 ? -1 : p);
+    }
+};
+template <int RT, int BN>
+__device__ __forceinline__ bool row_tile_of(const PagedPrefillArgs& a, const Item& x, RowTile& t) {
+    if (x.n < 0 || x.tile < 0) return false;
+    const int G = a.Hq / a.Hkv;
+    t.cu0 = a.cu[x.n] < 0 ? 0 : a.cu[x.n];
+    const int64_t cu1 = a.cu[x.n + 1] < a.T ? a.cu[x.n + 1] : a.T, fresh = cu1 - t.cu0, row0 = x.tile * RT;
+    if (row0 >= fresh * G) return false;
+    t.rows = (int)(fresh * G - row0 < RT ? fresh * G - row0 : RT);
+    t.i0 = row0 / G;
+    t.g0 = (int)(row0 - t.i0 * G);
+    const int length = a.lengths[x.n] > 0 ? a.lengths[x.n] : 0;
+    const int cap = length < a.max_length ? length : (int)a.max_length;
+    t.shift = length - fresh;
+    const int p_first = t.position(0, G), p_last = t.position(t.rows - 1, G);
+    t.end = p_last + 1 < cap ? p_last + 1 : cap;
+    const int near = a.window > 0 && p_first >= a.window ? p_first - a.window + 1 : 0;
+    t.near = near < t.end ? near : t.end;
+    t.head = a.sinks < t.near ? a.sinks : t.near;
+    t.head_tiles = (t.head + BN - 1) / BN;
+    t.first = t.near / BN;
+    t.tiles = t.head_tiles + (t.end + BN - 1) / BN - t.first;
+    return true;
+}
+// Parts that a row tile has in fact (the steps that decide on them are an upper bound).
+__device__ __forceinline__ int parts_in_fact(const Item& x, const RowTile& t, int STEP) {
+    if (x.parts == 1) return 1;
+    const int per = x.steps * STEP, y = (t.tiles + per - 1) / per;
+    return y < 1 ? 1 : y;
+}
+
 
 template <typename T, int D, bool ROWS>
 __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::PER_SIMD)) void paged_prefill_kernel(
-    PagedPrefillArgs a, PrefillPlan plan, float2* part_ml, float* part_o) {
+    PagedPrefillArgs a, PrefillPlan plan, Partials ws) {
     using S = Shape<T, D, ROWS>;
     constexpr bool kBf16 = std::is_same<T, uint16_t>::value;
     constexpr int ES = S::ES, ROW = S::ROW, BN = S::BN, WAVES = S::WAVES, RT = S::RT, KG = BN / 32, CT = D / 32;
@@ -133,35 +294,23 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.Hq / a.Hkv;
     // heads fastest: workgroups of one head go to the same XCDs where the heads divide the eight, whose L2 then
-    // holds that head's keys; late tiles first: they have the most keys
-    int64_t b = blockIdx.x;
-    const int h = (int)(b % a.Hkv);
-    b /= a.Hkv;
-    const int64_t slot = plan.slots - 1 - b % plan.slots;
-    const int part = (int)(b / plan.slots);
-    const int64_t n = sequence_of(a.cu, a.N, slot, G, RT);
-    const int64_t cu0 = a.cu[n] < 0 ? 0 : a.cu[n], cu1 = a.cu[n + 1] < a.T ? a.cu[n + 1] : a.T;
-    const int64_t fresh = cu1 - cu0, row0 = (slot - slot_begin(a.cu, n, G, RT)) * RT;
-    if (row0 < 0 || row0 >= fresh * G) return;
-    const int rows = (int)(fresh * G - row0 < RT ? fresh * G - row0 : RT);
-    const int64_t i0 = row0 / G;
-    const int g0 = (int)(row0 - i0 * G);
-    const int length = a.lengths[n] > 0 ? a.lengths[n] : 0;
-    const int cap = length < a.max_length ? length : (int)a.max_length;
-    // positions (64 bits: a contract that is broken gives any)
-    auto position = [&](int r) {
-        const int64_t p = (int64_t)length - fresh + i0 + (g0 + r) / G;
-        return (int)(p < -1 ? -1 : p);
-    };
-    const int p_first = position(0), p_last = position(rows - 1);
-    const int end = p_last + 1 < cap ? p_last + 1 : cap;
-    // visible to some row: 0 .. head-1 and near .. end-1
-    int near = a.window > 0 && p_first >= a.window ? p_first - a.window + 1 : 0;
-    near = near < end ? near : end;
-    const int head = a.sinks < near ? a.sinks : near;
-    const int head_tiles = (head + BN - 1) / BN, first = near / BN;
-    const int tiles = head_tiles + (end + BN - 1) / BN - first;
-    const int t0 = part * plan.part_tiles, t1 = t0 + plan.part_tiles < tiles ? t0 + plan.part_tiles : tiles;
+    // holds that head's keys
+    const int h = (int)(blockIdx.x % a.Hkv);
+    const Item item = item_of<RT, BN, ROWS ? 1 : WAVES>(a, plan, blockIdx.x / a.Hkv);
+    RowTile tile;
+    if (!row_tile_of<RT, BN>(a, item, tile)) return;
+    const int parts = parts_in_fact(item, tile, ROWS ? 1 : WAVES);
+    if (item.part >= parts || (parts > 1 && item.split + item.part >= places_of(plan.groups))) return;
+    if (plan.groups && item.part == 0 && h == 0 && tid == 0) {
+        const int64_t slot = slot_begin(a.cu, item.n, G, RT) + item.tile;
+        if (slot >= 0 && slot < plan.slots) ws.tiles[slot] = make_int2(parts, (int)item.split);
+    }
+    const int64_t cu0 = tile.cu0, i0 = tile.i0;
+    const int g0 = tile.g0, rows = tile.rows, near = tile.near, end = tile.end, head = tile.head;
+    const int head_tiles = tile.head_tiles, first = tile.first, tiles = tile.tiles;
+    const int part_tiles = parts > 1 ? item.steps * (ROWS ? 1 : WAVES) : tiles;
+    const int t0 = item.part * part_tiles, t1 = t0 + part_tiles < tiles ? t0 + part_tiles : tiles;
+    auto position = [&](int r) { return tile.position(r, G); };
 
     // this lane's row, and its row of q and out (formed again behind the loop, where registers are free)
     const int my = ROWS ? w * 32 + lr : lr;
@@ -210,7 +359,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
         if (t < t1) {
             const uint32_t pos = base_of(t) + lane % SUBS * kPage, col = pos / (uint32_t)a.page_size;
             next_slot = (int)(pos - col * (uint32_t)a.page_size);
-            if (col < (uint32_t)a.pt.width) next_page = a.pt.table[n * a.pt.stride + col];
+            if (col < (uint32_t)a.pt.width) next_page = a.pt.table[item.n * a.pt.stride + col];
         }
     };
     auto advance = [&](int i) {
@@ -693,7 +842,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
         for (int i = 0; i < 16; ++i) o[c][i] = (spoiled[c / 2] >> (c % 2 * 16 + i)) & 1 ? NAN : o[c][i];
     // Sums that are joined with others are brought near 1 first, by a power of two.
     float base = m == -INFINITY ? -INFINITY : ref;
-    if (!ROWS || plan.parts > 1) {
+    if (!ROWS || parts > 1) {
         const int e = l > 0.f && l < INFINITY ? __builtin_amdgcn_frexp_expf(l) : 0;
         l = __builtin_amdgcn_ldexpf(l, -e);
 #pragma unroll
@@ -710,10 +859,10 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
     };
     if constexpr (ROWS) {
         if (!mine) return;
-        if (plan.parts > 1) {
-            if (hl == 0) part_ml[out_row * plan.parts + part] = make_float2(base, l);
-            if (l == 0.f) return;
-            float* to = part_o + (out_row * plan.parts + part) * D;
+        if (parts > 1) {
+            const int64_t at = (h * places_of(plan.groups) + item.split + item.part) * RT + my;
+            if (hl == 0) ws.ml[at] = make_float2(base, l);
+            float* to = ws.out + at * D;
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -768,12 +917,13 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
                 L += top == -INFINITY ? 0.f : s_l[i][r] * exp2_hw(s_m[i][r] - top);
                 y += *place(i, r, c);
             }
-            const int64_t row = token_of(r) * a.Hq + head_of(r);
-            if (plan.parts > 1) {
-                if (c == 0) part_ml[row * plan.parts + part] = make_float2(top, L);
-                *reinterpret_cast<f32x4*>(part_o + (row * plan.parts + part) * D + c) = y;
+            if (parts > 1) {
+                const int64_t at = (h * places_of(plan.groups) + item.split + item.part) * RT + r;
+                if (c == 0) ws.ml[at] = make_float2(top, L);
+                *reinterpret_cast<f32x4*>(ws.out + at * D + c) = y;
                 continue;
             }
+            const int64_t row = token_of(r) * a.Hq + head_of(r);
             if (c == 0) finish(top, L, row);
             const float f = L == 0.f ? 0.f : 1.f / L;
             T* at = static_cast<T*>(a.o) + row * D + c;
@@ -784,105 +934,119 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
     }
 }
 
-// Join of the parts: a wave for a row, its lanes over the channels.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void prefill_join_kernel(PagedPrefillArgs a, PrefillPlan plan, const float2* part_ml,
-                                                           const float* part_o) {
-    constexpr int CH = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t token = row / a.Hq;
-    // rows of no sequence have no parts and keep what they hold
-    if (token >= a.T || token < a.cu[0] || token >= a.cu[a.N]) return;
-    const float2 y = lane < plan.parts ? part_ml[row * plan.parts + lane] : make_float2(-INFINITY, 0.f);
-    float M = y.x;
+// Join of the parts of the row tiles that are split: 4 channels of a row for each thread.
+template <typename T, int D, bool ROWS>
+__global__ __launch_bounds__(256) void prefill_join_kernel(PagedPrefillArgs a, PrefillPlan plan, Partials ws) {
+    using S = Shape<T, D, ROWS>;
+    constexpr int RT = S::RT, AHEAD = 8, COLS = D / 4, RG = 256 / COLS;  // rows of a workgroup
+    __shared__ float2 s_ml[kMaxParts][RG];
+    const int tid = threadIdx.x, G = a.Hq / a.Hkv, h = (int)(blockIdx.x % a.Hkv);
+    const int64_t b = blockIdx.x / a.Hkv, slot = b / (RT / RG);
+    const int2 info = ws.tiles[slot];
+    Item item{};
+    item.n = sequence_of(a.cu, a.N, slot, G, RT);
+    item.tile = slot - slot_begin(a.cu, item.n, G, RT);
+    RowTile tile;
+    if (!row_tile_of<RT, S::BN>(a, item, tile)) return;
+    const int parts = info.x, r0 = (int)(b % (RT / RG)) * RG, r = tid / COLS, c = tid % COLS * 4;
+    if (parts < 2 || parts > kMaxParts || info.y < 0 || info.y + parts > places_of(plan.groups) || r0 >= tile.rows) return;
+    const int64_t at = (h * places_of(plan.groups) + info.y) * RT + r0;
+    // (rows behind the tile's last have places too)
+    const float* from = ws.out + (at + r) * D + c;
+    f32x4 z[AHEAD];
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-    // (a NaN sum stays: its part takes part)
-    const float f = y.y == 0.f ? 0.f : exp2_hw(y.x - M);
-    float L = y.y * f;
+    for (int i = 0; i < AHEAD; ++i) z[i] = *reinterpret_cast<const f32x4*>(from + (int64_t)(i < parts ? i : 0) * RT * D);
+    for (int x = tid; x < parts * RG; x += 256) s_ml[x / RG][x % RG] = ws.ml[at + x / RG * RT + x % RG];
+    __syncthreads();
+    float M = -INFINITY, L = 0.f;
+    for (int i = 0; i < parts; ++i) M = fmaxf(M, s_ml[i][r].x);
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < parts; i0 += AHEAD) {
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) L += __shfl_xor(L, off, 64);
-    float acc[CH];
+        for (int i = 0; i < AHEAD; ++i) {
+            if (i0 + i >= parts) break;
+            const float2 x = s_ml[i0 + i][r];
+            const float f = x.x == -INFINITY ? 0.f : exp2_hw(x.x - M);
+            L += x.y * f;
+            y += z[i] * f;
+        }
 #pragma unroll
-    for (int c = 0; c < CH; ++c) acc[c] = 0.f;
-    const float* po = part_o + row * plan.parts * D + lane * CH;
-    for (int i = 0; i < plan.parts; ++i) {
-        const float part = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(y.y), i));
-        const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-        if (part == 0.f) continue;  // its outputs have not been written
-#pragma unroll
-        for (int c = 0; c < CH; ++c) acc[c] += g * po[(int64_t)i * D + c];
+        for (int i = 0; i < AHEAD; ++i)
+            if (i0 + AHEAD + i < parts) z[i] = *reinterpret_cast<const f32x4*>(from + (int64_t)(i0 + AHEAD + i) * RT * D);
     }
-    const float r = L == 0.f ? 0.f : 1.f / L;
-    T* to = static_cast<T*>(a.o) + row * D + lane * CH;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) to[c] = acc[c] * r;
-    } else if constexpr (CH == 1) {
-        to[0] = (uint16_t)pack_bf16(acc[0] * r, 0.f);
-    } else {
-#pragma unroll
-        for (int c = 0; c < CH; c += 2) *reinterpret_cast<uint32_t*>(to + c) = pack_bf16(acc[c] * r, acc[c + 1] * r);
-    }
-    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+    if (r0 + r >= tile.rows) return;
+    const float f = L == 0.f ? 0.f : 1.f / L;
+    const int64_t row = (tile.cu0 + tile.i0 + (tile.g0 + r0 + r) / G) * a.Hq + h * G + (tile.g0 + r0 + r) % G;
+    T* to = static_cast<T*>(a.o) + row * D + c;
+    if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(y[0] * f, y[1] * f), pack_bf16(y[2] * f, y[3] * f)};
+    else *reinterpret_cast<f32x4*>(to) = y * f;
+    if (c == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
 int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
-constexpr int kMaxParts = 64;
-
 // Few rows for each sequence: the waves share the rows and split the keys.
-bool many_rows(int64_t N, int64_t T, int G) { return T * G > 32 * N; }
+bool many_rows(const PagedPrefillArgs& a) { return a.T * (a.Hq / a.Hkv) > 32 * a.N; }
 
-PrefillPlan plan_of(int64_t N, int64_t T, int Hq, int Hkv, int d, int es, int64_t max_length, int window, int sinks) {
-    const int G = Hq / Hkv, row = d * es;
-    const bool rows = many_rows(N, T, G);
-    const int rt = rows ? 128 : 32, bn = rows && row <= 256 && es == 2 ? 64 : 32;
-    const int waves = rows ? 1 : row <= 256 ? 4 : row == 512 ? 2 : 1;
-    PrefillPlan p;
-    p.slots = T * G / rt + N;
-    int64_t tiles = div_up(max_length, bn);
-    if (window > 0 && max_length > window) {
-        const int64_t most = div_up(sinks, bn) + div_up((int64_t)window + div_up(rt, G) + 1, bn) + 1;
-        tiles = most < tiles + 1 ? most : tiles + 1;
+// A variant's sizes, as in Shape.
+struct Sizes {
+    int rt, bn, step;
+    bool rows;
+};
+Sizes sizes_of(const PagedPrefillArgs& a) {
+    const int row = a.d * (a.bf16 ? 2 : 4);
+    if (many_rows(a)) return {128, row <= 256 && a.bf16 ? 64 : 32, 1, true};
+    return {32, 32, row <= 256 ? 4 : row == 512 ? 2 : 1, false};
+}
+
+PrefillPlan plan_of(const PagedPrefillArgs& a) {
+    PrefillPlan p{};
+    const Sizes z = sizes_of(a);
+    p.slots = a.T * (a.Hq / a.Hkv) / z.rt + a.N;
+    const int64_t steps = steps_to(a, a.max_length, z.rt, z.bn, z.step);
+    if (steps < kSplitSteps[z.rows] || p.slots * a.Hkv > kSplitTiles[z.rows]) return p;
+    p.groups = (int)div_up(kGroups, a.Hkv);
+    if (a.N > 64) {
+        int64_t parts = p.groups / p.slots;
+        parts = parts < steps / kLeast ? parts : steps / kLeast;
+        p.parts = (int)(parts < kMaxParts ? parts : kMaxParts);
+        if (p.parts < 2) p.parts = p.groups = 0;
+        else p.steps = (int)div_up(steps, p.parts);
     }
-    // parts for two workgroups per CU, of at least four steps each
-    const int64_t base = p.slots * Hkv, steps = div_up(tiles, waves);
-    int64_t parts = base > 0 ? 512 / base : 1;
-    parts = parts < steps / 4 ? parts : steps / 4;
-    parts = parts < 1 ? 1 : parts > kMaxParts ? kMaxParts : parts;
-    p.part_tiles = (int)(div_up(steps > 0 ? steps : 1, parts) * waves);
-    p.parts = (int)(tiles > 0 ? div_up(tiles, p.part_tiles) : 1);
     return p;
 }
-PrefillPlan plan_of(const PagedPrefillArgs& a) {
-    return plan_of(a.N, a.T, a.Hq, a.Hkv, a.d, a.bf16 ? 2 : 4, a.max_length, a.window, a.sinks);
+int64_t items_of(const PrefillPlan& p) {
+    return p.parts ? p.slots * p.parts : p.slots + (p.groups ? places_of(p.groups) : 0);
 }
 
+int64_t part_rows(const PagedPrefillArgs& a, const PrefillPlan& p) { return a.Hkv * places_of(p.groups) * sizes_of(a).rt; }
+size_t tile_bytes(const PrefillPlan& p) { return (size_t)(div_up(p.slots * 8, 256) * 256); }
+
+template <typename T, int D, bool ROWS>
+hipError_t launch_shape(const PagedPrefillArgs& a, const PrefillPlan& p, const Partials& y, hipStream_t s) {
+    using S = Shape<T, D, ROWS>;
+    const bool timed = timing_on();
+    if (timed) timed_begin(kKernelPagedPrefill, s);
+    hipLaunchKernelGGL((paged_prefill_kernel<T, D, ROWS>), dim3((unsigned)(items_of(p) * a.Hkv)), dim3(S::THREADS), 0, s, a, p, y);
+    hipError_t e = hipGetLastError();
+    if (timed) timed_end(s);
+    if (e != hipSuccess || !p.groups) return e;
+    const unsigned join = (unsigned)(p.slots * a.Hkv * (S::RT * D / 1024));
+    if (timed) timed_begin(kKernelPrefillJoin, s);
+    hipLaunchKernelGGL((prefill_join_kernel<T, D, ROWS>), dim3(join), dim3(256), 0, s, a, p, y);
+    e = hipGetLastError();
+    if (timed) timed_end(s);
+    return e;
+}
 template <typename T, int D>
-void launch_typed(const PagedPrefillArgs& a, const PrefillPlan& p, float2* ml, float* po, hipStream_t s) {
-    const dim3 grid((unsigned)(p.slots * a.Hkv * p.parts));
-    if (many_rows(a.N, a.T, a.Hq / a.Hkv))
-        hipLaunchKernelGGL((paged_prefill_kernel<T, D, true>), grid, dim3(Shape<T, D, true>::THREADS), 0, s, a, p, ml, po);
-    else
-        hipLaunchKernelGGL((paged_prefill_kernel<T, D, false>), grid, dim3(Shape<T, D, false>::THREADS), 0, s, a, p, ml, po);
+hipError_t launch_typed(const PagedPrefillArgs& a, const PrefillPlan& p, const Partials& y, hipStream_t s) {
+    return many_rows(a) ? launch_shape<T, D, true>(a, p, y, s) : launch_shape<T, D, false>(a, p, y, s);
 }
 template <typename T>
-void launch_typed(const PagedPrefillArgs& a, const PrefillPlan& p, float2* ml, float* po, hipStream_t s) {
-    if (a.d == 64) launch_typed<T, 64>(a, p, ml, po, s);
-    else if (a.d == 128) launch_typed<T, 128>(a, p, ml, po, s);
-    else launch_typed<T, 256>(a, p, ml, po, s);
+hipError_t launch_typed(const PagedPrefillArgs& a, const PrefillPlan& p, const Partials& y, hipStream_t s) {
+    return a.d == 64 ? launch_typed<T, 64>(a, p, y, s) : a.d == 128 ? launch_typed<T, 128>(a, p, y, s) : launch_typed<T, 256>(a, p, y, s);
 }
-template <typename T>
-void launch_join(const PagedPrefillArgs& a, const PrefillPlan& p, const float2* ml, const float* po, hipStream_t s) {
-    const dim3 grid((unsigned)div_up(a.T * a.Hq, 4)), block(256);
-    if (a.d == 64) hipLaunchKernelGGL((prefill_join_kernel<T, 64>), grid, block, 0, s, a, p, ml, po);
-    else if (a.d == 128) hipLaunchKernelGGL((prefill_join_kernel<T, 128>), grid, block, 0, s, a, p, ml, po);
-    else hipLaunchKernelGGL((prefill_join_kernel<T, 256>), grid, block, 0, s, a, p, ml, po);
-}
-
-int64_t ml_bytes(const PagedPrefillArgs& a, const PrefillPlan& p) { return div_up(a.T * a.Hq * p.parts * 8, 256) * 256; }
 
 }  // namespace
 
@@ -891,29 +1055,20 @@ int64_t paged_prefill_groups(const PagedPrefillArgs& a, size_t* workspace) {
     const int64_t slots = a.T * (a.Hq / a.Hkv) / 32 + a.N;  // at most
     if (slots * a.Hkv > max_groups(256)) return slots * a.Hkv;
     const PrefillPlan p = plan_of(a);
-    const int64_t groups = p.slots * a.Hkv * p.parts;
-    if (p.parts > 1) *workspace = (size_t)(ml_bytes(a, p) + a.T * a.Hq * p.parts * (int64_t)a.d * 4);
-    return groups;
+    if (p.groups && a.T > 0 && a.N > 0) *workspace = tile_bytes(p) + (size_t)(part_rows(a, p) * (8 + (int64_t)a.d * 4));
+    return items_of(p) * a.Hkv;
 }
 
 hipError_t launch_paged_prefill(const PagedPrefillArgs& a, hipStream_t s) {
     if (a.T == 0 || a.N == 0) return hipSuccess;
     const PrefillPlan p = plan_of(a);
-    float2* ml = static_cast<float2*>(a.ws);
-    float* po = p.parts > 1 ? reinterpret_cast<float*>(static_cast<char*>(a.ws) + ml_bytes(a, p)) : nullptr;
-    const bool timed = timing_on();
-    if (timed) timed_begin(kKernelPagedPrefill, s);
-    if (a.bf16) launch_typed<uint16_t>(a, p, ml, po, s);
-    else launch_typed<float>(a, p, ml, po, s);
-    hipError_t e = hipGetLastError();
-    if (timed) timed_end(s);
-    if (e != hipSuccess || p.parts == 1) return e;
-    if (timed) timed_begin(kKernelPrefillJoin, s);
-    if (a.bf16) launch_join<uint16_t>(a, p, ml, po, s);
-    else launch_join<float>(a, p, ml, po, s);
-    e = hipGetLastError();
-    if (timed) timed_end(s);
-    return e;
+    Partials y{};
+    if (p.groups) {
+        y.tiles = static_cast<int2*>(a.ws);
+        y.ml = reinterpret_cast<float2*>(static_cast<char*>(a.ws) + tile_bytes(p));
+        y.out = reinterpret_cast<float*>(y.ml + part_rows(a, p));
+    }
+    return a.bf16 ? launch_typed<uint16_t>(a, p, y, s) : launch_typed<float>(a, p, y, s);
 }
 
 }  // namespace kda
