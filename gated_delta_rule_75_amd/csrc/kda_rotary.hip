@@ -6,13 +6,18 @@
 // with x, y the channels i, i + r / 2 (halves) or 2 i, 2 i + 1 (interleaved); channels from r on are copied.
 //
 // Pure traffic: every value is read once and written once.  The angles must not add to it.
-//  * A workgroup takes up to 16 tokens.  It forms the cosines and sines of each pair once, in LDS, for all heads
-//    of its tokens; p f is an fp64 product and is reduced by multiples of 2 pi there (a position of 2^17 in
-//    fp32 would be off by 2^-7 rad), the rest is fp32.
-//  * The first values are asked for before the angles are formed, so that these hide behind the loads.
+//  * A workgroup takes one token, or as many of few heads as its threads have two steps for.  It forms the cosines
+//    and sines of each pair once, in LDS, for all heads of its tokens; p f is an fp64 product and is reduced by
+//    multiples of 2 pi there (a position of 2^17 in fp32 would be off by 2^-7 rad), the rest is fp32.
+//  * The first values are asked for before the angles are formed, so that these hide behind the loads.  Many small
+//    workgroups keep the chip's loads and stores apart in time better than few large ones, and neither is kept in the
+//    caches (non-temporal).  65536 tokens of 32 + 32 heads of 128, bf16: 361 us, 5.9 TB/s (16 tokens a workgroup: 438, 8:
+//    417, 4: 402, without the hint for stores 382; a copy of that size: 420).  Into pages, 16384 tokens of segments: 199
+//    us, 6.0 TB/s, where the hint for stores saves 24 us and the attention behind it takes as long as before.
 //  * A thread always has the same place in a row.  Halves that start at 16-byte boundaries: a vector of the first
 //    half and its partner.  Interleaved: pairs lie inside one vector.  Halves that do not (r / 2 no multiple of a
-//    vector): the rows of a step are laid into LDS, from where each thread takes its partners.
+//    vector): the rows of a step are laid into LDS, from where each thread takes its partners (5.9 TB/s too).
+// One query head and one key head of 64 share their angles with no other: 3.3 TB/s, bound by the angles.
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -118,8 +123,8 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryPl
             const int64_t stride = is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride;
             const int h = is_q ? row[i] : is_k ? row[i] - a.Hq : row[i] - a.Hq - a.Hk;
             const T* p = base + (t0 + tok[i]) * stride + (int64_t)h * a.d;
-            raw[i][0] = *reinterpret_cast<const u32x4*>(p + c0);
-            if constexpr (NV == 2) raw[i][1] = *reinterpret_cast<const u32x4*>(p + c1);
+            raw[i][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + c0));
+            if constexpr (NV == 2) raw[i][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + c1));
         }
     };
     fetch(0);
@@ -225,42 +230,51 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryPl
             } else {
                 to = static_cast<T*>(a.k_out) + (t0 + j) * a.k_out_stride + (int64_t)(row[i] - a.Hq) * a.d;
             }
-            *reinterpret_cast<u32x4*>(to + c0) = got[0];
-            if constexpr (NV == 2) *reinterpret_cast<u32x4*>(to + c1) = got[1];
+            __builtin_nontemporal_store(got[0], reinterpret_cast<u32x4*>(to + c0));
+            if constexpr (NV == 2) __builtin_nontemporal_store(got[1], reinterpret_cast<u32x4*>(to + c1));
         }
     }
 }
 
-// Tokens of a workgroup: 16 where that still gives eight workgroups per CU, as many as have their angles in LDS,
-// and few enough for the division by the rows (16 up to 2^14 rows).
-int tokens_of(int64_t T, int r, int64_t rows) {
-    int64_t t = T / 2048;
+int rows_of(const RotaryArgs& a) { return a.Hq + a.Hk * (a.kp ? 2 : 1); }
+// Halves whose vectors start at 16-byte boundaries: a thread has a vector of each.
+bool whole_halves(const RotaryArgs& a) {
+    const int W = a.bf16 ? 8 : 4;
+    return !a.interleaved && a.r / 2 % W == 0 && a.d % (2 * W) == 0;
+}
+int units_of(const RotaryArgs& a) { return a.d / ((a.bf16 ? 8 : 4) * (whole_halves(a) ? 2 : 1)); }
+// Tokens of a workgroup: as many as its threads have two steps for (7 + 1 heads of 64, bf16: 50 us against 61 with one
+// step, 47 with four, which cost 40 heads of 128 a tenth), and whose angles have a place in LDS.  Where that gives more
+// workgroups than a launch has, more of them, while the division by the rows is exact.
+int tokens_of(const RotaryArgs& a) {
+    const int64_t units = units_of(a), rows = rows_of(a), pairs = a.r / 2;
+    int64_t t = 2 * kThreads / (units * rows);
     t = t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
-    while (t > 1 && (t * (r / 2) > kTurns || t * rows * rows >= ((int64_t)1 << 32))) t /= 2;
+    t = t * pairs > kTurns ? kTurns / pairs : t;
+    while ((a.T + t - 1) / t > max_groups(kThreads) && 2 * t <= kMaxTokens && 2 * t * pairs <= kTurns &&
+           2 * t * rows * rows < ((int64_t)1 << 32))
+        t *= 2;
     return (int)t;
 }
-int rows_of(const RotaryArgs& a) { return a.Hq + a.Hk * (a.kp ? 2 : 1); }
 
 template <typename T, bool PLACE>
 void launch_typed(const RotaryArgs& a, hipStream_t s) {
-    constexpr int W = 16 / sizeof(T);
     RotaryPlan p;
     p.rows = rows_of(a);
-    p.tokens = tokens_of(a.T, a.r, p.rows);
-    const bool halves = !a.interleaved && a.r / 2 % W == 0 && a.d % (2 * W) == 0;
-    p.units = halves ? a.d / (2 * W) : a.d / W;
+    p.tokens = tokens_of(a);
+    p.units = units_of(a);
     p.rows_magic = (uint32_t)(0xFFFFFFFFu / (uint32_t)p.rows + 1u);
     p.units_magic = (uint32_t)(0xFFFFFFFFu / (uint32_t)p.units + 1u);
     const dim3 grid((unsigned)((a.T + p.tokens - 1) / p.tokens)), block(kThreads);
     if (a.interleaved) hipLaunchKernelGGL((rotary_kernel<T, kInterleaved, PLACE>), grid, block, 0, s, a, p);
-    else if (halves) hipLaunchKernelGGL((rotary_kernel<T, kHalves, PLACE>), grid, block, 0, s, a, p);
+    else if (whole_halves(a)) hipLaunchKernelGGL((rotary_kernel<T, kHalves, PLACE>), grid, block, 0, s, a, p);
     else hipLaunchKernelGGL((rotary_kernel<T, kStaged, PLACE>), grid, block, 0, s, a, p);
 }
 
 }  // namespace
 
 int64_t rotary_groups(const RotaryArgs& a) {
-    const int64_t t = tokens_of(a.T, a.r, rows_of(a));
+    const int64_t t = tokens_of(a);
     return (a.T + t - 1) / t;
 }
 
