@@ -11,13 +11,19 @@
 //    branch that a wave takes a few times per row).  With r = fl(m log2 e), exp(x - m) = 2^(x log2 e - r) 2^rest,
 //    rest = r - m log2 e: one fused product and sum and one exponential per logit, the last factor once for all.
 //    Beyond |m| = 2^24, where rest leaves [-1, 1], the difference x - m is taken first.
-//  * Best alternatives: the least of the maxima so far of n disjoint groups of threads is a lower bound of the
-//    n-th best logit.  It is taken again in rounds 0, 1, 2, 4, 8, ..., since it moves less and less; the logits at
-//    or above it are collected into lists and ranked by (value, token) at the end.  Where a list overflows (a long
-//    stretch of equal logits, such as a mask of a finite value, before better ones), the row is read once more
-//    with the last bound, and where that overflows too, once for each place.
+//  * Best alternatives: the n-th largest of the maxima so far of 64 disjoint groups of threads is a lower bound of the
+//    n-th best logit; its upper 16 bits are found by 16 counts over a wave.  It is taken again in rounds 0, 1, 2, 4,
+//    8, ..., since it moves less and less; the logits at or above it are collected into lists, those below the last
+//    bound taken out, and the rest ranked by (value, token) at the end.  Where a list overflows (a long stretch of equal
+//    logits, such as a mask of a finite value, before better ones), the row is read once more with the last bound,
+//    and where that overflows too, once for each place.  (2048 rows of 50257 in bf16: 20 best with the entropy 58 us,
+//    115 with the least of the maxima of 32 groups as the bound, which lets five times as many logits pass; 5 best 53,
+//    none 43.)
 //  * A row belongs to one wave where it is short, to a workgroup where it is not, and to several workgroups where
 //    there are few rows; a second launch joins their parts.
+//  * Logits and gradients of more than the 256 MB of the memory's own cache pass the caches by: 4096 rows of 131072 in
+//    bf16, 188 us, 5.7 TB/s (196 without); their gradient 340 us, 6.3 TB/s (373).  Less of them stays there from
+//    the product before: 2048 rows of 50257, 205 MB, 41 us, past the caches 44.
 #include <math.h>
 
 #include "kda_device.h"
@@ -39,6 +45,13 @@ constexpr double kLn2 = 0.6931471805599453;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// 16 bytes; PASS: the caches are left to others
+template <bool PASS>
+__device__ __forceinline__ u32x4 load_16(const void* at) {
+    const u32x4* p = static_cast<const u32x4*>(at);
+    return PASS ? __builtin_nontemporal_load(p) : *p;
+}
+
 // The logits of a thread's round.  `wide`: the round lies inside the part and is read in 16-byte vectors; else the
 // tokens are strided over the threads, and those outside of the part become -inf.
 template <typename T, int TPR>
@@ -47,9 +60,11 @@ struct Rounds {
     static __device__ __forceinline__ int token(int base, int i, bool wide, int t) {
         return wide ? base + (i / W) * TPR * W + t * W + i % W : base + i * TPR + t;
     }
+    template <bool PASS>
     static __device__ __forceinline__ void fetch(const T* row, int base, int t, u32x4 (&raw)[NV]) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) raw[v] = *reinterpret_cast<const u32x4*>(row + base + v * TPR * W + t * W);
+        for (int v = 0; v < NV; ++v)
+            raw[v] = load_16<PASS>(row + base + v * TPR * W + t * W);
     }
     static __device__ __forceinline__ void values(const u32x4 (&raw)[NV], float (&x)[kPer]) {
 #pragma unroll
@@ -200,13 +215,13 @@ struct LogprobPlan {
     int per_part;  // tokens of a part, a multiple of a round
 };
 
-template <typename T, int WPR, bool TOP, bool ENT>
-__global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, LogprobPlan plan, int group_shift,
-                                                                uint64_t* keys, float4* sums) {
+template <typename T, int WPR, bool TOP, bool ENT, bool PASS>
+__global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, LogprobPlan plan, uint64_t* keys,
+                                                                float4* sums) {
     constexpr int TPR = 64 * WPR;
     using R = Rounds<T, TPR>;
     __shared__ uint64_t s_list[TOP ? kWaves : 1][TOP ? kList + 8 : 1], s_best[TOP ? kWaves : 1][TOP ? kMaxTop : 1];
-    __shared__ float s_m[kWaves], s_l[kWaves], s_s[kWaves], s_g[2][kWaves];
+    __shared__ float s_m[kWaves], s_l[kWaves], s_s[kWaves], s_g[2][64];
     __shared__ double s_lse;
     __shared__ int s_count[kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -232,25 +247,24 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
     Sums<ENT> sum;
     float most = -INFINITY, bar = -INFINITY;  // this thread's maximum, the row's bound
     int mine = 0, turns = 0;                  // keys this wave has collected
-    auto raise = [&] {  // the least of the maxima of groups of 2^group_shift threads
+    auto raise = [&] {  // the n-th largest of the maxima of 64 groups of threads, by its upper 16 bits
         float g = most;
-        g = max_min_step<0>(g, group_shift);
-        g = max_min_step<1>(g, group_shift);
-        g = max_min_step<2>(g, group_shift);
-        g = max_min_step<3>(g, group_shift);
-        g = max_min_step<4>(g, group_shift);
-        g = max_min_step<5>(g, group_shift);
         if constexpr (WPR == 4) {
+            g = max_min_step<0>(g, 2);
+            g = max_min_step<1>(g, 2);
             const int turn = turns++ & 1;
-            if (lane == 0) s_g[turn][wave] = g;
+            if ((lane & 3) == 0) s_g[turn][wave * 16 + lane / 4] = g;
             __syncthreads();
-            g = s_g[turn][0];
-            float h = s_g[turn][2];
-            g = group_shift > 6 ? fmaxf(g, s_g[turn][1]) : fminf(g, s_g[turn][1]);
-            h = group_shift > 6 ? fmaxf(h, s_g[turn][3]) : fminf(h, s_g[turn][3]);
-            g = group_shift > 7 ? fmaxf(g, h) : fminf(g, h);
+            g = s_g[turn][lane];
         }
-        bar = g;
+        const uint32_t u = ordered(g) >> 16;
+        uint32_t least = 0;
+#pragma unroll
+        for (int bit = 15; bit >= 0; --bit) {
+            const uint32_t more = least | 1u << bit;
+            least = __popcll(__ballot(u >= more)) >= a.top ? more : least;
+        }
+        bar = least << 16 > ordered(-INFINITY) ? unordered(least << 16) : -INFINITY;
     };
     auto collect = [&](const float (&x)[kPer], float top, int base, bool wide) {
         const float least = bar == -INFINITY ? -3.402823466e38f : bar;  // -inf is not collected
@@ -267,6 +281,20 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
             }
         }
     };
+    auto filter = [&] {  // this wave's keys below the bound leave its list
+        if (bar == -INFINITY || mine > kList) return;
+        const uint32_t least = ordered(bar + 0.f);
+        int kept = 0;
+        for (int i0 = 0; i0 < mine; i0 += 64) {
+            const uint64_t k = s_list[wave][i0 + lane < mine ? i0 + lane : 0];
+            const uint64_t mask = __ballot(i0 + lane < mine && (uint32_t)(k >> 32) >= least);
+            const int at = kept + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                            __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+            if (mask >> lane & 1) s_list[wave][at] = k;  // (not behind what has been read)
+            kept += __popcll(mask);
+        }
+        mine = kept;
+    };
     // (the maxima leave out NaN)
     auto top_of = [](const float (&x)[kPer]) {
         float y = -INFINITY;
@@ -277,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
 
     u32x4 next[R::NV];
     bool ready = begin >= 0 && begin + R::SIZE <= last;
-    if (ready) R::fetch(x0, begin, t, next);
+    if (ready) R::template fetch<PASS>(x0, begin, t, next);
     int round = 0;
     for (int base = begin; base < last; base += R::SIZE, ++round) {
         const bool wide = ready;
@@ -285,12 +313,15 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
         if (wide) R::values(next, x);
         else R::cut(x0, base, first, last, t, x);
         ready = base + R::SIZE >= 0 && base + 2 * R::SIZE <= last;
-        if (ready) R::fetch(x0, base + R::SIZE, t, next);  // on its way while this one is worked on
+        if (ready) R::template fetch<PASS>(x0, base + R::SIZE, t, next);  // on its way while this one is worked on
         const float top = top_of(x);
         sum.template add<false>(x, top);
         if constexpr (TOP) {
             most = fmaxf(most, top);
-            if ((round & (round - 1)) == 0) raise();
+            if ((round & (round - 1)) == 0) {
+                raise();
+                if (mine > kList / 2) filter();
+            }
             collect(x, top, base, wide);
         }
     }
@@ -326,6 +357,8 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
         lse = finish<T>(a, row, p);
     }
     if constexpr (!TOP) return;
+    raise();
+    filter();
 
     // the row's best, in order
     auto counts = [&](int& total) {  // of the row's waves; whether a list has overflowed
@@ -348,7 +381,6 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
     int total;
     bool full = counts(total);
     if (full) {  // once more with the last bound
-        raise();
         mine = 0;
         for (int base = begin; base < last; base += R::SIZE) {
             float x[kPer];
@@ -445,7 +477,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, L
     const bool on = lane < plan.parts;
     const float4 y = sums[row * plan.parts + (on ? lane : 0)];
     const uint64_t* mine = keys + (row * plan.parts + (on ? lane : 0)) * a.top;
-    uint64_t head = on && a.top ? mine[0] : 0;
+    uint64_t head = on && a.top ? mine[0] : 0, next = on && a.top > 1 ? mine[1] : 0;
     const Part p = over_wave(on ? Part{y.x, y.y, y.z} : Part{-INFINITY, 0.f, 0.f});
     double lse = 0.;
     if (lane == 0) lse = finish<T>(a, row, p);
@@ -453,14 +485,25 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, L
     int at = 0;
     uint64_t got = 0;  // lane o: the o-th best
     for (int o = 0; o < a.top; ++o) {
-        uint64_t top = head;
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            const uint64_t z = shfl_xor64(top, off);
-            top = z > top ? z : top;
+        // the first lane with the largest value: the parts' tokens ascend
+        const float value = head ? unordered((uint32_t)(head >> 32)) : -INFINITY;
+        float top = value;
+        top = max_min_step<0>(top, 6);
+        top = max_min_step<1>(top, 6);
+        top = max_min_step<2>(top, 6);
+        top = max_min_step<3>(top, 6);
+        top = max_min_step<4>(top, 6);
+        top = max_min_step<5>(top, 6);
+        const uint64_t among = __ballot(head != 0 && value == top);
+        if (among == 0) break;
+        const int from = __builtin_ctzll(among);
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)head, from);
+        const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(head >> 32), from);
+        if (lane == o) got = (uint64_t)hi << 32 | lo;
+        if (lane == from) {
+            head = next;
+            next = ++at + 1 < a.top ? mine[at + 1] : 0;
         }
-        if (lane == o) got = top;
-        if (head == top && head != 0) head = ++at < a.top ? mine[at] : 0;  // keys differ: one lane moves on
     }
     if (lane < a.top) put_best(a, row, lane, got, lse);
 }
@@ -470,7 +513,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, L
 // ------------------------------------------------------------------------------------------
 // dx_v = p_v (d_lse - d_logprob - d_H (log p_v + H)) + d_logprob [v = token].  Pure traffic in small pieces: a wave
 // takes 64 x 16 logits of a row.
-template <typename T, bool ENT>
+template <typename T, bool ENT, bool PASS>
 __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs a, int chunks) {
     constexpr int W = 16 / sizeof(T), NV = kPer / W, SPAN = 64 * kPer;
     const int lane = threadIdx.x & 63;
@@ -489,7 +532,7 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
     if (wide) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            raw[v] = *reinterpret_cast<const u32x4*>(x0 + base + v * 64 * W + lane * W);
+            raw[v] = load_16<PASS>(x0 + base + v * 64 * W + lane * W);
     } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -534,7 +577,8 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
                     out[i] = __builtin_bit_cast(uint32_t, y);
                 }
             }
-            *reinterpret_cast<u32x4*>(y0 + c0) = out;
+            if constexpr (PASS) __builtin_nontemporal_store(out, reinterpret_cast<u32x4*>(y0 + c0));
+            else *reinterpret_cast<u32x4*>(y0 + c0) = out;
         }
     } else {
 #pragma unroll
@@ -549,6 +593,9 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
 }
 
 int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
+
+// Whether so many bytes pass the caches by.
+bool pass_by(int64_t bytes) { return bytes > (int64_t)256 << 20; }
 
 LogprobPlan plan_of(int64_t R, int V) {
     LogprobPlan p;
@@ -565,19 +612,18 @@ LogprobPlan plan_of(int64_t R, int V) {
     return p;
 }
 
-int group_shift_of(int top, int waves) {
-    int groups = 1, shift = waves == 1 ? 6 : 8;
-    while (groups < top) groups *= 2, --shift;
-    return shift;
-}
-
 template <typename T, int WPR, bool TOP>
 void launch_scan(const LogprobArgs& a, const LogprobPlan& p, uint64_t* keys, float4* sums, hipStream_t s) {
     const int64_t items = a.R * p.parts;
     const dim3 grid((unsigned)(WPR == 1 ? div_up(items, kWaves) : items)), block(kThreads);
-    const int shift = group_shift_of(a.top, WPR);
-    if (a.entropy) hipLaunchKernelGGL((logprob_scan_kernel<T, WPR, TOP, true>), grid, block, 0, s, a, p, shift, keys, sums);
-    else hipLaunchKernelGGL((logprob_scan_kernel<T, WPR, TOP, false>), grid, block, 0, s, a, p, shift, keys, sums);
+    const bool past = WPR == kWaves && pass_by(a.R * a.V * (int64_t)sizeof(T));
+    if (past) {
+        if (a.entropy) hipLaunchKernelGGL((logprob_scan_kernel<T, WPR, TOP, true, WPR == kWaves>), grid, block, 0, s, a, p, keys, sums);
+        else hipLaunchKernelGGL((logprob_scan_kernel<T, WPR, TOP, false, WPR == kWaves>), grid, block, 0, s, a, p, keys, sums);
+    } else {
+        if (a.entropy) hipLaunchKernelGGL((logprob_scan_kernel<T, WPR, TOP, true, false>), grid, block, 0, s, a, p, keys, sums);
+        else hipLaunchKernelGGL((logprob_scan_kernel<T, WPR, TOP, false, false>), grid, block, 0, s, a, p, keys, sums);
+    }
 }
 template <typename T>
 void launch_scan(const LogprobArgs& a, const LogprobPlan& p, uint64_t* keys, float4* sums, hipStream_t s) {
@@ -591,6 +637,22 @@ void launch_scan(const LogprobArgs& a, const LogprobPlan& p, uint64_t* keys, flo
 }
 
 int64_t sums_bytes(int64_t R, const LogprobPlan& p) { return div_up(R * p.parts * (int64_t)sizeof(float4), 256) * 256; }
+
+int64_t grad_chunks(int V) { return div_up((int64_t)V + 7, 64 * kPer); }
+
+template <typename T, bool ENT>
+void launch_grad(const LogprobGradArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)logprob_grad_groups(a.R, a.V)), block(kThreads);
+    const int chunks = (int)grad_chunks(a.V);
+    if (pass_by(2 * a.R * a.V * (int64_t)sizeof(T)))
+        hipLaunchKernelGGL((logprob_grad_kernel<T, ENT, true>), grid, block, 0, s, a, chunks);
+    else hipLaunchKernelGGL((logprob_grad_kernel<T, ENT, false>), grid, block, 0, s, a, chunks);
+}
+template <typename T>
+void launch_grad(const LogprobGradArgs& a, hipStream_t s) {
+    if (a.d_entropy) launch_grad<T, true>(a, s);
+    else launch_grad<T, false>(a, s);
+}
 
 }  // namespace
 
@@ -623,22 +685,14 @@ hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s) {
     return e;
 }
 
-static int64_t grad_chunks(int V) { return div_up((int64_t)V + 7, 64 * kPer); }
 int64_t logprob_grad_groups(int64_t R, int V) { return div_up(R * grad_chunks(V), kWaves); }
 
 hipError_t launch_logprob_grad(const LogprobGradArgs& a, hipStream_t s) {
     if (a.R == 0) return hipSuccess;
-    const dim3 grid((unsigned)logprob_grad_groups(a.R, a.V)), block(kThreads);
-    const int chunks = (int)grad_chunks(a.V);
     const bool timed = timing_on();
     if (timed) timed_begin(kKernelLogprobGrad, s);
-    if (a.bf16) {
-        if (a.d_entropy) hipLaunchKernelGGL((logprob_grad_kernel<uint16_t, true>), grid, block, 0, s, a, chunks);
-        else hipLaunchKernelGGL((logprob_grad_kernel<uint16_t, false>), grid, block, 0, s, a, chunks);
-    } else {
-        if (a.d_entropy) hipLaunchKernelGGL((logprob_grad_kernel<float, true>), grid, block, 0, s, a, chunks);
-        else hipLaunchKernelGGL((logprob_grad_kernel<float, false>), grid, block, 0, s, a, chunks);
-    }
+    if (a.bf16) launch_grad<uint16_t>(a, s);
+    else launch_grad<float>(a, s);
     const hipError_t e = hipGetLastError();
     if (timed) timed_end(s);
     return e;
