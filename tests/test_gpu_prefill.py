@@ -1,4 +1,4 @@
-"""Attention of a chunk of new tokens over pages on the GPU against plain 64-bit code, and the prompt's calls together.
+"""Attention of a chunk of new tokens over pages on the GPU against plain 64-bit code.
 
 Tolerances (u = 2^-24; a rounding to bf16 is off by 2^-8 of the value at most): those of the one-token attention
 (test_gpu_serving.py) with two more roundings for bf16.  A score is off by ds <= (d + 3) u scale sum|q k|, a weight by
@@ -324,3 +324,24 @@ def test_paged_prefill_repeats_bit_for_bit(dtype):
     for _ in range(3):
         b = kda.paged_prefill(q, cache.kp, cache.vp, cache.table, cache.len, cu_of(new), lse=True)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 2, 17, 63, 64, 65, 100])
+def test_paged_prefill_of_uneven_sequences(dtype, n):
+    """Lengths from one to thousands in a batch, whose shares go by the lengths up to 64 sequences and by their bound
+    beyond; a table much wider than any of them."""
+    new = [1 + (3 * i) % 6 for i in range(n)]
+    past = [(2900 * (i % 5 == 0) + 53 * i) % 3300 for i in range(n)]
+    past[0] = 3000
+    cache = Cache([a + b for a, b in zip(new, past)], 1, 64, 32, dtype, seed=n, extra_cols=300)
+    check(cache, queries(sum(new), 4, 64, dtype, scale=1.0), new)
+    check(cache, queries(sum(new), 4, 64, dtype, scale=1.0), new, max_length=max(cache.lengths), window=1500, sinks=5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_paged_prefill_of_a_long_chunk_behind_short_ones(dtype):
+    """Many rows: one long sequence is split, the short ones are not; more key-value heads than one."""
+    new = [3, 120, 1, 40]
+    cache = Cache([9, 5000, 30, 700], 3, 64, 16, dtype, seed=91)
+    check(cache, queries(sum(new), 6, 64, dtype, scale=1.0), new)
