@@ -21,7 +21,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -118,14 +120,17 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t N, int
 // over kGroups workgroups (a little more where that gives no more parts than those), and the parts are numbered.  With
 // more sequences the parts' length goes by the bound of the lengths.  16 sequences with 5 new tokens each, 32 heads over
 // 8, after 1000 to 16379 tokens: 84 us, 135 us with parts by the bound; kGroups of 384 and 1024: 89 and 92 us.  Parts of
-// 8 steps at least: one such sequence after 8000 tokens takes 24 us instead of 21.
+// 8 steps at least: one such sequence after 8000 tokens takes 24 us instead of 19.
 constexpr int kMaxParts = 64;
 constexpr int kGroups = 512, kLeast = 4;  // two workgroups per CU; steps of a part at least
-// The join costs 5 us, so nothing is split if the longest row tile may have fewer steps than this (many rows, 512 tokens:
-// 26 us, split 30; 173 after 3000, 50 steps: 34 us, with longer parts 38), nor if there are more row tiles than this (many
-// rows, 8 sequences of 48 to 2048 new tokens: 129 us, 132 with parts; few rows, lengths differ more).
-constexpr int kSplitSteps[2] = {2 * kLeast, 4 * kLeast};  // few rows, many rows
-constexpr int64_t kSplitTiles[2] = {2048, 256};
+// A part costs its own first tiles and its results' way through memory, the join 5 us and more.  Few rows: not split below
+// two shortest parts, nor with several rounds of workgroups.  Many rows: only where few row tiles have many steps.  32
+// heads over 8, in us split and not: 33 tokens after 1000 (16 tiles, 17 steps) 19 and 28; 300 after 1500 (80, 29) 32 and
+// 39; 512 after 1500 (136, 32) 39 and 43; 600 after 600 (152, 19) 38 and 32; 900 after 1500 (232, 38) 56 and 50; 2048
+// (520, 33) 78 and 55; but 8 sequences of 48 to 2048 tokens (1272, 56) 108 and 113.
+__host__ inline bool worth_splitting(bool rows, int64_t tiles, int64_t steps) {
+    return rows ? tiles <= 256 && steps >= 12 + tiles / 8 : tiles <= 2048 && steps >= 2 * kLeast;
+}
 struct PrefillPlan {
     int64_t slots;  // row tiles of a key-value head at most
     int groups;     // workgroups of a head that the chip holds; 0: nothing is split
@@ -136,12 +141,14 @@ struct Item {
     int64_t n, tile;         // the row tile, of sequence n (-1: none)
     int part, parts, steps;  // steps of a part
     int64_t split;           // the row tile's first among the split parts
+    int places;              // split parts in all
 };
 
-// What the workspace holds: of every row tile its parts and its first split part; of the split parts of every head
-// (reference, sum) of the rows, then their outputs [RT, D].
+// What the workspace holds: the number of split parts; of each its sequence, row tile, the parts of that and its place
+// among them; of the split parts of every head (reference, sum) of the rows, then their outputs [RT, D].
 struct Partials {
-    int2* tiles;
+    int* count;
+    int4* part;
     float2* ml;
     float* out;
 };
@@ -162,7 +169,7 @@ __host__ __device__ __forceinline__ int steps_to(const PagedPrefillArgs& a, int6
 template <int RT, int BN, int STEP>
 __device__ __forceinline__ Item item_of(const PagedPrefillArgs& a, const PrefillPlan& plan, int64_t j) {
     const int G = a.Hq / a.Hkv;
-    Item x{-1, 0, 0, 1, 0x7FFFFFFF, 0};
+    Item x{-1, 0, 0, 1, 0x7FFFFFFF, 0, 0};
     if (plan.groups == 0 || plan.parts > 0) {
         if (plan.parts > 0) {
             x.parts = plan.parts;
@@ -170,6 +177,7 @@ __device__ __forceinline__ Item item_of(const PagedPrefillArgs& a, const Prefill
             x.part = (int)(j / plan.slots);
             j %= plan.slots;
             x.split = j * plan.parts;
+            x.places = (int)plan.slots * plan.parts;
         }
         j = plan.slots - 1 - j;  // late tiles first: they have the most keys
         x.n = sequence_of(a.cu, a.N, j, G, RT);
@@ -214,25 +222,27 @@ __device__ __forceinline__ Item item_of(const PagedPrefillArgs& a, const Prefill
     const int at_lane = __builtin_ctzll(good & fits);
     const float chosen = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(P), at_lane));
     const float chosen_per = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(per), at_lane));
-    // the item among the parts of all
+    // the item among the parts of all, late tiles first: they have the most keys
     const int k = (int)fmaxf(parts_of((float)steps, chosen, chosen_per), 1.f), mine = tiles * k, mine_split = k > 1 ? mine : 0;
-    int sum = mine, sum_split = mine_split;
+    int before = mine, split_before = mine_split;  // of this sequence and those behind it
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(sum, off, 64), z = __shfl_up(sum_split, off, 64);
-        if (lane >= off) sum += y, sum_split += z;
+        const int y = __shfl_down(before, off, 64), z = __shfl_down(split_before, off, 64);
+        if (lane + off < 64) before += y, split_before += z;
     }
-    const int items = __builtin_amdgcn_readlane(sum, 63);
+    const int items = __builtin_amdgcn_readfirstlane(before);
+    x.places = __builtin_amdgcn_readfirstlane(split_before);
+    before -= mine;
+    split_before -= mine_split;
     if (j >= items) return x;
-    const int at = items - 1 - (int)j;  // late tiles first
-    const int in = __builtin_ctzll(__ballot(sum > at));
-    const int inside = at - __builtin_amdgcn_readlane(sum - mine, in);
+    const int in = __builtin_ctzll(__ballot(before <= (int)j && (int)j < before + mine));
+    const int inside = __builtin_amdgcn_readlane(before + mine, in) - 1 - (int)j;
     x.n = in;
     x.parts = __builtin_amdgcn_readlane(k, in);
     x.tile = inside / x.parts;
     x.part = inside - (int)x.tile * x.parts;
     x.steps = (__builtin_amdgcn_readlane(steps, in) + x.parts - 1) / x.parts;
-    x.split = x.parts > 1 ? __builtin_amdgcn_readlane(sum_split - mine_split, in) + x.tile * x.parts : 0;
+    x.split = x.parts > 1 ? __builtin_amdgcn_readlane(split_before, in) + x.tile * x.parts : 0;
     return x;
 }
 
@@ -298,13 +308,15 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
     const int h = (int)(blockIdx.x % a.Hkv);
     const Item item = item_of<RT, BN, ROWS ? 1 : WAVES>(a, plan, blockIdx.x / a.Hkv);
     RowTile tile;
-    if (!row_tile_of<RT, BN>(a, item, tile)) return;
-    const int parts = parts_in_fact(item, tile, ROWS ? 1 : WAVES);
-    if (item.part >= parts || (parts > 1 && item.split + item.part >= places_of(plan.groups))) return;
-    if (plan.groups && item.part == 0 && h == 0 && tid == 0) {
-        const int64_t slot = slot_begin(a.cu, item.n, G, RT) + item.tile;
-        if (slot >= 0 && slot < plan.slots) ws.tiles[slot] = make_int2(parts, (int)item.split);
+    const bool any = row_tile_of<RT, BN>(a, item, tile);
+    const int parts = any ? parts_in_fact(item, tile, ROWS ? 1 : WAVES) : 0;
+    if (plan.groups && h == 0 && tid == 0) {  // for the join
+        const int64_t place = item.split + item.part;
+        if (blockIdx.x == 0) *ws.count = item.places;
+        if (item.parts > 1 && place < places_of(plan.groups))
+            ws.part[place] = make_int4((int)item.n, (int)item.tile, parts, item.part);
     }
+    if (item.part >= parts || (parts > 1 && item.split + item.part >= places_of(plan.groups))) return;
     const int64_t cu0 = tile.cu0, i0 = tile.i0;
     const int g0 = tile.g0, rows = tile.rows, near = tile.near, end = tile.end, head = tile.head;
     const int head_tiles = tile.head_tiles, first = tile.first, tiles = tile.tiles;
@@ -549,47 +561,60 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
         }
     };
 
-    // One tile of which some key is not visible to some row, or where some row has no reference yet.
-    auto work_edge = [&](const char* kt, int base, int lo, int hi, int gone, const Next& next) {
+    // One tile of which some key is not visible to some row (`hidden`), or where some row has no reference yet.
+    auto work_edge = [&](const char* kt, int base, int lo, int hi, int gone, bool hidden, const Next& next) {
         const char* vt = kt + S::TILE;
         if constexpr (!ROWS) wait_loads_but<ALL_LOADS / 2>();
         f32x16 x[KG];
+        u32x4 ring[AHEAD];
+        auto key = [&](int j) {
+            return *reinterpret_cast<const u32x4*>(kt + (j % NK / 4) * BN * 128 + (j / NK) * 32 * 128 + k_lane[j % NK & 3]);
+        };
 #pragma unroll
-        for (int kg = 0; kg < KG; ++kg) {
-            x[kg] = zeros();
-#pragma unroll
-            for (int s = 0; s < QW; ++s) {
-                const u32x4 k = *reinterpret_cast<const u32x4*>(kt + (s / 4) * BN * 128 + kg * 32 * 128 + k_lane[s & 3]);
-                if constexpr (kBf16) {
-                    x[kg] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, k),
-                                                                    __builtin_bit_cast(bf16x8, q[s]), x[kg], 0, 0, 0);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[kg] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(k[i]), __uint_as_float(q[s][i]),
-                                                                     x[kg], 0, 0, 0);
-                }
-            }
-        }
+        for (int j = 0; j < AHEAD; ++j) ring[j] = key(j);
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < KG * NK; ++j) {
+            const u32x4 k = ring[j % AHEAD];
+            const int kg = j / NK, s = j % NK;
+            if (s == 0) x[kg] = zeros();
+            if constexpr (kBf16) {
+                x[kg] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, k),
+                                                                __builtin_bit_cast(bf16x8, q[s]), x[kg], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[kg] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(k[i]), __uint_as_float(q[s][i]), x[kg], 0, 0, 0);
+            }
+            if (j + AHEAD < KG * NK) ring[j % AHEAD] = key(j + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if constexpr (!ROWS) {
             wait_loads_but<ALL_LOADS / 2>();
             load_some(next, 0, ALL_LOADS / 2);
         }
-        {
+        if (hidden) {
             // visible: places first .. first + many - 1 of the tile, and the sinks' 0 .. more - 1, for this lane's half
             const int top = (hi - 1 < p ? hi - 1 : p) - base + 1;  // places below it
             const int from = (lo > p_near ? lo : p_near) - base, many = top > from ? top - from : 0;
             const int sink = (a.sinks < base + top ? a.sinks : base + top) - lo, more = sink > 0 ? sink : 0;
             const int first = 4 * hl - from, less = 4 * hl - (lo - base);
+            if (a.window == 0 && gone == 0) {  // (from and lo are 0 or before the tile)
 #pragma unroll
-            for (int kg = 0; kg < KG; ++kg)
+                for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int at = kg * 32 + 8 * (i >> 2) + (i & 3);
-                    const bool on = ((uint32_t)(first + at) < (uint32_t)many) | ((uint32_t)(less + at) < (uint32_t)more);
-                    x[kg][i] = (on & !((gone >> (at / kPage)) & 1)) ? x[kg][i] : -INFINITY;
-                }
+                    for (int i = 0; i < 16; ++i)
+                        x[kg][i] = kg * 32 + 8 * (i >> 2) + (i & 3) < top - 4 * hl ? x[kg][i] : -INFINITY;
+            } else {
+#pragma unroll
+                for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int at = kg * 32 + 8 * (i >> 2) + (i & 3);
+                        const bool on = ((uint32_t)(first + at) < (uint32_t)many) | ((uint32_t)(less + at) < (uint32_t)more);
+                        x[kg][i] = (on & !((gone >> (at / kPage)) & 1)) ? x[kg][i] : -INFINITY;
+                    }
+            }
         }
         if (pass == 1 || __any(m == -INFINITY)) {
             float top = -INFINITY;
@@ -620,46 +645,83 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
         }
         // In a tile with hidden keys, values that are not finite count as 0: a hidden one's weight of 0 would make them
         // NaN.  The outputs that see them are noted below.
-        uint32_t odd = 0;
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (!ROWS) wait_loads_but<ALL_LOADS / 2>();
+        auto val = [&](int j) {
+            const int kg = j / NV, c = j % NV % CT, part = j % NV / CT;
+            u32x4 y;
+            if constexpr (kBf16) {
+                y = value(vt, c, kg, part);
+            } else {
 #pragma unroll
-        for (int kg = 0; kg < KG; ++kg) {
+                for (int i = 0; i < 4; ++i) y[i] = __float_as_uint(value32(vt, c, kg, part * 4 + i));
+            }
+            return y;
+        };
+        bool odd = false;
+        if (hidden) {
+            // the largest as unsigned and as signed numbers: a NaN or infinity of either sign is above the finite ones there
+            if constexpr (kBf16) {
+                s16x2 most = {0, 0};
+                u16x2 least = {0, 0};
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                if constexpr (kBf16) {
+                for (int j = 0; j < KG * NV; ++j) {
+                    const u32x4 y = val(j);
 #pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        u32x4 v = value(vt, c, kg, st);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t y = odd_bits(v[i]);
-                            odd |= y;
-                            v[i] &= ~y;
-                        }
-                        const u32x4 y = {pf[kg][4 * st], pf[kg][4 * st + 1], pf[kg][4 * st + 2], pf[kg][4 * st + 3]};
-                        o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
-                                                                       __builtin_bit_cast(bf16x8, y), o[c], 0, 0, 0);
-                        if constexpr (!ROWS) {
-                            const u32x4 z = {pr[kg][4 * st], pr[kg][4 * st + 1], pr[kg][4 * st + 2], pr[kg][4 * st + 3]};
-                            o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
-                                                                           __builtin_bit_cast(bf16x8, z), o[c], 0, 0, 0);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float v = value32(vt, c, kg, i);
-                        const bool y = !(fabsf(v) < INFINITY);
-                        odd |= y;
-                        v = y ? 0.f : v;
-                        o[c] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, x[kg][i], o[c], 0, 0, 0);
+                    for (int i = 0; i < 4; ++i) {
+                        most = __builtin_elementwise_max(most, __builtin_bit_cast(s16x2, (uint32_t)y[i]));
+                        least = __builtin_elementwise_max(least, __builtin_bit_cast(u16x2, (uint32_t)y[i]));
                     }
                 }
+                odd = max(most[0], most[1]) >= 0x7F80 || max(least[0], least[1]) >= 0xFF80;
+            } else {
+                int most = 0;
+                uint32_t least = 0;
+#pragma unroll
+                for (int j = 0; j < KG * NV; ++j) {
+                    const u32x4 y = val(j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        most = max(most, (int)y[i]);
+                        least = max(least, (uint32_t)y[i]);
+                    }
+                }
+                odd = most >= 0x7F800000 || least >= 0xFF800000u;
             }
+            odd = __any(odd);
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) ring[j] = val(j);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < KG * NV; ++j) {
+            u32x4 v = ring[j % AHEAD];
+            const int kg = j / NV, c = j % NV % CT, part = j % NV / CT;
+            if (odd) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (kBf16) v[i] &= ~odd_bits(v[i]);
+                    else v[i] = fabsf(__uint_as_float(v[i])) < INFINITY ? v[i] : 0u;
+                }
+            }
+            if constexpr (kBf16) {
+                const u32x4 y = {pf[kg][4 * part], pf[kg][4 * part + 1], pf[kg][4 * part + 2], pf[kg][4 * part + 3]};
+                o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
+                                                               __builtin_bit_cast(bf16x8, y), o[c], 0, 0, 0);
+                if constexpr (!ROWS) {
+                    const u32x4 z = {pr[kg][4 * part], pr[kg][4 * part + 1], pr[kg][4 * part + 2], pr[kg][4 * part + 3]};
+                    o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
+                                                                   __builtin_bit_cast(bf16x8, z), o[c], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[c] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(v[i]), x[kg][4 * part + i], o[c], 0, 0, 0);
+            }
+            if (j + AHEAD < KG * NV) ring[j % AHEAD] = val(j + AHEAD);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (__any(odd != 0)) {  // how many such values each sum has a weight for
+        if (odd) {  // how many such values each sum has a weight for
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 f32x16 count = zeros();
@@ -776,10 +838,11 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
     bool ready = false;  // all rows of the wave have a reference
     const int whole_lo = p_near_last > near ? p_near_last : near, whole_hi = pw_first + 1 < end ? pw_first + 1 : end;
     const int whole_t0 = head_tiles - first + (whole_lo + BN - 1) / BN, whole_t1 = head_tiles - first + whole_hi / BN;
-    auto whole = [&](int i) {
+    auto hides = [&](int i) {
         const int t = t0 + w0 + STEP * i;
-        return ready && absent_of(i) == 0 && t >= whole_t0 && t < whole_t1;
+        return absent_of(i) != 0 || t < whole_t0 || t >= whole_t1;
     };
+    auto whole = [&](int i) { return ready && !hides(i); };
     auto begin = [&](int i) {
         if ((i + 1) % PER == 0) advance(i + 1);
         if constexpr (ROWS) {  // tile i is there, and the other buffer has been read
@@ -799,13 +862,14 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
         for (int i = 0; i < steps;) {
             for (; i < steps && !whole(i); ++i) {
                 const int t = t0 + w0 + STEP * i, base = base_of(t), gone = absent_of(i);
+                const bool hidden = hides(i);
                 begin(i);
                 if constexpr (ROWS) {
                     load_some(next_of(i + 1), 0, ALL_LOADS);
                     if (!active || base > pw_last) continue;
                 }
                 work_edge(s_kv[ROWS ? i & 1 : w], base, t < head_tiles ? 0 : near, t < head_tiles ? head : end, gone,
-                          next_of(i + 1));
+                          hidden, next_of(i + 1));
                 ready = pass != 1 && !__any(m == -INFINITY);
             }
             for (; i < steps && whole(i); ++i) {
@@ -934,54 +998,62 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
     }
 }
 
-// Join of the parts of the row tiles that are split: 4 channels of a row for each thread.
+// Join of the parts of the row tiles that are split: 4 channels of a row for each thread.  A row tile's blocks of rows go
+// round its parts and kJoin workgroups of each.
+constexpr int kJoin = 4;
 template <typename T, int D, bool ROWS>
 __global__ __launch_bounds__(256) void prefill_join_kernel(PagedPrefillArgs a, PrefillPlan plan, Partials ws) {
     using S = Shape<T, D, ROWS>;
-    constexpr int RT = S::RT, AHEAD = 8, COLS = D / 4, RG = 256 / COLS;  // rows of a workgroup
+    constexpr int RT = S::RT, AHEAD = 8, COLS = D / 4, RG = 256 / COLS;  // rows of a block
     __shared__ float2 s_ml[kMaxParts][RG];
     const int tid = threadIdx.x, G = a.Hq / a.Hkv, h = (int)(blockIdx.x % a.Hkv);
-    const int64_t b = blockIdx.x / a.Hkv, slot = b / (RT / RG);
-    const int2 info = ws.tiles[slot];
+    const int b = (int)(blockIdx.x / a.Hkv), place = b / kJoin, r = tid / COLS, c = tid % COLS * 4;
+    const int places = (int)places_of(plan.groups);
+    if (place >= *ws.count) return;
+    const int4 info = ws.part[place];
+    const int parts = info.z, first = place - info.w;
+    if (parts < 2 || parts > kMaxParts || info.w < 0 || info.w >= parts || first < 0 || first + parts > places) return;
+    if (info.x < 0 || info.x >= a.N) return;
     Item item{};
-    item.n = sequence_of(a.cu, a.N, slot, G, RT);
-    item.tile = slot - slot_begin(a.cu, item.n, G, RT);
+    item.n = info.x;
+    item.tile = info.y;
     RowTile tile;
     if (!row_tile_of<RT, S::BN>(a, item, tile)) return;
-    const int parts = info.x, r0 = (int)(b % (RT / RG)) * RG, r = tid / COLS, c = tid % COLS * 4;
-    if (parts < 2 || parts > kMaxParts || info.y < 0 || info.y + parts > places_of(plan.groups) || r0 >= tile.rows) return;
-    const int64_t at = (h * places_of(plan.groups) + info.y) * RT + r0;
-    // (rows behind the tile's last have places too)
-    const float* from = ws.out + (at + r) * D + c;
-    f32x4 z[AHEAD];
+    for (int r0 = (info.w + b % kJoin * parts) * RG; r0 < tile.rows; r0 += kJoin * parts * RG) {
+        const int64_t at = (h * places_of(plan.groups) + first) * RT + r0;
+        // (rows behind the tile's last have places too)
+        const float* from = ws.out + (at + r) * D + c;
+        f32x4 z[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) z[i] = *reinterpret_cast<const f32x4*>(from + (int64_t)(i < parts ? i : 0) * RT * D);
-    for (int x = tid; x < parts * RG; x += 256) s_ml[x / RG][x % RG] = ws.ml[at + x / RG * RT + x % RG];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < parts; ++i) M = fmaxf(M, s_ml[i][r].x);
-    f32x4 y = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < parts; i0 += AHEAD) {
+        for (int i = 0; i < AHEAD; ++i) z[i] = *reinterpret_cast<const f32x4*>(from + (int64_t)(i < parts ? i : 0) * RT * D);
+        for (int x = tid; x < parts * RG; x += 256) s_ml[x / RG][x % RG] = ws.ml[at + x / RG * RT + x % RG];
+        __syncthreads();
+        float M = -INFINITY, L = 0.f;
+        for (int i = 0; i < parts; ++i) M = fmaxf(M, s_ml[i][r].x);
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+        for (int i0 = 0; i0 < parts; i0 += AHEAD) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            if (i0 + i >= parts) break;
-            const float2 x = s_ml[i0 + i][r];
-            const float f = x.x == -INFINITY ? 0.f : exp2_hw(x.x - M);
-            L += x.y * f;
-            y += z[i] * f;
+            for (int i = 0; i < AHEAD; ++i) {
+                if (i0 + i >= parts) break;
+                const float2 x = s_ml[i0 + i][r];
+                const float f = x.x == -INFINITY ? 0.f : exp2_hw(x.x - M);
+                L += x.y * f;
+                y += z[i] * f;
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (i0 + AHEAD + i < parts) z[i] = *reinterpret_cast<const f32x4*>(from + (int64_t)(i0 + AHEAD + i) * RT * D);
         }
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (i0 + AHEAD + i < parts) z[i] = *reinterpret_cast<const f32x4*>(from + (int64_t)(i0 + AHEAD + i) * RT * D);
+        __syncthreads();  // the next block's references go there
+        if (r0 + r >= tile.rows) continue;
+        const float f = L == 0.f ? 0.f : 1.f / L;
+        const int64_t row = (tile.cu0 + tile.i0 + (tile.g0 + r0 + r) / G) * a.Hq + h * G + (tile.g0 + r0 + r) % G;
+        T* to = static_cast<T*>(a.o) + row * D + c;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(y[0] * f, y[1] * f), pack_bf16(y[2] * f, y[3] * f)};
+        else *reinterpret_cast<f32x4*>(to) = y * f;
+        if (c == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
     }
-    if (r0 + r >= tile.rows) return;
-    const float f = L == 0.f ? 0.f : 1.f / L;
-    const int64_t row = (tile.cu0 + tile.i0 + (tile.g0 + r0 + r) / G) * a.Hq + h * G + (tile.g0 + r0 + r) % G;
-    T* to = static_cast<T*>(a.o) + row * D + c;
-    if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(y[0] * f, y[1] * f), pack_bf16(y[2] * f, y[3] * f)};
-    else *reinterpret_cast<f32x4*>(to) = y * f;
-    if (c == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
 int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
@@ -1005,7 +1077,7 @@ PrefillPlan plan_of(const PagedPrefillArgs& a) {
     const Sizes z = sizes_of(a);
     p.slots = a.T * (a.Hq / a.Hkv) / z.rt + a.N;
     const int64_t steps = steps_to(a, a.max_length, z.rt, z.bn, z.step);
-    if (steps < kSplitSteps[z.rows] || p.slots * a.Hkv > kSplitTiles[z.rows]) return p;
+    if (!worth_splitting(z.rows, p.slots * a.Hkv, steps)) return p;
     p.groups = (int)div_up(kGroups, a.Hkv);
     if (a.N > 64) {
         int64_t parts = p.groups / p.slots;
@@ -1021,7 +1093,7 @@ int64_t items_of(const PrefillPlan& p) {
 }
 
 int64_t part_rows(const PagedPrefillArgs& a, const PrefillPlan& p) { return a.Hkv * places_of(p.groups) * sizes_of(a).rt; }
-size_t tile_bytes(const PrefillPlan& p) { return (size_t)(div_up(p.slots * 8, 256) * 256); }
+size_t part_bytes(const PrefillPlan& p) { return (size_t)(places_of(p.groups) * 16 + 256); }
 
 template <typename T, int D, bool ROWS>
 hipError_t launch_shape(const PagedPrefillArgs& a, const PrefillPlan& p, const Partials& y, hipStream_t s) {
@@ -1032,7 +1104,7 @@ hipError_t launch_shape(const PagedPrefillArgs& a, const PrefillPlan& p, const P
     hipError_t e = hipGetLastError();
     if (timed) timed_end(s);
     if (e != hipSuccess || !p.groups) return e;
-    const unsigned join = (unsigned)(p.slots * a.Hkv * (S::RT * D / 1024));
+    const unsigned join = (unsigned)(places_of(p.groups) * a.Hkv * kJoin);
     if (timed) timed_begin(kKernelPrefillJoin, s);
     hipLaunchKernelGGL((prefill_join_kernel<T, D, ROWS>), dim3(join), dim3(256), 0, s, a, p, y);
     e = hipGetLastError();
@@ -1055,7 +1127,7 @@ int64_t paged_prefill_groups(const PagedPrefillArgs& a, size_t* workspace) {
     const int64_t slots = a.T * (a.Hq / a.Hkv) / 32 + a.N;  // at most
     if (slots * a.Hkv > max_groups(256)) return slots * a.Hkv;
     const PrefillPlan p = plan_of(a);
-    if (p.groups && a.T > 0 && a.N > 0) *workspace = tile_bytes(p) + (size_t)(part_rows(a, p) * (8 + (int64_t)a.d * 4));
+    if (p.groups && a.T > 0 && a.N > 0) *workspace = part_bytes(p) + (size_t)(part_rows(a, p) * (8 + (int64_t)a.d * 4));
     return items_of(p) * a.Hkv;
 }
 
@@ -1064,8 +1136,9 @@ hipError_t launch_paged_prefill(const PagedPrefillArgs& a, hipStream_t s) {
     const PrefillPlan p = plan_of(a);
     Partials y{};
     if (p.groups) {
-        y.tiles = static_cast<int2*>(a.ws);
-        y.ml = reinterpret_cast<float2*>(static_cast<char*>(a.ws) + tile_bytes(p));
+        y.count = static_cast<int*>(a.ws);
+        y.part = reinterpret_cast<int4*>(static_cast<char*>(a.ws) + 256);
+        y.ml = reinterpret_cast<float2*>(static_cast<char*>(a.ws) + part_bytes(p));
         y.out = reinterpret_cast<float*>(y.ml + part_rows(a, p));
     }
     return a.bf16 ? launch_typed<uint16_t>(a, p, y, s) : launch_typed<float>(a, p, y, s);
