@@ -93,7 +93,9 @@ struct Shape {
     static constexpr int RT = ROWS ? 128 : 32;               // rows of a workgroup
     static constexpr int TILE = BN * ROW;                    // bytes of a tile's keys
     static constexpr int BUFS = ROWS ? 2 : WAVES;            // tiles in LDS
-    static constexpr int PER_SIMD = ROW <= (ROWS ? 512 : 256) ? 2 : 1;  // waves
+    // waves that share a SIMD's registers (bf16, d = 256: with two, 100 registers spill, and their loads wait for the next
+    // tile's; 8192 tokens after 8192, 16 heads over 4, 1.53 ms, with two 1.66)
+    static constexpr int PER_SIMD = ROW <= (ROWS && ES == 4 ? 512 : 256) ? 2 : 1;
 };
 
 // Row tiles of all sequences, not split: tile k of sequence n has slot floor(cu[n] G / RT) + n + k, which leaves every
@@ -120,21 +122,15 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t N, int
 // over kGroups workgroups (a little more where that gives no more parts than those), and the parts are numbered.  With
 // more sequences the parts' length goes by the bound of the lengths.  16 sequences with 5 new tokens each, 32 heads over
 // 8, after 1000 to 16379 tokens: 84 us, 135 us with parts by the bound; kGroups of 384 and 1024: 89 and 92 us.  Parts of
-// 8 steps at least: one such sequence after 8000 tokens takes 24 us instead of 19.
+// 8 steps at least: one such sequence after 8000 tokens takes 24 us instead of 19 with 4; fp32 steps are longer, 14 tokens
+// after 471 of 6 heads of 128 over 3: 21 us, with 4 steps at least 42.
 constexpr int kMaxParts = 64;
-constexpr int kGroups = 512, kLeast = 4;  // two workgroups per CU; steps of a part at least
-// A part costs its own first tiles and its results' way through memory, the join 5 us and more.  Few rows: not split below
-// two shortest parts, nor with several rounds of workgroups.  Many rows: only where few row tiles have many steps.  32
-// heads over 8, in us split and not: 33 tokens after 1000 (16 tiles, 17 steps) 19 and 28; 300 after 1500 (80, 29) 32 and
-// 39; 512 after 1500 (136, 32) 39 and 43; 600 after 600 (152, 19) 38 and 32; 900 after 1500 (232, 38) 56 and 50; 2048
-// (520, 33) 78 and 55; but 8 sequences of 48 to 2048 tokens (1272, 56) 108 and 113.
-__host__ inline bool worth_splitting(bool rows, int64_t tiles, int64_t steps) {
-    return rows ? tiles <= 256 && steps >= 12 + tiles / 8 : tiles <= 2048 && steps >= 2 * kLeast;
-}
+constexpr int kGroups = 512;  // two workgroups per CU (one with many rows and d = 256)
 struct PrefillPlan {
     int64_t slots;  // row tiles of a key-value head at most
     int groups;     // workgroups of a head that the chip holds; 0: nothing is split
     int parts, steps;  // parts of a row tile and their steps by the bound; 0: by the lengths
+    int least;         // steps of a part at least
 };
 // A workgroup's share.
 struct Item {
@@ -206,7 +202,7 @@ __device__ __forceinline__ Item item_of(const PagedPrefillArgs& a, const Prefill
     // The shares to choose from, one in each lane: P, 1.09 P and so on.  Those from 2 P on split into few enough parts,
     // since a split row tile's parts are at most twice its steps / P.
     const float share = ceilf(total * 1.0001f / (2 * plan.groups));
-    const float P = ceilf(fmaxf(fminf(share, 1e7f), (float)kLeast) * exp2_hw(0.125f * lane)), per = 1.f / P;
+    const float P = ceilf(fmaxf(fminf(share, 1e7f), (float)plan.least) * exp2_hw(0.125f * lane)), per = 1.f / P;
     auto parts_of = [&](float steps, float P, float per) { return fminf(floorf((steps + P - 1.f) * per), (float)kMaxParts); };
     float parts = 0.f, split = 0.f;
     for (int n = 0; n < a.N; ++n) {
@@ -488,7 +484,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
     // written out, since the compiler's own asks LDS for each
     // piece right before its use.
     constexpr int NK = QW, NV = kBf16 ? 2 * CT : 4 * CT;  // pieces of 32 keys, and of their values
-    constexpr int AHEAD = 6;
+    constexpr int AHEAD = ROWS && ROW == 512 && !kBf16 ? 4 : 6;
     constexpr int EACH = (ALL_LOADS + KG * NK - 1) / (KG * NK);  // loads of the next tile under each of the first steps
     auto work = [&](const char* kt, const Next& next) {
         const char* vt = kt + S::TILE;
@@ -922,31 +918,51 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
         if (a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
     };
     if constexpr (ROWS) {
-        if (!mine) return;
+        // A lane's outputs are four channels of its row at a time: stored like that, every request would carry 16 bytes of
+        // a row.  They go through LDS (each wave has a quarter of it), where 16 bytes are at piece ^ row of theirs.  (7
+        // sequences of 2048 tokens, 40 heads of 128 over 8, window 19: 149 us, 164 straight from the registers.)
+        __syncthreads();  // the tiles have been read
+        if (!active) return;
+        auto store = [&](auto type, float f, auto row_of) {  // outputs times f, as `type`, row r of the wave to row_of(r)
+            using E = decltype(type);
+            constexpr int EB = sizeof(E), CC = D * EB * 32 <= S::TILE ? D : S::TILE / (32 * EB), PIECES = CC * EB / 16;
+            constexpr int MASK = PIECES < 16 ? PIECES - 1 : 15;
+            char* at = s_kv[0] + w * S::TILE;
+#pragma unroll
+            for (int k = 0; k < D / CC; ++k) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int x = 0; x < CC / 8; ++x) {
+                    const int c = (k * CC + 8 * x) / 32, e = x % 4, byte = (8 * x + 4 * hl) * EB;
+                    char* to = at + lr * CC * EB + (((byte >> 4) ^ (lr & MASK)) << 4) + (byte & 15);
+                    const f32x4 y = {o[c][4 * e] * f, o[c][4 * e + 1] * f, o[c][4 * e + 2] * f, o[c][4 * e + 3] * f};
+                    if constexpr (EB == 2) *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+                    else *reinterpret_cast<f32x4*>(to) = y;
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int x = 0; x < PIECES / 2; ++x) {
+                    const int r = (x * 64 + lane) / PIECES, piece = (x * 64 + lane) % PIECES;
+                    E* to = row_of(r);
+                    if (r < wave_rows)
+                        *reinterpret_cast<u32x4*>(to + k * CC + piece * (16 / EB)) =
+                            *reinterpret_cast<const u32x4*>(at + r * CC * EB + ((piece ^ (r & MASK)) << 4));
+                }
+            }
+        };
         if (parts > 1) {
-            const int64_t at = (h * places_of(plan.groups) + item.split + item.part) * RT + my;
-            if (hl == 0) ws.ml[at] = make_float2(base, l);
-            float* to = ws.out + at * D;
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<f32x4*>(to + c * 32 + 8 * e + 4 * hl) =
-                        f32x4{o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]};
+            const int64_t at = (h * places_of(plan.groups) + item.split + item.part) * RT;
+            if (mine && hl == 0) ws.ml[at + my] = make_float2(base, l);
+            store(0.f, 1.f, [&](int r) { return ws.out + (at + wave_first + r) * D; });
             return;
         }
-        if (hl == 0) finish(base, l, out_row);
-        const float f = l == 0.f ? 0.f : 1.f / l;
-        T* to = static_cast<T*>(a.o) + out_row * D;
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f32x4 y = {o[c][4 * e] * f, o[c][4 * e + 1] * f, o[c][4 * e + 2] * f, o[c][4 * e + 3] * f};
-                T* at = to + c * 32 + 8 * e + 4 * hl;
-                if constexpr (kBf16) *reinterpret_cast<u32x2*>(at) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-                else *reinterpret_cast<f32x4*>(at) = y;
-            }
+        if (mine && hl == 0) finish(base, l, out_row);
+        store(T(), l == 0.f ? 0.f : 1.f / l, [&](int r) {
+            const uint32_t lo = __shfl((uint32_t)out_row, r, 64), hi = __shfl((uint32_t)(out_row >> 32), r, 64);
+            return static_cast<T*>(a.o) + (int64_t)((uint64_t)hi << 32 | lo) * D;
+        });
     } else {
         // join the waves: their sums go where the tiles were, four channels c of row r at place c / 4 ^ r % 8 of its row
         static_assert(32 * D * 4 <= 2 * S::TILE, "a wave's outputs fit its buffer");
@@ -1072,16 +1088,36 @@ Sizes sizes_of(const PagedPrefillArgs& a) {
     return {32, 32, row <= 256 ? 4 : row == 512 ? 2 : 1, false};
 }
 
+// us of a workgroup's step alone on its CU, about.
+float step_time(const PagedPrefillArgs& a) {
+    return a.bf16 ? (many_rows(a) ? (a.d == 64 ? 0.7f : 1.1f) : a.d == 256 ? 0.9f : 0.4f) : a.d * (1.9f / 64);
+}
+
+// What is split.  Few rows: two shortest parts and more, and no more than several rounds of workgroups.  Many rows: where
+// the longest row tile takes longer than its share, which runs next to another, and than the parts' results and the join
+// (5 us) together.  32 heads of 128 over 8, in bf16, us split and not: 33 tokens after 1000 (16 tiles, 17 steps) 19 and 28;
+// 300 after 1500 (80, 29) 32 and 39; 512 after 1500 (136, 32) 39 and 43; 600 after 600 (152, 19) 38 and 32; 900 after 1500
+// (232, 38) 56 and 50; 2048 (520, 33) 78 and 55.  fp32 steps take so long that uneven lengths are worth it up to a round of
+// workgroups: 40 sequences of 8 to 344 tokens after 1326 to 3978, 4 heads of 128 (284, 136), 316 and 721.
 PrefillPlan plan_of(const PagedPrefillArgs& a) {
     PrefillPlan p{};
     const Sizes z = sizes_of(a);
     p.slots = a.T * (a.Hq / a.Hkv) / z.rt + a.N;
-    const int64_t steps = steps_to(a, a.max_length, z.rt, z.bn, z.step);
-    if (!worth_splitting(z.rows, p.slots * a.Hkv, steps)) return p;
-    p.groups = (int)div_up(kGroups, a.Hkv);
+    const int64_t steps = steps_to(a, a.max_length, z.rt, z.bn, z.step), tiles = p.slots * a.Hkv;
+    const float t = step_time(a), out = 1.6e-6f * z.rt * a.d;  // us of a part's outputs, written and read at 5 TB/s
+    p.least = t < 1.5f ? 4 : t < 2.5f ? 2 : 1;
+    if (z.rows) {
+        const float parts = fminf((float)kGroups, (float)tiles * steps / p.least);
+        float saved = tiles <= 256 ? t * steps * (1.f - 0.85f / 256 * tiles) : 0.f;
+        if (!a.bf16 && tiles > 256 && tiles <= kGroups) saved = 0.2f * t * steps;
+        if (saved < 5.f + parts * out) return p;
+    } else if (tiles > 2048 || steps < 2 * p.least) {
+        return p;
+    }
+    p.groups = (int)div_up(z.rows && a.d == 256 ? kGroups / 2 : kGroups, a.Hkv);
     if (a.N > 64) {
         int64_t parts = p.groups / p.slots;
-        parts = parts < steps / kLeast ? parts : steps / kLeast;
+        parts = parts < steps / p.least ? parts : steps / p.least;
         p.parts = (int)(parts < kMaxParts ? parts : kMaxParts);
         if (p.parts < 2) p.parts = p.groups = 0;
         else p.steps = (int)div_up(steps, p.parts);
@@ -1091,7 +1127,6 @@ PrefillPlan plan_of(const PagedPrefillArgs& a) {
 int64_t items_of(const PrefillPlan& p) {
     return p.parts ? p.slots * p.parts : p.slots + (p.groups ? places_of(p.groups) : 0);
 }
-
 int64_t part_rows(const PagedPrefillArgs& a, const PrefillPlan& p) { return a.Hkv * places_of(p.groups) * sizes_of(a).rt; }
 size_t part_bytes(const PrefillPlan& p) { return (size_t)(places_of(p.groups) * 16 + 256); }
 
