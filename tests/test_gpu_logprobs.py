@@ -313,3 +313,30 @@ def test_gradient_of_the_formula_and_of_differences():
     exact = float((g.double() * v.double()).sum())
     # each value is off by about 100 u of its terms (below 4 * 3 * 8), and a third derivative below 20 |v|^3
     assert abs(slope - exact) <= 100 * U * 96 / step + 20 * step * step * float(v.abs().max()) ** 3
+
+
+@pytest.mark.parametrize("dtype,R", [(BF16, 4200), (F32, 2100)])
+def test_logits_of_more_than_the_caches_hold(dtype, R):
+    """Such calls pass the caches by: rows give what they give alone (where they are split: within the sums' bounds)."""
+    V = 32768
+    x = torch.zeros(R, V, dtype=dtype, device=DEV)
+    x[-3:] = rows(3, V, dtype, seed=5)
+    x[7] = x[-1]
+    tokens = torch.arange(R, dtype=torch.int32, device=DEV) * 3
+    d = torch.ones(R, device=DEV)
+    for top, entropy in ((0, False), (0, True), (3, False), (3, True)):
+        print(f"large {dtype} top={top} entropy={entropy}", flush=True)
+        got = kda.token_logprobs(x, tokens, top=top, entropy=entropy)
+        lp, lse, h, best, which, s, s2 = plain64(x[-3:], tokens[-3:], top)
+        tol = U * (4 * s2 + (V / 1024 + 70) * (1 + s) + 8 * lse.abs())
+        for a, b in zip(got[:3], (lp, lse, h)):
+            if a is not None:
+                assert bool(((a[-3:].cpu().double() - b).abs() <= tol + U * b.abs()).all())
+        assert float(got[1][7]) == float(got[1][-1]) and abs(float(got[1][0]) - math.log(V)) <= 1e-5
+        if top:
+            assert torch.equal(got[4][-3:].cpu().long(), which) and got[4][0].tolist() == [0, 1, 2]
+        lse, h = got[1], got[2]
+        grad = kda.token_logprobs_grad(x, tokens, lse, d, entropy=h, d_entropy=d if entropy else None)
+        alone = kda.token_logprobs_grad(x[-3:].clone(), tokens[-3:].clone(), lse[-3:].clone(), d[-3:].clone(),
+                                        entropy=None if h is None else h[-3:].clone(), d_entropy=d[-3:].clone() if entropy else None)
+        assert torch.equal(grad[-3:].contiguous().view(torch.uint8), alone.view(torch.uint8))

@@ -345,3 +345,19 @@ def test_paged_prefill_of_a_long_chunk_behind_short_ones(dtype):
     new = [3, 120, 1, 40]
     cache = Cache([9, 5000, 30, 700], 3, 64, 16, dtype, seed=91)
     check(cache, queries(sum(new), 6, 64, dtype, scale=1.0), new)
+
+
+@pytest.mark.parametrize("dtype,d,n,m,past", [
+    (BF16, 64, 70, 20, 2500), (F32, 64, 70, 20, 1300), (BF16, 256, 66, 20, 1500),   # shares by the bound of the lengths
+    (F32, 64, 40, 190, 1100), (F32, 128, 33, 250, 700),                             # a round of row tiles, uneven lengths
+    (BF16, 256, 3, 30, 2500), (F32, 256, 3, 30, 900)])
+def test_paged_prefill_of_many_rows_is_split_and_joined(dtype, d, n, m, past):
+    hkv = 4 if n in (33, 40) else 1
+    new = [m + i % 3 for i in range(n)]
+    cache = Cache([a + past * (1 + i % 4) // 4 for i, a in enumerate(new)], hkv, d, 32, dtype, seed=n + d)
+    group = 1 if hkv == 4 else 2
+    need = kda._lib.load().kda_paged_prefill_workspace(n, sum(new), hkv * group, hkv, d, int(dtype == BF16),
+                                                       max(cache.lengths), 0, 0)
+    assert need > 0
+    print(f"many rows {dtype} d={d} n={n}", flush=True)
+    check(cache, queries(sum(new), hkv * group, d, dtype, scale=1.0), new, max_length=max(cache.lengths))
