@@ -361,3 +361,29 @@ def test_paged_prefill_of_many_rows_is_split_and_joined(dtype, d, n, m, past):
     assert need > 0
     print(f"many rows {dtype} d={d} n={n}", flush=True)
     check(cache, queries(sum(new), hkv * group, d, dtype, scale=1.0), new, max_length=max(cache.lengths))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("new", [[4], [140]])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_paged_prefill_visible_values_that_are_not_finite_in_wide_heads(dtype, d, new, bad):
+    """In each block of channels, in tiles with hidden keys and without: they reach the rows that see them, and no other
+    row or channel.  (Rows whose sums are not finite are formed again with another reference, so that the others are within
+    the bound of the exact ones, not bit for bit what they are without.)"""
+    cache = Cache([400], 1, d, 16, dtype, seed=13)
+    q = queries(sum(new), 2, d, dtype, scale=0.2)
+    exact, _, tol, _ = attention64(cache.k[0], cache.v[0], q.cpu(), 400 - new[0], d ** -0.5)
+    tol = tol + STEP[dtype] * (exact.abs() + tol)
+    for i in (3, 400 - new[0], 399):
+        vp = cache.vp.clone()
+        channels = [5, 63, d - 40, d - 1]
+        for c in channels:
+            vp[int(cache.table_cpu[0, i // 16]), 0, i % 16, c] = bad
+        out = kda.paged_prefill(q, cache.kp, vp, cache.table, cache.len, cu_of(new)).cpu().double()
+        sees = torch.arange(400 - new[0], 400) >= i
+        mask = torch.zeros(d, dtype=torch.bool)
+        mask[channels] = True
+        want = (sees[:, None, None] & mask).expand(-1, 2, -1)
+        assert torch.equal(~out.isfinite(), want), i
+        assert bool(((out - exact).abs() <= tol)[~want].all()), i
