@@ -563,6 +563,23 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
         }
     };
 
+    // What this lane's row sees of a tile that begins at token `base`: places first .. first + many - 1, and the sinks' 0 ..
+    // more - 1, for this lane's half, but for the pieces that are gone.
+    struct Seen {
+        int top, first, many, less, more, gone;  // no place from `top` on
+        __device__ __forceinline__ bool operator()(int kg, int i) const {
+            const int at = kg * 32 + 8 * (i >> 2) + (i & 3);
+            return (((uint32_t)(first + at) < (uint32_t)many) | ((uint32_t)(less + at) < (uint32_t)more)) &
+                   !((gone >> (at / kPage)) & 1);
+        }
+    };
+    auto seen_from = [&](int base, int lo, int hi, int gone) {
+        const int top = (hi - 1 < p ? hi - 1 : p) - base + 1;
+        const int from = (lo > p_near ? lo : p_near) - base, many = top > from ? top - from : 0;
+        const int sink = (a.sinks < base + top ? a.sinks : base + top) - lo, more = sink > 0 ? sink : 0;
+        return Seen{top, 4 * hl - from, many, 4 * hl - (lo - base), more, gone};
+    };
+
     // One tile of which some key is not visible to some row (`hidden`), or where some row has no reference yet.
     auto work_edge = [&](const char* kt, int base, int lo, int hi, int gone, bool hidden, const Next& next) {
         const char* vt = kt + S::TILE;
@@ -596,26 +613,18 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
             load_some(next, 0, ALL_LOADS / 2);
         }
         if (hidden) {
-            // visible: places first .. first + many - 1 of the tile, and the sinks' 0 .. more - 1, for this lane's half
-            const int top = (hi - 1 < p ? hi - 1 : p) - base + 1;  // places below it
-            const int from = (lo > p_near ? lo : p_near) - base, many = top > from ? top - from : 0;
-            const int sink = (a.sinks < base + top ? a.sinks : base + top) - lo, more = sink > 0 ? sink : 0;
-            const int first = 4 * hl - from, less = 4 * hl - (lo - base);
+            const auto seen = seen_from(base, lo, hi, gone);
             if (a.window == 0 && gone == 0) {  // (from and lo are 0 or before the tile)
 #pragma unroll
                 for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        x[kg][i] = kg * 32 + 8 * (i >> 2) + (i & 3) < top - 4 * hl ? x[kg][i] : -INFINITY;
+                        x[kg][i] = kg * 32 + 8 * (i >> 2) + (i & 3) < seen.top - 4 * hl ? x[kg][i] : -INFINITY;
             } else {
 #pragma unroll
                 for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int at = kg * 32 + 8 * (i >> 2) + (i & 3);
-                        const bool on = ((uint32_t)(first + at) < (uint32_t)many) | ((uint32_t)(less + at) < (uint32_t)more);
-                        x[kg][i] = (on & !((gone >> (at / kPage)) & 1)) ? x[kg][i] : -INFINITY;
-                    }
+                    for (int i = 0; i < 16; ++i) x[kg][i] = seen(kg, i) ? x[kg][i] : -INFINITY;
             }
         }
         if (pass == 1 || __any(m == -INFINITY)) {
@@ -723,7 +732,8 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
             if (j + AHEAD < KG * NV) ring[j % AHEAD] = val(j + AHEAD);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (odd) {  // how many such values each sum has a weight for
+        if (odd) {  // how many such values each row sees: a weight of 0 makes NaN of them too, as it does in other tiles
+            const auto seen = seen_from(base, lo, hi, gone);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 f32x16 count = zeros();
@@ -735,11 +745,8 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
                             u32x4 v = value(vt, c, kg, st), y;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint32_t z = pf[kg][4 * st + i];
                                 v[i] = odd_bits(v[i]) & 0x3F803F80u;
-                                // 1 for a weight that is not 0 (no weight is negative, and the least one is 2^-133)
-                                const uint32_t s = ((z & 0x7FFF7FFFu) + 0x7FFF7FFFu) & 0x80008000u;
-                                y[i] = ((s << 1) - (s >> 15)) & 0x3F803F80u;
+                                y[i] = (seen(kg, 8 * st + 2 * i) ? 0x3F80u : 0u) | (seen(kg, 8 * st + 2 * i + 1) ? 0x3F800000u : 0u);
                             }
                             count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                                 __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, y), count, 0, 0, 0);
@@ -748,7 +755,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             count = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                                fabsf(value32(vt, c, kg, i)) < INFINITY ? 0.f : 1.f, x[kg][i] != 0.f ? 1.f : 0.f, count,
+                                fabsf(value32(vt, c, kg, i)) < INFINITY ? 0.f : 1.f, seen(kg, i) ? 1.f : 0.f, count,
                                 0, 0, 0);
                     }
                 }

@@ -613,10 +613,10 @@ int kda_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_
  *              to no sequence are left as they were.
  * A query without a visible token (or whose every visible score is -inf) gives out = 0 and lse = -inf.  Tokens that a
  * query does not see never change its result, whatever bits their slots hold; a visible key or value that is not finite
- * makes what it enters not finite, but for a weight of 0.  Products are exact in bf16 with fp32 sums.  With KDA_BF16
- * and T_total * H_q / H_kv > 32 N (many new tokens) the softmax weights are rounded to bf16 for their product with the
- * values (their sum is not), which adds to the output's own rounding about as much again; with fewer they are two bf16
- * each.
+ * makes what it enters not finite, but for a key with a score of -inf, which has weight 0.  Products are exact in
+ * bf16 with fp32 sums.  With KDA_BF16 and T_total * H_q / H_kv > 32 N (many new tokens) the softmax weights are rounded
+ * to bf16 for their product with the values (their sum is not), which adds to the output's own rounding about as much
+ * again; with fewer they are two bf16 each.
  * workspace: kda_paged_prefill_workspace bytes for the same arguments, 256-byte aligned, overlapping no argument; holds
  * the partial results where the keys of some rows are split over several workgroups.  Needs no initialisation.  How they
  * are split goes by the lengths of all sequences, so that a sequence's last bits may depend on the others' lengths.

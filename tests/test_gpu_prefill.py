@@ -387,3 +387,30 @@ def test_paged_prefill_visible_values_that_are_not_finite_in_wide_heads(dtype, d
         want = (sees[:, None, None] & mask).expand(-1, 2, -1)
         assert torch.equal(~out.isfinite(), want), i
         assert bool(((out - exact).abs() <= tol)[~want].all()), i
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [[4], [140]])
+@pytest.mark.parametrize("key", [-math.inf, -8192.0])
+def test_paged_prefill_values_that_are_not_finite_with_a_weight_of_0(dtype, d, new, key):
+    """A score of -inf, or one so low that its weight is 0 in fp32: the value's product with it is NaN, in tiles with hidden
+    keys and without, as in the one-token attention; no other row or channel changes, nor a log-sum."""
+    m = new[0]
+    cache = Cache([400], 1, d, 16, dtype, seed=15)
+    q = torch.full((m, 2, d), 0.0625, dtype=dtype, device=DEV)
+    for i in (3, 70, 400 - m, 399):
+        kp, vp = cache.kp.clone(), cache.vp.clone()
+        at = (int(cache.table_cpu[0, i // 16]), 0, i % 16)
+        kp[at] = key  # a score of -512 d / sqrt(d): below -4096
+        clean = kda.paged_prefill(q, kp, vp, cache.table, cache.len, cu_of(new), lse=True)
+        assert bool(clean[0].isfinite().all()) and bool(clean[1].isfinite().all())
+        for bad in (math.inf, math.nan):
+            vp[at][d - 17] = bad
+            out, lse = kda.paged_prefill(q, kp, vp, cache.table, cache.len, cu_of(new), lse=True)
+            want = (torch.arange(400 - m, 400) >= i)[:, None].expand(-1, 2)
+            assert torch.equal(out[..., d - 17].isnan().cpu(), want), (i, bad)
+            out[..., d - 17], clean[0][..., d - 17] = 0.0, 0.0
+            assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
+            one = kda.paged_decode(q[-1:], kp, vp, cache.table, cache.len)
+            assert bool(one[..., d - 17].isnan().all())
