@@ -1007,7 +1007,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
             f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < WAVES; ++i) {
-                L += top == -INFINITY ? 0.f : s_l[i][r] * exp2_hw(s_m[i][r] - top);
+                L += s_l[i][r] * (s_m[i][r] == -INFINITY ? 0.f : exp2_hw(s_m[i][r] - top));  // (NaN without a reference stays)
                 y += *place(i, r, c);
             }
             if (parts > 1) {

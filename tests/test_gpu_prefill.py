@@ -414,3 +414,21 @@ def test_paged_prefill_values_that_are_not_finite_with_a_weight_of_0(dtype, d, n
             assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
             one = kda.paged_decode(q[-1:], kp, vp, cache.table, cache.len)
             assert bool(one[..., d - 17].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new,length,first,last", [(4, 20, 0, 20), (4, 400, 0, 400), (4, 9000, 1024, 7000), (9, 9000, 0, 9000),
+                                                   (140, 400, 0, 400), (140, 4000, 1024, 3000)])
+def test_paged_prefill_keys_that_are_all_nan(dtype, d, new, length, first, last):
+    """A row that sees nothing but such keys, in all of a sequence or in whole parts of it, has NaN outputs and a NaN
+    log-sum: -inf would say that it sees no key.  The sequence next to it is what it is without."""
+    cache = Cache([length, 50], 1, d, 16, dtype, seed=17)
+    q = queries(new + 2, 2, d, dtype)
+    cu = cu_of([new, 2])
+    clean = kda.paged_prefill(q, cache.kp, cache.vp, cache.table, cache.len, cu, lse=True)
+    for j in range(first // 16, -(-last // 16)):
+        cache.kp[int(cache.table_cpu[0, j])] = math.nan
+    out, lse = kda.paged_prefill(q, cache.kp, cache.vp, cache.table, cache.len, cu, lse=True)
+    assert bool(out[:new].isnan().all()) and bool(lse[:new].isnan().all())
+    assert torch.equal(out[new:], clean[0][new:]) and torch.equal(lse[new:], clean[1][new:])
