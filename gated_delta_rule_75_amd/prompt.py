@@ -170,7 +170,7 @@ def paged_prefill(q, k_pages, v_pages, page_table, lengths, cu_seqlens, *, scale
     v_pages [n_pages,H_kv,page_size,d], page_table int32 [N,P], lengths int32 [N], the new tokens included: the
     last one of sequence n is at position lengths[n] - 1.  A token sees those before it and itself; window > 0:
     of these only the last `window` and the first `sinks`.  scale: 1 / sqrt(d) by default.  max_length: an upper
-    bound of lengths that sizes the launch (P * page_size by default).
+    bound of lengths that sizes the launch (P * page_size by default); tokens behind it are not visible.
     Returns out [T,H_q,d] in q's dtype; with lse=True (or a tensor for it) (out, lse [T,H_q] float32).  A token
     that sees none gives 0 and -inf; rows that belong to no sequence are not written."""
     if serving._M is not None:
@@ -210,7 +210,9 @@ def paged_prefill(q, k_pages, v_pages, page_table, lengths, cu_seqlens, *, scale
     if max_length is not None and max_length < most:
         if max_length < 0:
             raise ValueError("max_length must be >= 0")
-        most = max_length if max_length else 1  # 0 would mean no bound
+        most = max_length
+        if most == 0:
+            P = 0  # the library's 0 is no bound; a table without columns shows nothing
     L = _lib_()
     _run_scratch(L.kda_paged_prefill, di, workspace,
                  (L.kda_paged_prefill_workspace, N, T, Hq, H, d, code, most, window, sinks), q.data_ptr(), qs,

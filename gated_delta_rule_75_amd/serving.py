@@ -206,7 +206,7 @@ def paged_decode(q, k_pages, v_pages, page_table, lengths, *, scale=None, window
     q [N,H_q,d] (float32 or bfloat16; rows of any stride), k_pages, v_pages [n_pages,H_kv,page_size,d],
     page_table int32 [N,P], lengths int32 [N].  scale: 1 / sqrt(d) by default.  window > 0: only the last
     `window` tokens and the first `sinks` are visible.  max_length: an upper bound of lengths that sizes the
-    launch (P * page_size by default).
+    launch (P * page_size by default); a longer sequence is cut there.
     Returns out [N,H_q,d] float32; with lse=True (or a tensor for it) (out, lse [N,H_q] float32).  A sequence
     with no visible token gives 0 and -inf."""
     if _M is not None:
@@ -245,7 +245,9 @@ def paged_decode(q, k_pages, v_pages, page_table, lengths, *, scale=None, window
     if max_length is not None and max_length < most:
         if max_length < 0:
             raise ValueError("max_length must be >= 0")
-        most = max_length if max_length else 1  # 0 would mean no bound
+        most = max_length
+        if most == 0:
+            P = 0  # the library's 0 is no bound; a table without columns shows nothing
     L = _lib_()
     _run_scratch(L.kda_paged_decode, di, workspace,
                  (L.kda_paged_decode_workspace, N, Hq, H, d, code, most, window, sinks), q.data_ptr(), qs,

@@ -432,3 +432,20 @@ def test_paged_prefill_keys_that_are_all_nan(dtype, d, new, length, first, last)
     out, lse = kda.paged_prefill(q, cache.kp, cache.vp, cache.table, cache.len, cu, lse=True)
     assert bool(out[:new].isnan().all()) and bool(lse[:new].isnan().all())
     assert torch.equal(out[new:], clean[0][new:]) and torch.equal(lse[new:], clean[1][new:])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [[2, 1], [70, 40]])
+def test_a_bound_of_0_shows_nothing(dtype, new):
+    """max_length hides what lies behind it: with 0, everything, in the one-token attention too; 1 shows one token."""
+    cache = Cache([200, 90], 2, 256, 16, dtype, seed=19)
+    q = queries(sum(new), 4, 256, dtype)
+    out, lse = kda.paged_prefill(q, cache.kp, cache.vp, cache.table, cache.len, cu_of(new), lse=True, max_length=0)
+    one, lse1 = kda.paged_decode(q[:2], cache.kp, cache.vp, cache.table, cache.len, lse=True, max_length=0)
+    for o, l in ((out, lse), (one, lse1)):
+        assert not o.any() and bool(torch.isneginf(l).all())
+    out = kda.paged_prefill(q, cache.kp, cache.vp, cache.table, cache.len, cu_of(new), max_length=1)
+    # out = fl(fl(w v) fl(1 / w)) with the one weight w = 2^(s - fl(s)) about 1: three roundings to fp32 (3 u of v, which a
+    # rounding to bf16 takes back to v; the weight's own rounding to bf16 is 1, and two bf16 are w but for 2^-17)
+    first = cache.v[0][0].to(DEV).repeat_interleave(2, 0).expand(new[0], 4, 256)
+    assert bool(((out[:new[0]] - first).abs() <= (4 * U * first.abs() if dtype == F32 else 0.0)).all())
