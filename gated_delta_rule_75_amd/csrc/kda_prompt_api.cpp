@@ -171,7 +171,9 @@ size_t kda_paged_prefill_workspace(int32_t N, int64_t T_total, int32_t H_q, int3
         return (size_t)-1;
     kda::PagedPrefillArgs a{};
     a.N = N; a.T = T_total; a.Hq = H_q; a.Hkv = H_kv; a.d = d; a.bf16 = dtype == KDA_BF16;
-    a.window = window; a.sinks = sinks; a.max_length = max_length;
+    a.window = window; a.sinks = sinks;
+    // (0 is no bound, as in the call: what splits a short table's rows, a longer one's splits too, in as many bytes)
+    a.max_length = max_length > 0 ? max_length : kMaxCount - 4096;
     size_t need;
     return kda::paged_prefill_groups(a, &need) > kda::max_groups(256) ? (size_t)-1 : need;
 }

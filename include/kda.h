@@ -629,8 +629,8 @@ int kda_paged_prefill(const void* q, int64_t q_stride, const void* k_pages, cons
                       int32_t window, int32_t sinks, int64_t max_length, void* out, float* lse, void* workspace,
                       size_t workspace_bytes, void* hip_stream);
 
-/* Workspace bytes of kda_paged_prefill, max_length being the smaller of the bound given and
- * table_pages * page_size (not 0 for "no bound" here); (size_t)-1 for an unsupported or invalid combination. */
+/* Workspace bytes of kda_paged_prefill for a bound of max_length (or a table of as many tokens, if that is less); 0, no
+ * bound: enough for a table of any width.  (size_t)-1 for an unsupported or invalid combination. */
 size_t kda_paged_prefill_workspace(int32_t N, int64_t T_total, int32_t H_q, int32_t H_kv, int32_t d, int32_t dtype,
                                    int64_t max_length, int32_t window, int32_t sinks);
 

@@ -322,3 +322,25 @@ def test_rotary_frequencies_refusals(kw):
 
     with pytest.raises(ValueError):
         rotary_frequencies(device="cpu", **kw)
+
+
+@pytest.mark.parametrize("N,T,Hq,Hkv,d", [(1, 4, 8, 4, 128), (2, 10, 8, 2, 128), (1, 300, 8, 2, 256), (70, 3000, 4, 2, 64),
+                                          (40, 9000, 4, 4, 128), (3, 8000, 16, 8, 64), (1, 1, 1, 1, 64), (64, 320, 32, 8, 128),
+                                          (65, 325, 8, 1, 128), (2, 0, 8, 2, 128), (0, 0, 8, 2, 128)])
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 3)])
+def test_workspace_of_paged_prefill_without_a_bound(monkeypatch, N, T, Hq, Hkv, d, dtype, window, sinks):
+    """max_length 0 is no bound there as in the call, so the size serves tables of any width: a call with the same
+    arguments does not ask for more."""
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    need = L.kda_paged_prefill_workspace(N, T, Hq, Hkv, d, dtype, 0, window, sinks)
+    assert need < 1 << 40
+    for width in (0, 1, 2, 3, 7, 64, 65, 300, 8191, 1 << 20, (1 << 27) - 257):
+        for most in {0, 1, 16 * width, 12345}:
+            assert L.kda_paged_prefill_workspace(N, T, Hq, Hkv, d, dtype, max(most, 1), window, sinks) <= need
+            status = _call(L, "kda_paged_prefill", PREFILL, q=1 << 45, out=1 << 46, lse=1 << 47, ws=1 << 48, kp=1 << 49,
+                           vp=1 << 50, table=1 << 51, N=N, T=T, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, q_stride=Hq * d,
+                           kp_stride=16 * Hkv * d, vp_stride=16 * Hkv * d, width=width, stride=max(width, 1), window=window,
+                           sinks=sinks, max_length=most, ws_bytes=need)
+            assert status == _l.KDA_ERR_HIP and b"injected" in L.kda_last_error(), (width, most, L.kda_last_error())
