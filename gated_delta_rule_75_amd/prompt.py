@@ -113,6 +113,8 @@ def rotary(q, k, positions, freqs, *, layout="half", amplitude=1.0, inverse=Fals
         Hk = k.shape[1]
     elif k_out is not None:
         raise ValueError("k_out given without k")
+    if (Hq | Hk | d) >> 31:
+        _int32(H_q=Hq, H_k=Hk, d=d)
     _vector(positions, "positions", _I32, (T,), di)
     lay, r = _turn(freqs, layout, di, d)
     q_out, qos = _turned(q_out, "q_out", q, di)
@@ -149,6 +151,8 @@ def rotary_append(q, k, v, k_pages, v_pages, page_table, start, freqs, *, cu_seq
                          f"v_pages {tuple(v_pages.shape)} do not go together")
     ts = _row(page_table, "page_table", _I32, 2, di)
     N, P = page_table.shape
+    if (N | P | Hq | H | d | n_pages | page_size) >> 31:
+        _int32(N=N, P=P, H_q=Hq, H_kv=H, d=d, n_pages=n_pages, page_size=page_size)
     _vector(start, "start", _I32, (N,), di)
     cu = None
     if cu_seqlens is not None:
@@ -191,6 +195,8 @@ def paged_prefill(q, k_pages, v_pages, page_table, lengths, cu_seqlens, *, scale
     if v_pages.shape != pages or dp != d:
         raise ValueError(f"q {tuple(shape)}, k_pages {tuple(pages)} and v_pages {tuple(v_pages.shape)} do not go "
                          "together")
+    if (N | P | Hq | H | d | n_pages | page_size) >> 31:
+        _int32(N=N, P=P, H_q=Hq, H_kv=H, d=d, n_pages=n_pages, page_size=page_size)
     _vector(lengths, "lengths", _I32, (N,), di)
     _vector(cu_seqlens, "cu_seqlens", _I32, (N + 1,), di)
     dev = q.device
@@ -246,6 +252,8 @@ def token_logprobs(logits, tokens, *, top=0, entropy=False, workspace=None):
     code, di = _lead(logits, "logits")
     stride = _row(logits, "logits", logits.dtype, 2, di)
     R, V = logits.shape
+    if V >> 31:
+        _int32(V=V)
     if top < 0 or top > V:
         raise ValueError(f"top must be in 0 .. V, got {top}")
     dev = logits.device
@@ -274,6 +282,8 @@ def token_logprobs_grad(logits, tokens, lse, d_logprobs=None, *, d_lse=None, ent
     code, di = _lead(logits, "logits")
     stride = _row(logits, "logits", logits.dtype, 2, di)
     R, V = logits.shape
+    if V >> 31:
+        _int32(V=V)
     _vector(lse, "lse", _F32, (R,), di)
     if d_logprobs is not None and tokens is None:
         raise ValueError("d_logprobs needs tokens")

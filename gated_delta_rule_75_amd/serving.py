@@ -189,6 +189,8 @@ def cache_append(k, v, k_pages, v_pages, page_table, start, *, cu_seqlens=None):
                          f"{tuple(v_pages.shape)} do not go together")
     ts = _row(page_table, "page_table", _I32, 2, di)
     N, P = page_table.shape
+    if (N | P | H | d | n_pages | page_size) >> 31:
+        _int32(N=N, P=P, H_kv=H, d=d, n_pages=n_pages, page_size=page_size)
     _vector(start, "start", _I32, (N,), di)
     cu = None
     if cu_seqlens is not None:
@@ -227,6 +229,8 @@ def paged_decode(q, k_pages, v_pages, page_table, lengths, *, scale=None, window
     if v_pages.shape != pages or dp != d or rows != N:
         raise ValueError(f"q {tuple(shape)}, k_pages {tuple(pages)}, v_pages {tuple(v_pages.shape)} and page_table "
                          f"{(rows, P)} do not go together")
+    if (N | P | Hq | H | d | n_pages | page_size) >> 31:
+        _int32(N=N, P=P, H_q=Hq, H_kv=H, d=d, n_pages=n_pages, page_size=page_size)
     _vector(lengths, "lengths", _I32, (N,), di)
     dev = q.device
     if out is None:
@@ -273,6 +277,8 @@ def cache_fork(page_table, lengths, refcount, parents, *, table_out=None, length
     _vector(refcount, "refcount", _I32, None, di)
     _vector(parents, "parents", _I32, None, di)
     N_out = parents.shape[0]
+    if (N | P | N_out | refcount.shape[0]) >> 31:
+        _int32(N=N, P=P, N_out=N_out, n_pages=refcount.shape[0])
     dev = page_table.device
     if table_out is None:
         table_out = _EMPTY((N_out, P), dtype=_I32, device=dev)
@@ -302,6 +308,8 @@ def cache_free(page_table, lengths, refcount, rows):
     _vector(lengths, "lengths", _I32, (N,), di)
     _vector(refcount, "refcount", _I32, None, di)
     _vector(rows, "rows", _I32, None, di)
+    if (N | P | rows.shape[0] | refcount.shape[0]) >> 31:
+        _int32(N=N, P=P, rows=rows.shape[0], n_pages=refcount.shape[0])
     _run(_lib_().kda_cache_free, di, page_table.data_ptr(), ts, lengths.data_ptr(), N, P, refcount.data_ptr(),
          refcount.shape[0], rows.data_ptr(), rows.shape[0])
 
@@ -324,6 +332,8 @@ def cache_reserve(page_table, lengths, refcount, new_tokens, page_size, *, copie
     _vector(lengths, "lengths", _I32, (N,), di)
     _vector(refcount, "refcount", _I32, None, di)
     _vector(new_tokens, "new_tokens", _I32, (N,), di)
+    if (N | P | refcount.shape[0]) >> 31:
+        _int32(N=N, P=P, n_pages=refcount.shape[0])
     dev = page_table.device
     if copies is None:
         copies = _EMPTY((N, 2), dtype=_I32, device=dev)
@@ -353,6 +363,8 @@ def cache_compact(page_table, refcount, *, table_out=None, refcount_out=None, mo
     N, P = page_table.shape
     _vector(refcount, "refcount", _I32, None, di)
     n_pages = refcount.shape[0]
+    if (N | P | n_pages) >> 31:
+        _int32(N=N, P=P, n_pages=n_pages)
     dev = page_table.device
     if table_out is None:
         table_out = _EMPTY((N, P), dtype=_I32, device=dev)
@@ -411,6 +423,8 @@ def pages_copy(pools, pairs):
         base.append(t.data_ptr())
         size.append(row)
         stride.append(row if t.is_contiguous() else _rows(t, f"pools[{i}]", t.shape) * es)
+    if n_pages >> 31:
+        _int32(n_pages=n_pages)
     _run(_lib_().kda_pages_copy, di, (ctypes.c_void_p * n)(*base), (ctypes.c_int64 * n)(*stride),
          (ctypes.c_int64 * n)(*size), n, n_pages, pairs.data_ptr(), pairs.shape[0])
 
@@ -431,6 +445,8 @@ def beam_select(logits, scores, *, n_out=None, finished=None, eos=-1, workspace=
     if logits.dim() != 3:
         raise ValueError(f"logits must have 3 axes, got {logits.dim()}")
     B, K, V = logits.shape
+    if (B | K | V) >> 31:
+        _int32(B=B, K=K, V=V)
     if logits.is_contiguous():
         row = V
     else:
@@ -485,6 +501,8 @@ def beam_reorder(states, parents):
         _gpu(parents, "parents", _I32, 2, di)
         _check(parents, "parents", _I32)
     B, K = parents.shape
+    if (B | K) >> 31:
+        _int32(B=B, K=K)
     rows = B * K
     base, size = [], []
     for i, t in enumerate(states):

@@ -437,3 +437,42 @@ def test_rows_beyond_32_bits():
     want = kda.token_logprobs_grad(x[-2:].clone(), tokens[-2:].clone(), got[1][-2:].clone(), d_lp[-2:].clone())
     kda.token_logprobs_grad(x, tokens, got[1], d_lp, out=x)
     assert torch.equal(bits(x[-2:]), bits(want)) and float(x[5, 5]) == 1.0 and float(x[5, 6]) == -2.0 ** -17
+
+
+def test_sizes_that_32_bits_do_not_hold_are_refused():
+    """They would reach the library cut to their lower bits (2^32 + 5 logits as 5).  No tensor here has an element, so
+    that none of these calls has anything to launch."""
+    big = 2 ** 32
+
+    def f(*shape, dtype=F32):
+        return torch.empty(*shape, dtype=dtype, device=DEV)
+
+    def i(*shape):
+        return f(*shape, dtype=torch.int32)
+
+    freqs, none, pages = kda.rotary_frequencies(64), i(0), f(2, 1, 16, 64)
+    cu = i32([0])
+    calls = [
+        ("V", lambda: kda.token_logprobs(f(0, big + 5), none, top=3)),
+        ("V", lambda: kda.token_logprobs_grad(f(0, big + 5, dtype=BF16), none, f(0), f(0))),
+        ("H_q", lambda: kda.rotary(f(0, big + 8, 64), None, none, freqs)),
+        ("H_k", lambda: kda.rotary(f(0, 8, 64), f(0, big + 1, 64), none, freqs)),
+        ("d", lambda: kda.rotary(f(0, 8, big + 64), None, none, freqs)),
+        ("H_q", lambda: kda.rotary_append(f(0, big + 8, 64), f(0, 1, 64), f(0, 1, 64), pages, pages.clone(), i(0, 4), none, freqs)),
+        ("P", lambda: kda.rotary_append(f(0, 8, 64), f(0, 1, 64), f(0, 1, 64), pages, pages.clone(), i(0, big + 4), none, freqs)),
+        ("H_q", lambda: kda.paged_prefill(f(0, big + 8, 64), pages, pages, i(0, 4), none, cu)),
+        ("P", lambda: kda.paged_prefill(f(0, 8, 64), pages, pages, i(0, big + 4), none, cu)),
+        ("H_q", lambda: kda.paged_decode(f(0, big + 8, 64), pages, pages, i(0, 4), none)),
+        ("P", lambda: kda.cache_append(f(0, 1, 64), f(0, 1, 64), pages, pages.clone(), i(0, big + 4), none)),
+        ("P", lambda: kda.cache_fork(i(0, big + 4), none, i(3), none)),
+        ("P", lambda: kda.cache_free(i(0, big + 4), none, i(3), none)),
+        ("P", lambda: kda.cache_reserve(i(0, big + 4), none, i(3), none, 16)),
+        ("P", lambda: kda.cache_compact(i(0, big + 4), i(3))),
+        ("n_pages", lambda: kda.pages_copy(f(big + 2, 0), i(0, 2))),
+        ("V", lambda: kda.beam_select(f(0, 2, big + 5), f(0, 2))),
+        ("K", lambda: kda.beam_reorder(f(0, 4), i(0, big + 2))),
+    ]
+    for at, (name, call) in enumerate(calls):
+        print(f"call {at}: {name}", flush=True)
+        with pytest.raises(ValueError, match=f"{name} must be a 32-bit whole number"):
+            call()
