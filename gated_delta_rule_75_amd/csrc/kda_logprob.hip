@@ -14,17 +14,21 @@
 //  * Best alternatives: the n-th largest of the maxima so far of 64 disjoint groups of threads is a lower bound of the
 //    n-th best logit; its upper 16 bits are found by 16 counts over a wave.  It is taken again in rounds 0, 1, 2, 4,
 //    8, ..., since it moves less and less; the logits at or above it are collected into lists, those below the last
-//    bound taken out, and the rest ranked by (value, token) at the end.  Where a list overflows (a long stretch of equal
-//    logits, such as a mask of a finite value, before better ones), the row is read once more with the last bound,
-//    and where that overflows too, once for each place.  (2048 rows of 50257 in bf16: 20 best with the entropy 58 us,
-//    115 with the least of the maxima of 32 groups as the bound, which lets five times as many logits pass; 5 best 53,
-//    none 43.)
+//    bound taken out, and the rest ranked by (value, token) at the end.  Lists that are too long to rank, or overflow,
+//    are made again with the bound in all its bits, the latter from the row once more: a long stretch of equal logits
+//    before better ones (a mask of a finite value), and fp32 logits whose offset is large against their spread (of 100 +-
+//    0.1 half of a row is at or above the 100.0 of the upper bits; 2048 rows of 50257 of them, 20 best: 136 us, others
+//    71, 1377 without those bits).  Where that overflows too (equal logits at the bound), the row is read once for each
+//    place (all equal, 20 best: 1360 us).  (2048 rows of 50257 in bf16: 20 best with the entropy 58 us, 115 with the
+//    least of the maxima of 32 groups as the bound, which lets five times as many logits pass; 5 best 53, none 43.)
 //  * A row belongs to one wave where it is short, to a workgroup where it is not, and to several workgroups where
 //    there are few rows; a second launch joins their parts.
 //  * Logits and gradients of more than the 256 MB of the memory's own cache pass the caches by: 4096 rows of 131072 in
 //    bf16, 188 us, 5.7 TB/s (196 without); their gradient 340 us, 6.3 TB/s (373).  Less of them stays there from
 //    the product before: 2048 rows of 50257, 205 MB, 41 us, past the caches 44.
 #include <math.h>
+
+#include <type_traits>
 
 #include "kda_device.h"
 #include "kda_internal.h"
@@ -41,6 +45,8 @@ constexpr int kPer = 16;       // logits of a thread per round
 constexpr int kList = 512;     // collected keys of a wave (the best 64 of one round come with 270 on average, 6 rows of
                                // 3315 logits took 131 us with lists of 256, 68 now)
 constexpr int kMaxParts = 64;
+template <int N>
+using Bits = std::integral_constant<int, N>;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453;
 
@@ -248,7 +254,8 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
     Sums<ENT> sum;
     float most = -INFINITY, bar = -INFINITY;  // this thread's maximum, the row's bound
     int mine = 0, turns = 0;                  // keys this wave has collected
-    auto raise = [&] {  // the n-th largest of the maxima of 64 groups of threads, by its upper 16 bits
+    auto raise = [&](auto bits) {  // the n-th largest of the maxima of 64 groups of threads, by its upper bits
+        constexpr int BITS = decltype(bits)::value, LOW = 32 - BITS;
         float g = most;
         if constexpr (WPR == 4) {
             g = max_min_step<0>(g, 2);
@@ -258,14 +265,14 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
             __syncthreads();
             g = s_g[turn][lane];
         }
-        const uint32_t u = ordered(g) >> 16;
+        const uint32_t u = ordered(g) >> LOW;
         uint32_t least = 0;
 #pragma unroll
-        for (int bit = 15; bit >= 0; --bit) {
+        for (int bit = BITS - 1; bit >= 0; --bit) {
             const uint32_t more = least | 1u << bit;
             least = __popcll(__ballot(u >= more)) >= a.top ? more : least;
         }
-        bar = least << 16 > ordered(-INFINITY) ? unordered(least << 16) : -INFINITY;
+        bar = least << LOW > ordered(-INFINITY) ? unordered(least << LOW) : -INFINITY;
     };
     auto collect = [&](const float (&x)[kPer], float top, int base, bool wide) {
         const float least = bar == -INFINITY ? -3.402823466e38f : bar;  // -inf is not collected
@@ -320,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
         if constexpr (TOP) {
             most = fmaxf(most, top);
             if ((round & (round - 1)) == 0) {
-                raise();
+                raise(Bits<16>());
                 if (mine > kList / 2) filter();
             }
             collect(x, top, base, wide);
@@ -358,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
         lse = finish<T>(a, row, p);
     }
     if constexpr (!TOP) return;
-    raise();
+    raise(Bits<16>());
     filter();
 
     // the row's best, in order
@@ -381,12 +388,18 @@ __global__ __launch_bounds__(kThreads) void logprob_scan_kernel(LogprobArgs a, L
     };
     int total;
     bool full = counts(total);
-    if (full) {  // once more with the last bound
-        mine = 0;
-        for (int base = begin; base < last; base += R::SIZE) {
-            float x[kPer];
-            R::cut(x0, base, first, last, t, x);
-            collect(x, top_of(x), base, false);
+    // Too many: those at or above the bound in all its bits (bf16 has no others), of the lists or of the row once more.
+    if (full || (sizeof(T) == 4 && total > kList)) {
+        raise(Bits<8 * sizeof(T)>());
+        if (full) {
+            mine = 0;
+            for (int base = begin; base < last; base += R::SIZE) {
+                float x[kPer];
+                R::cut(x0, base, first, last, t, x);
+                collect(x, top_of(x), base, false);
+            }
+        } else {
+            filter();
         }
         full = counts(total);
     }
