@@ -436,7 +436,7 @@ int append_impl(const void* q, const void* k, const void* v, const float* g, con
     const Span snp{op.snaps, (size_t)H * d_k * d_v * 4};
     const Span ins[] = {{q, tokens * H * d_k * esz}, {k, tokens * H * d_k * esz}, {v, tokens * H * d_v * esz},
                         {g, tokens * H * (op.gate_head ? 1 : d_k) * 4}, {beta, tokens * H * esz},
-                        {cu_seqlens, (size_t)(N + 1) * 4}, {op.snap_cu, op.snap_cu ? (size_t)(N + 1) * 4 : 0}, sin};
+                        {cu_seqlens, ((size_t)N + 1) * 4}, {op.snap_cu, op.snap_cu ? ((size_t)N + 1) * 4 : 0}, sin};
     for (const Span& in : ins)
         if (overlap(o, in) || (overlap(sout, in) && in.p != state_in) || overlap(snp, in))
             return fail(KDA_ERR_ALIAS, "%s: out/state_out/snapshots overlap an input", name);
@@ -543,7 +543,7 @@ int kda_chunked_backward(const void* q, const void* k, const void* v, const floa
                         {v, tokens * H * d_v * esz},
                         {g, tokens * H * gk * 4},
                         {beta, tokens * H * esz},
-                        {cu_seqlens, (size_t)(N + 1) * 4},
+                        {cu_seqlens, ((size_t)N + 1) * 4},
                         {state_in, state_in ? sbytes : 0},
                         {d_out, tokens * H * d_v * 4},
                         {d_state_out, d_state_out ? sbytes : 0}};

@@ -136,7 +136,7 @@ int kda_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_
     if ((!same(qi, qo) && overlap(qi, qo)) || overlap(qo, ki) || overlap(qo, vi))
         return fail(KDA_ERR_ALIAS, "%s: q_out overlaps an input that it is not", name);
     const Span ins[] = {qi.span(), ki.span(), vi.span(), qo.span(),
-                        {cu_seqlens, cu_seqlens ? (size_t)(N + 1) * 4 : 0}, {start, (size_t)N * 4},
+                        {cu_seqlens, cu_seqlens ? ((size_t)N + 1) * 4 : 0}, {start, (size_t)N * 4},
                         {freqs, (size_t)rotary_dim * 4}, table_span(page_table, table_stride, N, table_pages)};
     for (const Span& in : ins)
         if (overlap(kp.span(), in) || overlap(vp.span(), in))
@@ -222,7 +222,7 @@ int kda_paged_prefill(const void* q, int64_t q_stride, const void* k_pages, cons
     if (int rc = check_groups(name, kda::paged_prefill_groups(a, &need))) return rc;
     if (int rc = check_workspace(name, workspace, workspace_bytes, need)) return rc;
     const Span ins[] = {qi.span(), kp.span(), vp.span(), table_span(page_table, table_stride, N, table_pages),
-                        {lengths, (size_t)N * 4}, {cu_seqlens, (size_t)(N + 1) * 4}};
+                        {lengths, (size_t)N * 4}, {cu_seqlens, ((size_t)N + 1) * 4}};
     const Span outs[] = {{out, (size_t)T_total * H_q * d * es}, {lse, lse ? (size_t)T_total * H_q * 4 : 0},
                          {workspace, need}};
     if (int rc = check_alias(name, outs, ins)) return rc;

@@ -97,7 +97,7 @@ int kda_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_s
         return fail(KDA_ERR_MISALIGNED, "%s: cu_seqlens and start must be 4-byte aligned", name);
     const Span ins[] = {{k, extent(T_total, k_stride * es, row)},
                         {v, extent(T_total, v_stride * es, row)},
-                        {cu_seqlens, cu_seqlens ? (size_t)(N + 1) * 4 : 0},
+                        {cu_seqlens, cu_seqlens ? ((size_t)N + 1) * 4 : 0},
                         {start, (size_t)N * 4},
                         table_span(page_table, table_stride, N, table_pages)};
     for (const Span& in : ins)

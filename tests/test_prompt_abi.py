@@ -344,3 +344,18 @@ def test_workspace_of_paged_prefill_without_a_bound(monkeypatch, N, T, Hq, Hkv, 
                            kp_stride=16 * Hkv * d, vp_stride=16 * Hkv * d, width=width, stride=max(width, 1), window=window,
                            sinks=sinks, max_length=most, ws_bytes=need)
             assert status == _l.KDA_ERR_HIP and b"injected" in L.kda_last_error(), (width, most, L.kda_last_error())
+
+
+def test_segment_ends_of_the_largest_batch_are_kept_apart_from_the_pages(monkeypatch):
+    """2^31 ends are 8 GiB that no output may overlap (the count of them does not fit 32 bits)."""
+    _l, L = _lib()
+    monkeypatch.setenv("KDA_TEST_FAIL_LAUNCH", "1")
+    change = dict(N=(1 << 31) - 1, width=0, stride=0, table=None)
+    assert _call(L, "kda_rotary_append", PLACE, **change) == _l.KDA_ERR_HIP, L.kda_last_error()
+    for where in dict(kp=0, vp=0, q_out=0):
+        assert _call(L, "kda_rotary_append", PLACE, **change, **{where: P[3] + (1 << 32)}) == _l.KDA_ERR_ALIAS, where
+    from test_serving_abi import APPEND
+
+    far = dict(APPEND, cu=P[10], **change)
+    assert _call(L, "kda_cache_append", far) == _l.KDA_ERR_HIP, L.kda_last_error()
+    assert _call(L, "kda_cache_append", far, kp=far["cu"] + (1 << 32)) == _l.KDA_ERR_ALIAS
