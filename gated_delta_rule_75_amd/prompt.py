@@ -30,7 +30,7 @@ def rotary_frequencies(rotary_dim, *, base=10000.0, scaling=None, factor=1.0, or
       "ntk"     base * factor^(rotary_dim / (rotary_dim - 2)): the slowest pair turns 1 / factor as fast
       "smooth"  f / factor where t <= slow, f where t >= fast, linear in t between
       "ramp"    the same ends, linear in i between the pairs that make `fast` and `slow` turns (these rounded
-                down and up)
+                down and up, and kept in 0 .. rotary_dim - 1)
     Any other frequencies may be used as well.  The factor of the rotated channels that such scalings come with
     is the calls' `amplitude`, for instance 0.1 log(factor) + 1."""
     if rotary_dim < 2 or rotary_dim % 2:
@@ -57,7 +57,8 @@ def rotary_frequencies(rotary_dim, *, base=10000.0, scaling=None, factor=1.0, or
             lo, hi = (rotary_dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
                       for turns in (fast, slow))
             lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rotary_dim - 1)
-            keep = 1.0 - (i - lo) / max(hi - lo, 1e-3)
+            # (hi <= 0: no pair makes more than `slow` turns)
+            keep = 1.0 - (i - lo) / max(hi - lo, 1e-3) if hi > 0 else torch.zeros_like(i)
         keep = keep.clamp(0.0, 1.0)
         f = f * (keep + (1.0 - keep) / factor)
     elif scaling not in (None, "ntk"):

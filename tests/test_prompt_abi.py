@@ -359,3 +359,21 @@ def test_segment_ends_of_the_largest_batch_are_kept_apart_from_the_pages(monkeyp
     far = dict(APPEND, cu=P[10], **change)
     assert _call(L, "kda_cache_append", far) == _l.KDA_ERR_HIP, L.kda_last_error()
     assert _call(L, "kda_cache_append", far, kp=far["cu"] + (1 << 32)) == _l.KDA_ERR_ALIAS
+
+
+@pytest.mark.parametrize("original_length", [1, 3, 6, 2 * math.pi, 6.3, 7, 40, 200, 201.1])
+@pytest.mark.parametrize("kind", ["smooth", "ramp"])
+def test_rotary_frequencies_of_short_originals(kind, original_length):
+    """Where not even the fastest pair makes more than `slow` turns, all are slowed by the factor; pairs that make fewer
+    are in any case."""
+    from gated_delta_rule_75_amd import rotary_frequencies as freq
+
+    f = freq(16, device="cpu")
+    g = freq(16, scaling=kind, factor=8.0, original_length=original_length, device="cpu") / f
+    turns = original_length * f / (2 * math.pi)
+    assert bool(((g >= 1 / 8 - 1e-12) & (g <= 1)).all())
+    assert bool(((g * 8 - 1).abs() < 1e-12)[turns < 1 - 1e-9].all())
+    if float(turns[0]) <= 1:
+        assert bool(((g * 8 - 1).abs() < 1e-12).all())
+    if float(turns[0]) > 32:
+        assert float(g[0]) == 1.0
