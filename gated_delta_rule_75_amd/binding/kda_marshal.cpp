@@ -142,6 +142,11 @@ bool output_of(PyObject* o, at::IntArrayRef shape, at::ScalarType type, int dev,
     return true;
 }
 
+// Marks a tensor as modified in place, for autograd (inference tensors have no version).
+void written(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 #define KDA_USUAL(cond) \
     if (!(cond)) Py_RETURN_FALSE
 #define KDA_CALL(status_expr)            \
@@ -488,6 +493,8 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                       T, (int32_t)q->size(1), k ? (int32_t)k->size(1) : 0, (int32_t)d, (int32_t)(2 * freqs->size(0)),
                       layout, (float)PyFloat_AS_DOUBLE(a[5]), a[6] == Py_True, code, qo.data_ptr(), qo.stride(0),
                       k ? ko.data_ptr() : nullptr, k ? ko.stride(0) : 0, stream));
+    written(qo);
+    if (k) written(ko);
     if (k) return pair(std::move(qo), std::move(ko));
     PyObject* x = THPVariable_Wrap(std::move(qo));
     PyObject* r = x ? PyTuple_Pack(2, x, Py_None) : nullptr;
@@ -531,6 +538,9 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                      kp->stride(0), vp->stride(0), (int32_t)kp->size(0), (int32_t)kp->size(2),
                      static_cast<const int32_t*>(table->data_ptr()), table->stride(0), (int32_t)table->size(1),
                      (int32_t)q->size(1), (int32_t)k->size(1), (int32_t)d, code, stream));
+    written(qo);
+    written(*kp);
+    written(*vp);
     return THPVariable_Wrap(std::move(qo));
     END_HANDLE_TH_ERRORS
 }
@@ -580,6 +590,8 @@ PyObject* paged_prefill(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                        ints(*cu), (int32_t)N, T, (int32_t)Hq, (int32_t)kp->size(1), (int32_t)d, code, (float)scale,
                        window, sinks, most, out.data_ptr(), want ? static_cast<float*>(lse.data_ptr()) : nullptr, ws,
                        ws_bytes, stream));
+    written(out);
+    if (want) written(lse);
     return want ? pair(std::move(out), std::move(lse)) : THPVariable_Wrap(std::move(out));
     END_HANDLE_TH_ERRORS
 }
@@ -665,6 +677,7 @@ PyObject* token_logprobs_grad(PyObject*, PyObject* const* a, Py_ssize_t n_args) 
     KDA_CALL(f_logprobs_grad(x->data_ptr(), x->stride(0), static_cast<const int32_t*>(tokens), floats(lse), floats(ent),
                              floats(d_lp), floats(d_lse), floats(d_ent), R, (int32_t)x->size(1), code, out.data_ptr(),
                              out.stride(0), stream));
+    written(out);
     return THPVariable_Wrap(std::move(out));
     END_HANDLE_TH_ERRORS
 }

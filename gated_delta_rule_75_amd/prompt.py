@@ -6,6 +6,11 @@ New tokens are packed ``[T, H, d]`` with ``cu_seqlens`` int32 ``[N + 1]``; pages
 
 As in the package's other calls, this module checks and marshals torch tensors; the work is done by
 the library's HIP kernels on the current stream of the tensors' device.
+
+Autograd records none of the calls: what they return requires no gradient, whatever their inputs do.  In training
+they are the two sides of a ``torch.autograd.Function``: ``rotary`` with its own ``inverse=True`` as the backward,
+``token_logprobs`` with ``token_logprobs_grad``; ``paged_prefill`` has no backward.  Tensors that a call is given to
+write to (outputs, pages) count as modified in place, so that a backward pass that needs their old values fails.
 """
 from __future__ import annotations
 
@@ -17,6 +22,7 @@ from . import _lib, serving
 from .serving import _EMPTY, _F32, _I32, _int32, _lead, _lib_, _row, _run, _run_scratch, _vector
 
 _F64 = torch.float64
+_WRITTEN = torch.autograd.graph.increment_version
 _LAYOUTS = {"half": _lib.KDA_ROTARY_HALVES, "interleaved": _lib.KDA_ROTARY_INTERLEAVED}
 
 
@@ -95,7 +101,8 @@ def rotary(q, k, positions, freqs, *, layout="half", amplitude=1.0, inverse=Fals
     float64 [rotary_dim / 2] (``rotary_frequencies``); channels from rotary_dim on are copied.  layout "half":
     pairs (i, i + rotary_dim / 2); "interleaved": pairs (2 i, 2 i + 1).  The rotated channels are multiplied by
     amplitude.  inverse=True rotates back by the same angles: given the gradients of the outputs, the call
-    returns those of q and k.  q_out, k_out: outputs, which may be q and k themselves.
+    returns those of q and k (autograd does not do so by itself: the outputs require no gradient).  q_out, k_out:
+    outputs, which may be q and k themselves.
 
     Returns (q_out, k_out), k_out None without k."""
     if serving._M is not None:
@@ -124,6 +131,7 @@ def rotary(q, k, positions, freqs, *, layout="half", amplitude=1.0, inverse=Fals
         pk, pko = k.data_ptr(), k_out.data_ptr()
     _run(_lib_().kda_rotary, di, q.data_ptr(), qs, pk, ks, positions.data_ptr(), freqs.data_ptr(), T, Hq, Hk, d, r, lay,
          amplitude, int(bool(inverse)), code, q_out.data_ptr(), qos, pko, kos)
+    _WRITTEN([q_out] if k is None else [q_out, k_out])
     return q_out, k_out
 
 
@@ -133,8 +141,8 @@ def rotary_append(q, k, v, k_pages, v_pages, page_table, start, freqs, *, cu_seq
 
     q [T,H_q,d], k, v [T,H_kv,d]; k_pages, v_pages, page_table, start and cu_seqlens as in cache_append: token i
     of sequence n is at position start[n] + i.  freqs, layout, amplitude as in rotary.
-    Returns q_out [T,H_q,d] (which may be given as q itself).  Rows of q_out that belong to no sequence are not
-    written."""
+    Returns q_out [T,H_q,d] (which may be given as q itself), which requires no gradient.  Rows of q_out that belong
+    to no sequence are not written."""
     if serving._M is not None:
         done = serving._M.rotary_append(q, k, v, k_pages, v_pages, page_table, start, freqs, cu_seqlens, layout,
                                         amplitude, q_out)
@@ -164,6 +172,7 @@ def rotary_append(q, k, v, k_pages, v_pages, page_table, start, freqs, *, cu_seq
     _run(_lib_().kda_rotary_append, di, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu, start.data_ptr(), N,
          T, freqs.data_ptr(), r, lay, amplitude, q_out.data_ptr(), qos, k_pages.data_ptr(), v_pages.data_ptr(), kps,
          vps, n_pages, page_size, page_table.data_ptr(), ts, P, Hq, H, d, code)
+    _WRITTEN([q_out, k_pages, v_pages])
     return q_out
 
 
@@ -177,7 +186,8 @@ def paged_prefill(q, k_pages, v_pages, page_table, lengths, cu_seqlens, *, scale
     of these only the last `window` and the first `sinks`.  scale: 1 / sqrt(d) by default.  max_length: an upper
     bound of lengths that sizes the launch (P * page_size by default); tokens behind it are not visible.
     Returns out [T,H_q,d] in q's dtype; with lse=True (or a tensor for it) (out, lse [T,H_q] float32).  A token
-    that sees none gives 0 and -inf; rows that belong to no sequence are not written."""
+    that sees none gives 0 and -inf; rows that belong to no sequence are not written.  There is no backward: the
+    results require no gradient."""
     if serving._M is not None:
         done = serving._M.paged_prefill(q, k_pages, v_pages, page_table, lengths, cu_seqlens, scale, window, sinks,
                                         max_length, out, lse, workspace)
@@ -226,7 +236,11 @@ def paged_prefill(q, k_pages, v_pages, page_table, lengths, cu_seqlens, *, scale
                  k_pages.data_ptr(), v_pages.data_ptr(), kps, vps, n_pages, page_size, page_table.data_ptr(), ts, P,
                  lengths.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, H, d, code, d ** -0.5 if scale is None else scale,
                  window, sinks, most, out.data_ptr(), pl)
-    return out if lse is None else (out, lse)
+    if lse is None:
+        _WRITTEN(out)
+        return out
+    _WRITTEN([out, lse])
+    return out, lse
 
 
 def _optional(t, name, dtype, shape, di):
@@ -244,7 +258,7 @@ def token_logprobs(logits, tokens, *, top=0, entropy=False, workspace=None):
     ignored (0).  NaN logits count as -inf.
     Returns (logprobs [R], lse [R], entropy [R], top_logprobs [R,top], top_tokens int32 [R,top]), float32 but for
     the last; None for what was not asked for.  The alternatives are in descending order, ties to the lower
-    token; top <= 64."""
+    token; top <= 64.  The results require no gradient: ``token_logprobs_grad`` forms that of the first three."""
     if serving._M is not None:
         done = serving._M.token_logprobs(logits, tokens, top, entropy, workspace)
         if done is not False:
@@ -275,7 +289,8 @@ def token_logprobs_grad(logits, tokens, lse, d_logprobs=None, *, d_lse=None, ent
     p (d_lse - d_logprob - d_entropy (log p + entropy)) + d_logprob at the token.
 
     logits, tokens as given to token_logprobs, lse and entropy float32 [R] as it returned them; d_logprobs, d_lse,
-    d_entropy float32 [R] or None (zero).  out: a tensor [R,V], which may be logits itself."""
+    d_entropy float32 [R] or None (zero).  out: a tensor [R,V], which may be logits itself (they are lost then, also to
+    what autograd has saved of them, which raises in its backward)."""
     if serving._M is not None:
         done = serving._M.token_logprobs_grad(logits, tokens, lse, d_logprobs, d_lse, entropy, d_entropy, out)
         if done is not False:
@@ -302,4 +317,5 @@ def token_logprobs_grad(logits, tokens, lse, d_logprobs=None, *, d_lse=None, ent
             raise ValueError(f"out must have shape {(R, V)}, got {tuple(out.shape)}")
     _run(_lib_().kda_token_logprobs_grad, di, logits.data_ptr(), stride, pt, lse.data_ptr(), *rows, R, V, code,
          out.data_ptr(), os)
+    _WRITTEN(out)
     return out

@@ -476,3 +476,47 @@ def test_sizes_that_32_bits_do_not_hold_are_refused():
         print(f"call {at}: {name}", flush=True)
         with pytest.raises(ValueError, match=f"{name} must be a 32-bit whole number"):
             call()
+
+
+@pytest.mark.parametrize("marshalled", [True, False])
+def test_tensors_that_calls_write_to_count_as_modified(monkeypatch, marshalled):
+    """A value that autograd has saved and a call overwrites makes the backward fail instead of using what is there now;
+    what the calls return requires no gradient; tensors of inference mode are written without a count."""
+    from gated_delta_rule_75_amd import serving
+
+    freqs = kda.rotary_frequencies(64)
+    kda.rotary(queries(1, 1, 64, F32), None, i32([0]), freqs)
+    if not marshalled:
+        monkeypatch.setattr(serving, "_M", None)
+    cache = Cache([40], 1, 64, 16, F32, seed=71)
+    q, k = queries(3, 2, 64, F32), queries(3, 1, 64, F32)
+    pos, cu, start = i32([5, 6, 7]), i32([0, 3]), i32([37])
+    x, tokens = torch.randn(3, 90, generator=gen(1)).to(DEV), i32([1, 2, 3])
+    lse, d = torch.logsumexp(x, 1), torch.ones(3, device=DEV)
+
+    def writes(shape, call):
+        leaf = torch.randn(shape, device=DEV, requires_grad=True)
+        saved = leaf.exp()  # its backward needs its own result
+        call(saved.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.sum().backward()
+
+    writes(q.shape, lambda y: kda.rotary(q, k, pos, freqs, q_out=y))
+    writes(k.shape, lambda y: kda.rotary(q, k, pos, freqs, k_out=y))
+    writes(q.shape, lambda y: kda.rotary(y, None, pos, freqs, q_out=y))
+    writes(q.shape, lambda y: kda.rotary_append(q, k, k, cache.kp, cache.vp, cache.table, start, freqs, cu_seqlens=cu,
+                                                q_out=y))
+    writes(cache.kp.shape, lambda y: kda.rotary_append(q, k, k, y, cache.vp, cache.table, start, freqs, cu_seqlens=cu))
+    writes(cache.vp.shape, lambda y: kda.rotary_append(q, k, k, cache.kp, y, cache.table, start, freqs, cu_seqlens=cu))
+    writes(q.shape, lambda y: kda.paged_prefill(q, cache.kp, cache.vp, cache.table, cache.len, cu, out=y))
+    writes((3, 2), lambda y: kda.paged_prefill(q, cache.kp, cache.vp, cache.table, cache.len, cu, lse=y))
+    writes(x.shape, lambda y: kda.token_logprobs_grad(x, tokens, lse, d, out=y))
+    writes(x.shape, lambda y: kda.token_logprobs_grad(y, tokens, lse, d, out=y))
+    z = q.clone().requires_grad_()
+    for got in (*kda.rotary(z, k, pos, freqs), kda.paged_prefill(z, cache.kp, cache.vp, cache.table, cache.len, cu),
+                kda.token_logprobs(x.clone().requires_grad_(), tokens)[0]):
+        assert not got.requires_grad
+    want = kda.rotary(q, None, pos, freqs)[0]
+    with torch.inference_mode():
+        y = q.clone()
+        assert torch.equal(kda.rotary(y, None, pos, freqs, q_out=y)[0], want)
