@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryPl
     constexpr int W = V::W, NV = MODE == kHalves ? 2 : 1;  // vectors of a thread's step
     constexpr int kUnroll = 4 / NV;
     __shared__ float2 s_turn[kTurns];
-    __shared__ int64_t s_pos[kMaxTokens], s_k[kMaxTokens], s_v[kMaxTokens];
+    __shared__ int64_t s_k[kMaxTokens], s_v[kMaxTokens];
     __shared__ int s_on[kMaxTokens];
     __shared__ __attribute__((aligned(16))) T s_row[MODE == kStaged ? kThreads * W : 8];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -154,7 +154,6 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryPl
             pos = a.positions[t];
         }
         if (lane == 0) {
-            s_pos[j] = pos;
             s_on[j] = on;
             s_k[j] = ko;
             s_v[j] = vo;
