@@ -24,8 +24,8 @@
 //  * A row belongs to one wave where it is short, to a workgroup where it is not, and to several workgroups where
 //    there are few rows; a second launch joins their parts.
 //  * Logits and gradients of more than the 256 MB of the memory's own cache pass the caches by: 4096 rows of 131072 in
-//    bf16, 188 us, 5.7 TB/s (196 without); their gradient 340 us, 6.3 TB/s (373).  Less of them stays there from
-//    the product before: 2048 rows of 50257, 205 MB, 41 us, past the caches 44.
+//    bf16, 184 to 195 us by the card, 5.5 to 5.8 TB/s (8 us more without); their gradient 341 to 344 us, 6.2 TB/s (373).
+//    Less of them stays there from the product before: 2048 rows of 50257, 205 MB, 42 us, past the caches 44.
 #include <math.h>
 
 #include <type_traits>

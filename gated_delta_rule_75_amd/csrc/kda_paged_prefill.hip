@@ -8,8 +8,15 @@
 // both results, so a lane holds values of one query only.  The softmax needs one exchange between the two halves
 // of a wave, and the scores that a lane holds are, rounded, its share of the second product's right operand.
 //
-// Many rows are bound by the matrix cores: 8192 tokens after 24576, 32 heads of 128 over 8, bf16, 3.4 ms, 1130 TFLOP/s
-// (these are busy 64% of the time at the 1.7 GHz that the power then allows; a library's product of 8192^3 reaches 1250).
+// With many rows bf16 weights are rounded once for their product with the values, as its operand is; their sum is of the
+// weights themselves.  Outputs are then off by 0.0022 of their size instead of 0.0017, the rounding of the outputs alone.
+// A second product with what the rounding left, as with few rows, would cost 4.8 ms instead of 3.4 for the long prompt
+// below, 138 us instead of 111 for 8 prompts of 48 to 2048 tokens after 1 to 8000, 336 instead of 238 for 4096 tokens after
+// 4096 with d = 64.
+//
+// Many rows are bound by the matrix cores: 8192 tokens after 24576, 32 heads of 128 over 8, bf16, 3.4 to 3.6 ms by the card,
+// 1060 to 1140 TFLOP/s (these are busy 64% of the time at the 1.7 GHz that the power then allows; a library's product of
+// 8192^3 reaches 1250).  4096 tokens after 4096 with d = 64: 233 to 240 us, 860 to 890 TFLOP/s.
 // fp32 with a window of 1024 and d = 64: 300 us, 94 TFLOP/s of visible pairs (busy 77%, of 154 that fp32 products reach).
 // Few rows are bound by HBM: 64 sequences of 8192 tokens with 5 new ones each, 374 us, 5.8 TB/s (fp32 5.8).  Short calls
 // are bound by latency: 64 tokens alone 12 us, in a chain of segment, length, page and keys.
@@ -100,7 +107,7 @@ struct Shape {
     static constexpr int TILE = BN * ROW;                    // bytes of a tile's keys
     static constexpr int BUFS = ROWS ? 2 : WAVES;            // tiles in LDS
     // waves that share a SIMD's registers (bf16, d = 256: with two, 100 registers spill, and their loads wait for the next
-    // tile's; 8192 tokens after 8192, 16 heads over 4, 1.53 ms, with two 1.66)
+    // tile's; 8192 tokens after 8192, 16 heads over 4, 1.53 to 1.58 ms, with two 1.66)
     static constexpr int PER_SIMD = ROW <= (ROWS && ES == 4 ? 512 : 256) ? 2 : 1;
 };
 
@@ -933,7 +940,7 @@ __global__ __launch_bounds__((Shape<T, D, ROWS>::THREADS), (Shape<T, D, ROWS>::P
     if constexpr (ROWS) {
         // A lane's outputs are four channels of its row at a time: stored like that, every request would carry 16 bytes of
         // a row.  They go through LDS (each wave has a quarter of it), where 16 bytes are at piece ^ row of theirs.  (7
-        // sequences of 2048 tokens, 40 heads of 128 over 8, window 19: 149 us, 164 straight from the registers.)
+        // sequences of 2048 tokens, 40 heads of 128 over 8, window 19: 139 to 149 us, 164 straight from the registers.)
         __syncthreads();  // the tiles have been read
         if (!active) return;
         auto store = [&](auto type, float f, auto row_of) {  // outputs times f, as `type`, row r of the wave to row_of(r)
@@ -1087,7 +1094,9 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(PagedPrefillArgs a, P
 
 int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
-// Few rows for each sequence: the waves share the rows and split the keys.
+// Few rows for each sequence, on average (the host knows no more): the waves share the rows and split the keys.  A prompt
+// next to single tokens makes them many, and the others' row tiles mostly empty: 2048 tokens next to 4 single ones after
+// 65536 take 1.07 ms, next to 31 after 10000 240 us, alone 54.
 bool many_rows(const PagedPrefillArgs& a) { return a.T * (a.Hq / a.Hkv) > 32 * a.N; }
 
 // A variant's sizes, as in Shape.

@@ -11,9 +11,10 @@
 //    multiples of 2 pi there (a position of 2^17 in fp32 would be off by 2^-7 rad), the rest is fp32.
 //  * The first values are asked for before the angles are formed, so that these hide behind the loads.  Many small
 //    workgroups keep the chip's loads and stores apart in time better than few large ones, and neither is kept in the
-//    caches (non-temporal).  65536 tokens of 32 + 32 heads of 128, bf16: 361 us, 5.9 TB/s (16 tokens a workgroup: 438, 8:
-//    417, 4: 402, without the hint for stores 382; a copy of that size: 420).  Into pages, 16384 tokens of segments: 199
-//    us, 6.0 TB/s, where the hint for stores saves 24 us and the attention behind it takes as long as before.
+//    caches (non-temporal).  65536 tokens of 32 + 32 heads of 128, bf16: 361 to 375 us by the card, 5.7 to 5.9 TB/s (on
+//    the faster one 16 tokens a workgroup: 438, 8: 417, 4: 402, without the hint for stores 382; a copy of that size: 420).
+//    Into pages, segments of 1K to 16K tokens, 8 in all: 196 to 200 us, 6.0 TB/s, where the hint for stores saves 24 us and
+//    the attention behind it takes as long as before.
 //  * A thread always has the same place in a row.  Halves that start at 16-byte boundaries: a vector of the first
 //    half and its partner.  Interleaved: pairs lie inside one vector.  Halves that do not (r / 2 no multiple of a
 //    vector): the rows of a step are laid into LDS, from where each thread takes its partners (5.9 TB/s too).

@@ -616,10 +616,12 @@ int kda_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_
  * makes what it enters not finite, but for a key with a score of -inf, which has weight 0.  Products are exact in
  * bf16 with fp32 sums.  With KDA_BF16 and T_total * H_q / H_kv > 32 N (many new tokens) the softmax weights are rounded
  * to bf16 for their product with the values (their sum is not), which adds to the output's own rounding about as much
- * again; with fewer they are two bf16 each.
+ * again; with fewer they are two bf16 each.  This goes by the batch: a single token or a draft has two alone or with
+ * others of its kind, and one next to a prompt that brings the average above 32.
  * workspace: kda_paged_prefill_workspace bytes for the same arguments, 256-byte aligned, overlapping no argument; holds
  * the partial results where the keys of some rows are split over several workgroups.  Needs no initialisation.  How they
  * are split goes by the lengths of all sequences, so that a sequence's last bits may depend on the others' lengths.
+ * T_total * H_q / 32 + N * H_kv is below 2^24.
  * d in {64, 128, 256}; lengths and cu_seqlens are a caller contract (checked with KDA_DEBUG_CHECK=1).
  */
 int kda_paged_prefill(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int64_t k_page_stride,
@@ -649,7 +651,7 @@ size_t kda_paged_prefill_workspace(int32_t N, int64_t T_total, int32_t H_q, int3
  *   top_logprobs, top_tokens float, int32 [R, top]; NULL with top = 0
  * A row whose log-sum is not finite (all -inf, or a logit of +inf) has entropy 0, and a log-probability that is NaN
  * there counts as -inf.
- * V < 2^24, 0 <= top <= 64, top <= V.
+ * V < 2^24, 0 <= top <= 64, top <= V, R < 2^24 (a workgroup is counted for every row, also where four share one).
  * workspace: kda_token_logprobs_workspace bytes, 256-byte aligned, overlapping no argument; needs no
  * initialisation.
  */
