@@ -45,8 +45,6 @@ struct SelectPlan {
     int per_part;  // tokens of a part, a multiple of kRound
 };
 
-__host__ __device__ inline int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
-
 inline SelectPlan select_plan(int64_t rows, int V) {
     // about eight workgroups per CU, and at least one round each; rounds begin at 16-byte boundaries,
     // up to 7 tokens before the row

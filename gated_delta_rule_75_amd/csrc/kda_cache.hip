@@ -752,8 +752,6 @@ hipError_t timed_launch(int id, hipStream_t s, F launch) {
     return e;
 }
 
-int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
-
 }  // namespace
 
 static int append_tokens(int64_t T_total, int vpt) {

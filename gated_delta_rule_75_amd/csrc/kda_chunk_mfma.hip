@@ -132,7 +132,6 @@ __device__ __forceinline__ float bf(uint16_t b) { return bf16_to_f32(b); }
 // The prep kernel keeps log-decays in base-2 units (G * log2(e)), so that every decay factor is
 // one hardware exp2 with no scaling multiply.
 constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 // the diagonal-tile factors leave the fp16 range beyond e^10 = 2^(10 log2 e)
 constexpr float kDiagBound2 = 10.f * kLog2e;
 

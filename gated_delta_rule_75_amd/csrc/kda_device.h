@@ -48,7 +48,15 @@ __device__ __forceinline__ float ld_buf<uint16_t>(__amdgpu_buffer_rsrc_t r, int 
     return bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, i * 2, 0, 0));
 }
 
-// exp(x) through the hardware base-2 exponential (v_exp_f32).
+// Two values rounded to bfloat16 (nearest even), the first in the lower half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 y = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, y);
+}
+
+// 2^x by the hardware (v_exp_f32), and exp(x) through it.
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float fast_exp(float x) {
     return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
 }

@@ -7,6 +7,8 @@
 
 namespace kda {
 
+__host__ __device__ inline int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
+
 // Per-kernel event timing (diagnostics).  When timing is on for the calling
 // thread, launchers bracket each kernel with timed_begin/timed_end.
 enum KernelId {

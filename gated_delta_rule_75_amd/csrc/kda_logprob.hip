@@ -50,8 +50,6 @@ using Bits = std::integral_constant<int, N>;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453;
 
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-
 // 16 bytes; PASS: the caches are left to others
 template <bool PASS>
 __device__ __forceinline__ u32x4 load_16(const void* at) {
@@ -586,9 +584,7 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
                 if constexpr (sizeof(T) == 4) {
                     out[i] = __float_as_uint(g[i]);
                 } else {
-                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-                    const bf16x2 y = {(__bf16)g[2 * i], (__bf16)g[2 * i + 1]};
-                    out[i] = __builtin_bit_cast(uint32_t, y);
+                    out[i] = pack_bf16(g[2 * i], g[2 * i + 1]);
                 }
             }
             if constexpr (PASS) __builtin_nontemporal_store(out, reinterpret_cast<u32x4*>(y0 + c0));
@@ -605,8 +601,6 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
         }
     }
 }
-
-int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 // Whether so many bytes pass the caches by.
 bool pass_by(int64_t bytes) { return bytes > (int64_t)256 << 20; }

@@ -57,8 +57,6 @@ constexpr int kTile = 16;          // tokens
 constexpr int kMaxPartTiles = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-
 // Visible tiles of a sequence: sink tiles 0 .. head_tiles-1, then the tiles from near / 16 on.
 struct Visible {
     int head, near, len;  // tokens 0 .. head-1 and near .. len-1 are visible, head <= near
@@ -122,12 +120,7 @@ __device__ __forceinline__ floatx4 mfma_bf16(u32x4 a, u32x4 b, floatx4 c) {
                                                    0, 0);
 }
 
-// two fp32 weights to packed bf16 (nearest even), and what is left of them
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const bf16x2 y = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, y);
-}
+// the values of a packed pair
 __device__ __forceinline__ float low_of(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float high_of(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
@@ -503,8 +496,6 @@ __global__ __launch_bounds__(kThreads) void paged_join_kernel(PagedDecodeArgs a,
     a.o[row * D + threadIdx.x] = L == 0.f ? 0.f : x / L;
     if (a.lse && threadIdx.x == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
-
-int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 // 32 query heads a workgroup where a key-value head has more than 16 (fp32 and D = 256 have no
 // registers for that)

@@ -37,7 +37,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // 16 bytes per lane from a buffer to LDS: lane i's go to at + 16 i; those behind the descriptor's end become 0.  Written
@@ -65,11 +64,6 @@ __device__ __forceinline__ void wait_loads_but() {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kPage = 16;  // tokens that surely share a page
 
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const bf16x2 y = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, y);
-}
 // the larger of lane and lane ^ 32
 __device__ __forceinline__ float other_half_max(float x) {
     const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -1091,8 +1085,6 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(PagedPrefillArgs a, P
         if (c == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
     }
 }
-
-int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 // Few rows for each sequence, on average (the host knows no more): the waves share the rows and split the keys.  A prompt
 // next to single tokens makes them many, and the others' row tiles mostly empty: 2048 tokens next to 4 single ones after

@@ -33,12 +33,7 @@ constexpr int kTurns = 2048;  // angles of a workgroup at most
 
 enum Mode { kHalves, kInterleaved, kStaged };
 
-// bf16 pair to the values, and rounded back (nearest even)
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const bf16x2 y = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, y);
-}
+// 16 bytes to their values, and rounded back (bf16: nearest even)
 template <typename T>
 struct Vec {
     static constexpr int W = 16 / sizeof(T);
