@@ -7,8 +7,8 @@ New tokens are packed ``[T, H, d]`` with ``cu_seqlens`` int32 ``[N + 1]``; pages
 As in the package's other calls, this module checks and marshals torch tensors; the work is done by
 the library's HIP kernels on the current stream of the tensors' device.
 
-Autograd records none of the calls: what they return requires no gradient, whatever their inputs do.  In training
-they are the two sides of a ``torch.autograd.Function``: ``rotary`` with its own ``inverse=True`` as the backward,
+Autograd records none of the calls: what they return requires no gradient, whatever their inputs do (an output that
+is given is returned as it is).  In training they are the two sides of a ``torch.autograd.Function``: ``rotary`` with its own ``inverse=True`` as the backward,
 ``token_logprobs`` with ``token_logprobs_grad``; ``paged_prefill`` has no backward.  Tensors that a call is given to
 write to (outputs, pages) count as modified in place, so that a backward pass that needs their old values fails.
 """
